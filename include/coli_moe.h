@@ -232,6 +232,123 @@ coli_status coli_moe_layer_noalloc(const coli_moe_config *cfg, const coli_moe_we
  * stream capture). */
 coli_status coli_moe_noalloc_error_word(void *stream, int *code);
 
+/* ---------------------------------------------------------------- router scores ------------
+ * a2 in its general form: softmax or sigmoid scores, with or without a selection bias, with
+ * masked experts, for routers other than the noaux_tc one of coli_moe_route. */
+typedef enum { COLI_SCORE_SIGMOID = 0, COLI_SCORE_SOFTMAX = 1 } coli_score;
+typedef enum { COLI_GROUP_TOP2 = 0, COLI_GROUP_MAX = 1 } coli_group_score;
+
+typedef struct {
+    int n_experts;      /* E (<= 1024) */
+    int top_k;          /* K (<= 32), at most topk_group * E / n_group */
+    int n_group;        /* G (<= 32); E % G == 0 */
+    int topk_group;     /* TG, 1 <= TG <= G */
+    int score;          /* coli_score */
+    int group_score;    /* coli_group_score: what ranks the groups when TG < G */
+    int renorm;         /* 1: the chosen scores are divided by their sum; 0: taken as they are */
+    int logits;         /* coli_act: type of the logits */
+    double scaling;     /* factor of the weights, > 0 */
+} coli_moe_router;
+
+/* Validates a router description (the checks of coli_moe_route_scores).  Host only. */
+coli_status coli_moe_check_router(const coli_moe_router *r);
+
+/* Routing of T tokens from their logits (row t at logits + t * ld elements, ld >= n_experts; 0:
+ * n_experts), an optional selection bias[E] (NULL: none) to topk_ids[T][K] and topk_w[T][K].
+ *   s = 1/(1+exp(-l)), or the softmax of the row; c = s + bias.  Without a bias the experts are
+ *   ranked by l itself (s grows with it).
+ *   An expert can be chosen when l and c are neither NaN nor -inf: a logit of -inf (or NaN)
+ *   masks an expert of a token, a bias of -inf masks it for all tokens.  NaN logits and logits
+ *   of -inf take no part in the softmax; logits of +inf share it equally.
+ *   TG < G: each group is ranked by the largest c (l without a bias) of the experts that can be
+ *   chosen (COLI_GROUP_MAX), or the sum of the two largest c, s without a bias, or of the only
+ *   one (COLI_GROUP_TOP2); the TG best are kept, ties going to the lower group, groups without an
+ *   expert that can be chosen last.
+ *   The K best of the kept groups in descending order, ties to the lower id, with weights
+ *   s / sum(chosen s) * scaling (renorm; 0 where that sum is 0) or s * scaling.  Where fewer than
+ *   K can be chosen the row is filled up with the lowest other ids, in ascending order, with
+ *   weight 0: every row holds K different ids, so it can be grouped and multiplied as it is.
+ * Biased scores are compared in double, logits exactly; weights carry float32 sums.
+ * T = 0 is a no-op.  Asynchronous on `stream`; one kernel; may be captured. */
+coli_status coli_moe_route_scores(const coli_moe_router *r, const void *logits, size_t ld,
+                                  const float *bias, int T, int32_t *topk_ids, float *topk_w,
+                                  void *stream);
+
+/* ---------------------------------------------------------------- microscaled 4-bit --------
+ * Rows of e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; element 2j in the low
+ * nibble of byte j) with one scale per block of consecutive elements of a row.
+ *   COLI_FP4_MX  blocks of 32, scale 2^(byte - 127) (e8m0)
+ *   COLI_FP4_NV  blocks of 16, scale e4m3 (not negative)
+ * A value is code * block scale * row scale, the row scale a float32 per row (NULL: 1).
+ * k is a multiple of 32.  A row's block scales take coli_moe_fp4_scale_pitch bytes: whole runs of
+ * 256 elements, the bytes behind the last block zero.  Two layouts of the scales:
+ *   COLI_FP4_ROWS   [rows][pitch], for activations
+ *   COLI_FP4_TILES  for weight matrices: tiles of 128 rows x 4 scales, 512 bytes each, the tiles
+ *                   of 128 rows one after another: scale j of row r at byte
+ *                   (r / 128) * 128 * pitch + (j / 4) * 512 + (r % 32) * 16 + (r % 128) / 32 * 4 + j % 4;
+ *                   rows behind the last one zero. */
+typedef enum { COLI_FP4_MX = 0, COLI_FP4_NV = 1 } coli_fp4;
+typedef enum { COLI_FP4_ROWS = 0, COLI_FP4_TILES = 1 } coli_fp4_layout;
+
+/* Bytes of one row of block scales, and of a whole array of them.  Host only. */
+coli_status coli_moe_fp4_scale_pitch(int fmt, int k, size_t *bytes);
+coli_status coli_moe_fp4_scale_bytes(int fmt, int layout, int rows, int k, size_t *bytes);
+
+/* Quantises `rows` rows of k values.  Row r is read from source row r (row_index NULL; rows ==
+ * src_rows) or row_index[r] / row_div (device int32; a slot's token with row_div = top_k), source
+ * row i at x + i * ldx elements (act: coli_act).
+ *   NV: row scale 2^(floor(log2(largest |x| of the row)) - 10) (1 for a row of zeros), block scale
+ *       the e4m3 nearest to (largest |x| of the block) / (6 * row scale);
+ *   MX: block scale 2^(floor(log2(largest |x| of the block)) - 2), at least 2^-127; row scale 1;
+ *   code: the e2m1 nearest to x / (block scale * row scale), ties to the even code, at most 6.
+ * Both are exact: the quotients are those of the real numbers.  A block that holds a NaN or an
+ * infinity gets the scale NaN (0x7F, 0xFF) and codes 0, and does not count for the row scale.
+ * codes [rows][k/2] (8-byte aligned), scales in `layout` (4-byte aligned), row_scale [rows].  An
+ * index outside [0, src_rows) writes a row of zeros and sets COLI_DEVERR_GROUPING in the error
+ * word of `ws` (256-byte aligned, its header cleared once, as for the layer).
+ * x 16-byte aligned, ldx a multiple of 16 bytes.  rows = 0 is a no-op.  One kernel. */
+coli_status coli_moe_fp4_quantize(int fmt, int layout, int act, const void *x, int src_rows,
+                                  size_t ldx, const int32_t *row_index, int row_div, int rows,
+                                  int k, uint8_t *codes, uint8_t *scales, float *row_scale,
+                                  void *ws, void *stream);
+
+/* The values that codes and scales stand for, rounded once to `act`: out row r at out + r * ldo
+ * elements (16-byte aligned, ldo a multiple of 16 bytes).  row_scale NULL: 1.  One kernel. */
+coli_status coli_moe_fp4_dequantize(int fmt, int layout, const uint8_t *codes,
+                                    const uint8_t *scales, const float *row_scale, int rows,
+                                    int k, int act, void *out, size_t ldo, void *stream);
+
+typedef struct {
+    const uint8_t *codes;    /* [rows][k/2], 16-byte aligned */
+    const uint8_t *scales;   /* COLI_FP4_ROWS, 16-byte aligned */
+    const float *row_scale;  /* [rows], or NULL */
+    int rows;
+} coli_fp4_rows;
+
+typedef struct {
+    const uint8_t *codes;    /* `count` matrices [n][k/2], 16-byte aligned */
+    const uint8_t *scales;   /* `count` arrays in COLI_FP4_TILES, 16-byte aligned */
+    const float *row_scale;  /* `count` arrays [n], or NULL */
+    int count, n;            /* count <= 1024 */
+    size_t codes_stride;     /* bytes between matrices; a multiple of 16 */
+    size_t scales_stride;    /* bytes; a multiple of 16 */
+    size_t row_scale_stride; /* elements */
+} coli_fp4_mats;
+
+/* out[i][j] = sum_k a[i][k] * w[j][k] for every row i of `a`, w the matrix of the row's group:
+ * rows offsets[e] .. offsets[e+1] - 1 belong to matrix e (device int32 [count + 1], ascending, as
+ * coli_moe_group writes them); offsets NULL: one matrix (count == 1) for all rows.  Rows outside
+ * every group keep what `out` held.  Groups that are not ascending within [0, rows] are left out
+ * and set COLI_DEVERR_GROUPING in the error word of `ws`.
+ * Products on the tensor cores, block scales applied there, float32 sums; the row scales are
+ * applied to the sum, which is rounded once to out_type (coli_act).  No atomics: the same call
+ * gives the same bits.
+ * out: row i at out + i * ldo elements, ldo >= n, aligned to its elements.  rows = 0 is a no-op.
+ * One kernel; allocates nothing; may be captured. */
+coli_status coli_moe_fp4_product(int fmt, const coli_fp4_rows *a, const coli_fp4_mats *w, int k,
+                                 const int32_t *offsets, int out_type, void *out, size_t ldo,
+                                 void *ws, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,6 +22,11 @@ __all__ = [
     "coli_moe_set_dispatch_threshold",
     "coli_moe_dispatch_threshold",
     "config_for", "weights_for",
+    "MoERouter", "coli_moe_check_router", "coli_moe_route_scores",
+    "FP4Rows", "FP4Mats", "coli_moe_fp4_scale_pitch", "coli_moe_fp4_scale_bytes", "coli_moe_fp4_quantize",
+    "coli_moe_fp4_dequantize", "coli_moe_fp4_product", "fp4_rows_for", "fp4_mats_for",
+    "COLI_SCORE_SIGMOID", "COLI_SCORE_SOFTMAX", "COLI_GROUP_TOP2", "COLI_GROUP_MAX",
+    "COLI_FP4_MX", "COLI_FP4_NV", "COLI_FP4_ROWS", "COLI_FP4_TILES",
     "COLI_W_INT2", "COLI_W_INT4", "COLI_W_INT8", "COLI_ACT_F32", "COLI_ACT_BF16",
 ]
 
@@ -29,6 +34,10 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libcoli_moe
 
 COLI_W_INT2, COLI_W_INT4, COLI_W_INT8 = 2, 4, 8
 COLI_ACT_F32, COLI_ACT_BF16 = 0, 1
+COLI_SCORE_SIGMOID, COLI_SCORE_SOFTMAX = 0, 1
+COLI_GROUP_TOP2, COLI_GROUP_MAX = 0, 1
+COLI_FP4_MX, COLI_FP4_NV = 0, 1
+COLI_FP4_ROWS, COLI_FP4_TILES = 0, 1
 DEVERR_EXPERT_ID, DEVERR_GROUPING, DEVERR_TIMEOUT = 0x1, 0x2, 0x4
 
 if not os.path.exists(LIB_PATH):
@@ -50,6 +59,26 @@ class MoEWeights(C.Structure):
     _fields_ = [
         ("router_w", C.c_void_p), ("router_bias", C.c_void_p), ("experts", C.c_void_p),
         ("expert_stride", C.c_size_t), ("shared", C.c_void_p),
+    ]
+
+
+class MoERouter(C.Structure):
+    """coli_moe_router: the description of a router from scores (coli_moe_route_scores)."""
+    _fields_ = [
+        ("n_experts", C.c_int), ("top_k", C.c_int), ("n_group", C.c_int), ("topk_group", C.c_int),
+        ("score", C.c_int), ("group_score", C.c_int), ("renorm", C.c_int), ("logits", C.c_int),
+        ("scaling", C.c_double),
+    ]
+
+
+class FP4Rows(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("row_scale", C.c_void_p), ("rows", C.c_int)]
+
+
+class FP4Mats(C.Structure):
+    _fields_ = [
+        ("codes", C.c_void_p), ("scales", C.c_void_p), ("row_scale", C.c_void_p), ("count", C.c_int), ("n", C.c_int),
+        ("codes_stride", C.c_size_t), ("scales_stride", C.c_size_t), ("row_scale_stride", C.c_size_t),
     ]
 
 
@@ -88,13 +117,22 @@ def _load():
     L.coli_moe_set_dispatch_threshold.argtypes = [I]
     L.coli_moe_dispatch_threshold.argtypes = []
     L.coli_moe_dispatch_threshold.restype = I
+    L.coli_moe_check_router.argtypes = [C.POINTER(MoERouter)]
+    L.coli_moe_route_scores.argtypes = [C.POINTER(MoERouter), P, S, P, I, P, P, P]
+    L.coli_moe_fp4_scale_pitch.argtypes = [I, I, C.POINTER(S)]
+    L.coli_moe_fp4_scale_bytes.argtypes = [I, I, I, I, C.POINTER(S)]
+    L.coli_moe_fp4_quantize.argtypes = [I, I, I, P, I, S, P, I, I, I, P, P, P, P, P]
+    L.coli_moe_fp4_dequantize.argtypes = [I, I, P, P, P, I, I, I, P, S, P]
+    L.coli_moe_fp4_product.argtypes = [I, C.POINTER(FP4Rows), C.POINTER(FP4Mats), I, P, I, P, S, P, P]
     L.coli_moe_layer_kernels.restype = I
     L.coli_moe_layer_noalloc.restype = I
     for name in ("coli_moe_record_bytes", "coli_moe_check_config", "coli_moe_workspace_size",
                  "coli_moe_clear_error", "coli_moe_error_word", "coli_moe_gate",
                  "coli_moe_route", "coli_moe_group", "coli_moe_ffn", "coli_moe_layer",
                  "coli_moe_residual", "coli_moe_debug_set_wait", "coli_moe_set_dispatch_threshold",
-                 "coli_moe_noalloc_error_word"):
+                 "coli_moe_noalloc_error_word", "coli_moe_check_router", "coli_moe_route_scores",
+                 "coli_moe_fp4_scale_pitch", "coli_moe_fp4_scale_bytes", "coli_moe_fp4_quantize",
+                 "coli_moe_fp4_dequantize", "coli_moe_fp4_product"):
         getattr(L, name).restype = I
     return L
 
@@ -257,3 +295,58 @@ def weights_for(router_w, router_bias, experts, shared=None) -> MoEWeights:
     """MoEWeights over device tensors: experts is [E, stride] uint8, shared [stride_s] uint8."""
     return MoEWeights(_p(router_w), _p(router_bias), _p(experts), experts.stride(0),
                       _p(shared))
+
+
+def coli_moe_check_router(router: MoERouter) -> None:
+    _check("coli_moe_check_router", lib.coli_moe_check_router(C.byref(router)))
+
+
+def coli_moe_route_scores(router: MoERouter, logits, ld, bias, T, topk_ids, topk_w, stream=None) -> None:
+    """Softmax or sigmoid routing of T tokens: row t of the logits at element t * ld (0: n_experts),
+    bias [E] float32 or None."""
+    _check("coli_moe_route_scores", lib.coli_moe_route_scores(
+        C.byref(router), _p(logits), ld, _p(bias), T, _p(topk_ids), _p(topk_w), _stream(stream)))
+
+
+def coli_moe_fp4_scale_pitch(fmt: int, k: int) -> int:
+    n = C.c_size_t()
+    _check("coli_moe_fp4_scale_pitch", lib.coli_moe_fp4_scale_pitch(fmt, k, C.byref(n)))
+    return n.value
+
+
+def coli_moe_fp4_scale_bytes(fmt: int, layout: int, rows: int, k: int) -> int:
+    n = C.c_size_t()
+    _check("coli_moe_fp4_scale_bytes", lib.coli_moe_fp4_scale_bytes(fmt, layout, rows, k, C.byref(n)))
+    return n.value
+
+
+def coli_moe_fp4_quantize(fmt, layout, act, x, src_rows, ldx, row_index, row_div, rows, k, codes, scales, row_scale, ws,
+                          stream=None) -> None:
+    """Rows of x (row i at element i * ldx) to 4-bit codes, block scales and row scales; row r of the
+    result is source row r, or row_index[r] // row_div."""
+    _check("coli_moe_fp4_quantize", lib.coli_moe_fp4_quantize(
+        fmt, layout, act, _p(x), src_rows, ldx, _p(row_index), row_div, rows, k, _p(codes), _p(scales), _p(row_scale),
+        _p(ws), _stream(stream)))
+
+
+def coli_moe_fp4_dequantize(fmt, layout, codes, scales, row_scale, rows, k, act, out, ldo, stream=None) -> None:
+    _check("coli_moe_fp4_dequantize", lib.coli_moe_fp4_dequantize(
+        fmt, layout, _p(codes), _p(scales), _p(row_scale), rows, k, act, _p(out), ldo, _stream(stream)))
+
+
+def coli_moe_fp4_product(fmt, a: FP4Rows, w: FP4Mats, k, offsets, out_type, out, ldo, ws, stream=None) -> None:
+    """out row i = a's row i times the matrix of its group (offsets [count + 1] int32; None: one matrix)."""
+    _check("coli_moe_fp4_product", lib.coli_moe_fp4_product(
+        fmt, C.byref(a), C.byref(w), k, _p(offsets), out_type, _p(out), ldo, _p(ws), _stream(stream)))
+
+
+def fp4_rows_for(codes, scales, row_scale=None) -> FP4Rows:
+    """FP4Rows over device tensors: codes [rows, k/2] uint8, scales [rows, pitch] uint8, row_scale [rows]."""
+    return FP4Rows(_p(codes), _p(scales), _p(row_scale), codes.shape[0])
+
+
+def fp4_mats_for(codes, scales, row_scale=None) -> FP4Mats:
+    """FP4Mats over device tensors: codes [count, n, k/2] uint8, scales [count, bytes] uint8 in tiles,
+    row_scale [count, n]."""
+    return FP4Mats(_p(codes), _p(scales), _p(row_scale), codes.shape[0], codes.shape[1], codes.stride(0), scales.stride(0),
+                   0 if row_scale is None else row_scale.stride(0))

@@ -7,6 +7,7 @@
 #include <string.h>
 
 #include "coli_moe.h"
+#include "fp4.h"
 #include "internal.h"
 #include "residual.h"
 
@@ -431,6 +432,143 @@ coli_status coli_moe_layer(const coli_moe_config *c, const coli_moe_weights *w, 
     if (e == cudaSuccess) e = launch_group(*c, ids, T, counts, offsets, perm, uniq, nu, err, st);
     if (e != cudaSuccess) return from_cuda(e);
     return run_ffn(c, p, base, st);
+}
+
+// ---------------------------------------------------------------- router scores ------------
+
+coli_status coli_moe_check_router(const coli_moe_router *r) {
+    if (!r) return COLI_ERR_INVALID_ARG;
+    if (r->score != COLI_SCORE_SIGMOID && r->score != COLI_SCORE_SOFTMAX) return COLI_ERR_INVALID_ARG;
+    if (r->group_score != COLI_GROUP_TOP2 && r->group_score != COLI_GROUP_MAX) return COLI_ERR_INVALID_ARG;
+    if (r->renorm != 0 && r->renorm != 1) return COLI_ERR_INVALID_ARG;
+    if (r->logits != COLI_ACT_F32 && r->logits != COLI_ACT_BF16) return COLI_ERR_INVALID_ARG;
+    if (!(r->scaling > 0.0)) return COLI_ERR_INVALID_ARG;
+    if (r->n_experts <= 0 || r->top_k <= 0 || r->n_group <= 0 || r->topk_group <= 0) return COLI_ERR_SHAPE;
+    if (r->n_experts % r->n_group || r->topk_group > r->n_group) return COLI_ERR_SHAPE;
+    if (r->top_k > r->topk_group * (r->n_experts / r->n_group)) return COLI_ERR_SHAPE;
+    if (r->n_experts > 1024 || r->top_k > 32 || r->n_group > 32) return COLI_ERR_UNSUPPORTED;
+    return COLI_OK;
+}
+
+coli_status coli_moe_route_scores(const coli_moe_router *r, const void *logits, size_t ld, const float *bias, int T,
+                                  int32_t *topk_ids, float *topk_w, void *stream) {
+    coli_status s = coli_moe_check_router(r);
+    if (s != COLI_OK) return s;
+    if (T < 0) return COLI_ERR_SHAPE;
+    if (ld == 0) ld = static_cast<size_t>(r->n_experts);
+    if (ld < static_cast<size_t>(r->n_experts)) return COLI_ERR_SHAPE;
+    if (T == 0) return COLI_OK;
+    if (!logits || !topk_ids || !topk_w) return COLI_ERR_INVALID_ARG;
+    if (!aligned(logits, r->logits == COLI_ACT_F32 ? 4 : 2) || (bias && !aligned(bias, 4)) || !aligned(topk_ids, 4) || !aligned(topk_w, 4))
+        return COLI_ERR_ALIGN;
+    return from_cuda(launch_route_scores(*r, logits, ld, bias, T, topk_ids, topk_w, static_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------- microscaled 4-bit --------
+
+static coli_status fp4_shape(int fmt, int rows, int k) {
+    if (fmt != COLI_FP4_MX && fmt != COLI_FP4_NV) return COLI_ERR_INVALID_ARG;
+    if (rows < 0 || k <= 0 || k % 32) return COLI_ERR_SHAPE;
+    if (rows > (1 << 30) || k > (1 << 20)) return COLI_ERR_UNSUPPORTED;
+    return COLI_OK;
+}
+
+coli_status coli_moe_fp4_scale_pitch(int fmt, int k, size_t *bytes) {
+    if (!bytes) return COLI_ERR_INVALID_ARG;
+    const coli_status s = fp4_shape(fmt, 0, k);
+    if (s == COLI_OK) *bytes = fp4_pitch(fmt, k);
+    return s;
+}
+
+coli_status coli_moe_fp4_scale_bytes(int fmt, int layout, int rows, int k, size_t *bytes) {
+    if (!bytes || (layout != COLI_FP4_ROWS && layout != COLI_FP4_TILES)) return COLI_ERR_INVALID_ARG;
+    const coli_status s = fp4_shape(fmt, rows, k);
+    if (s == COLI_OK) *bytes = fp4_scale_bytes(fmt, layout, rows, k);
+    return s;
+}
+
+coli_status coli_moe_fp4_quantize(int fmt, int layout, int act, const void *x, int src_rows, size_t ldx,
+                                  const int32_t *row_index, int row_div, int rows, int k, uint8_t *codes,
+                                  uint8_t *scales, float *row_scale, void *ws, void *stream) {
+    if (layout != COLI_FP4_ROWS && layout != COLI_FP4_TILES) return COLI_ERR_INVALID_ARG;
+    if (act != COLI_ACT_F32 && act != COLI_ACT_BF16) return COLI_ERR_INVALID_ARG;
+    coli_status s = fp4_shape(fmt, rows, k);
+    if (s != COLI_OK) return s;
+    if (src_rows < 0 || ldx < static_cast<size_t>(k) || row_div < 1) return COLI_ERR_SHAPE;
+    if (!row_index && (rows != src_rows || row_div != 1)) return COLI_ERR_SHAPE;
+    if (rows == 0) return COLI_OK;
+    if (!x || !codes || !scales || !row_scale) return COLI_ERR_INVALID_ARG;
+    const size_t item = act == COLI_ACT_F32 ? 4 : 2;
+    if (!aligned(x, 16) || ldx * item % 16 || !aligned(codes, 8) || !aligned(scales, 4) || !aligned(row_scale, 4) ||
+        (row_index && !aligned(row_index, 4)))
+        return COLI_ERR_ALIGN;
+    if (!ws || !aligned(ws, 256)) return COLI_ERR_WORKSPACE;
+    Fp4QuantArgs a;
+    a.x = x;
+    a.src_rows = src_rows;
+    a.ldx = ldx;
+    a.row_index = row_index;
+    a.n_index = rows;
+    a.row_div = row_div;
+    a.inverse = nullptr;
+    a.rows = rows;
+    a.k = k;
+    a.codes = codes;
+    a.scales = scales;
+    a.row_scale = row_scale;
+    a.err = static_cast<int *>(ws);
+    return from_cuda(launch_fp4_quantize(fmt, layout, act, a, static_cast<cudaStream_t>(stream)));
+}
+
+coli_status coli_moe_fp4_dequantize(int fmt, int layout, const uint8_t *codes, const uint8_t *scales,
+                                    const float *row_scale, int rows, int k, int act, void *out, size_t ldo,
+                                    void *stream) {
+    if (layout != COLI_FP4_ROWS && layout != COLI_FP4_TILES) return COLI_ERR_INVALID_ARG;
+    if (act != COLI_ACT_F32 && act != COLI_ACT_BF16) return COLI_ERR_INVALID_ARG;
+    coli_status s = fp4_shape(fmt, rows, k);
+    if (s != COLI_OK) return s;
+    if (ldo < static_cast<size_t>(k)) return COLI_ERR_SHAPE;
+    if (rows == 0) return COLI_OK;
+    if (!codes || !scales || !out) return COLI_ERR_INVALID_ARG;
+    const size_t item = act == COLI_ACT_F32 ? 4 : 2;
+    if (!aligned(codes, 8) || (row_scale && !aligned(row_scale, 4)) || !aligned(out, 16) || ldo * item % 16) return COLI_ERR_ALIGN;
+    return from_cuda(launch_fp4_dequantize(fmt, layout, codes, scales, row_scale, rows, k, act, out, ldo, static_cast<cudaStream_t>(stream)));
+}
+
+coli_status coli_moe_fp4_product(int fmt, const coli_fp4_rows *a, const coli_fp4_mats *w, int k, const int32_t *offsets,
+                                 int out_type, void *out, size_t ldo, void *ws, void *stream) {
+    if (!a || !w || (out_type != COLI_ACT_F32 && out_type != COLI_ACT_BF16)) return COLI_ERR_INVALID_ARG;
+    coli_status s = fp4_shape(fmt, a->rows, k);
+    if (s != COLI_OK) return s;
+    if (w->count <= 0 || w->n <= 0 || ldo < static_cast<size_t>(w->n)) return COLI_ERR_SHAPE;
+    if (!offsets && w->count != 1) return COLI_ERR_SHAPE;
+    if (w->count > 1024) return COLI_ERR_UNSUPPORTED;
+    // tiles of all groups, even of groups that overlap, are counted in 32 bits
+    if ((static_cast<long>(a->rows) / 16 + 1) * ((w->n + 127L) / 128) * (w->count + 1) > 0x7fffffffL) return COLI_ERR_UNSUPPORTED;
+    if (a->rows == 0) return COLI_OK;
+    if (!a->codes || !a->scales || !w->codes || !w->scales || !out) return COLI_ERR_INVALID_ARG;
+    if (w->count > 1) {
+        if (w->codes_stride < static_cast<size_t>(w->n) * (k / 2) || w->scales_stride < fp4_scale_bytes(fmt, COLI_FP4_TILES, w->n, k) ||
+            (w->row_scale && w->row_scale_stride < static_cast<size_t>(w->n)))
+            return COLI_ERR_SHAPE;
+        if (w->codes_stride % 16 || w->scales_stride % 16) return COLI_ERR_ALIGN;
+    }
+    if (!aligned(a->codes, 16) || !aligned(a->scales, 16) || !aligned(w->codes, 16) || !aligned(w->scales, 16) ||
+        (a->row_scale && !aligned(a->row_scale, 4)) || (w->row_scale && !aligned(w->row_scale, 4)) ||
+        (offsets && !aligned(offsets, 4)) || !aligned(out, out_type == COLI_ACT_F32 ? 4 : 2))
+        return COLI_ERR_ALIGN;
+    if (!ws || !aligned(ws, 256)) return COLI_ERR_WORKSPACE;
+    Fp4ProductArgs p;
+    p.a = *a;
+    p.w = *w;
+    p.shared = nullptr;
+    p.k = k;
+    p.offsets = offsets;
+    p.out_kind = out_type == COLI_ACT_F32 ? FP4_OUT_F32 : FP4_OUT_BF16;
+    p.out = out;
+    p.ldo = ldo;
+    p.err = static_cast<int *>(ws);
+    return from_cuda(launch_fp4_product(fmt, p, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

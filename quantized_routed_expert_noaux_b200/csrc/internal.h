@@ -142,6 +142,8 @@ cudaError_t launch_gate(const coli_moe_config &c, const float *Wr, const void *x
                         float *logits, cudaStream_t st);
 cudaError_t launch_route(const coli_moe_config &c, const float *logits, const float *bias,
                          int T, int32_t *ids, float *w, cudaStream_t st);
+cudaError_t launch_route_scores(const coli_moe_router &r, const void *logits, size_t ld, const float *bias, int T,
+                                int32_t *ids, float *w, cudaStream_t st);
 cudaError_t launch_group(const coli_moe_config &c, const int32_t *ids, int T, int32_t *counts,
                          int32_t *offsets, int32_t *perm, int32_t *unique, int32_t *n_unique,
                          int *err, cudaStream_t st);
