@@ -155,8 +155,28 @@ def _nbytes(t) -> int:
 def _stream(stream) -> Optional[int]:
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
+    return _current_stream()
+
+
+def _current_stream() -> int:
+    """Handle of the current device's current torch stream.  The handle alone: building torch's Stream
+    object takes longer (3.3 us against 0.3) than launching a small kernel."""
     import torch
-    return torch.cuda.current_stream().cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return torch.cuda.current_stream().cuda_stream
+    return raw(torch.cuda.current_device())
+
+
+def _device_stream(fn: str, stream, t) -> Optional[int]:
+    """_stream for a call whose tensors must live on the current device: t is one of them."""
+    if stream is not None:
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    if t is not None and not isinstance(t, int):
+        import torch
+        if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+            raise ColiError(fn, 1)
+    return _current_stream()
 
 
 def _check(fn: str, status: int) -> None:
@@ -305,7 +325,8 @@ def coli_moe_route_scores(router: MoERouter, logits, ld, bias, T, topk_ids, topk
     """Softmax or sigmoid routing of T tokens: row t of the logits at element t * ld (0: n_experts),
     bias [E] float32 or None."""
     _check("coli_moe_route_scores", lib.coli_moe_route_scores(
-        C.byref(router), _p(logits), ld, _p(bias), T, _p(topk_ids), _p(topk_w), _stream(stream)))
+        C.byref(router), _p(logits), ld, _p(bias), T, _p(topk_ids), _p(topk_w),
+        _device_stream("coli_moe_route_scores", stream, logits)))
 
 
 def coli_moe_fp4_scale_pitch(fmt: int, k: int) -> int:
@@ -326,18 +347,20 @@ def coli_moe_fp4_quantize(fmt, layout, act, x, src_rows, ldx, row_index, row_div
     result is source row r, or row_index[r] // row_div."""
     _check("coli_moe_fp4_quantize", lib.coli_moe_fp4_quantize(
         fmt, layout, act, _p(x), src_rows, ldx, _p(row_index), row_div, rows, k, _p(codes), _p(scales), _p(row_scale),
-        _p(ws), _stream(stream)))
+        _p(ws), _device_stream("coli_moe_fp4_quantize", stream, x)))
 
 
 def coli_moe_fp4_dequantize(fmt, layout, codes, scales, row_scale, rows, k, act, out, ldo, stream=None) -> None:
     _check("coli_moe_fp4_dequantize", lib.coli_moe_fp4_dequantize(
-        fmt, layout, _p(codes), _p(scales), _p(row_scale), rows, k, act, _p(out), ldo, _stream(stream)))
+        fmt, layout, _p(codes), _p(scales), _p(row_scale), rows, k, act, _p(out), ldo,
+        _device_stream("coli_moe_fp4_dequantize", stream, out)))
 
 
 def coli_moe_fp4_product(fmt, a: FP4Rows, w: FP4Mats, k, offsets, out_type, out, ldo, ws, stream=None) -> None:
     """out row i = a's row i times the matrix of its group (offsets [count + 1] int32; None: one matrix)."""
     _check("coli_moe_fp4_product", lib.coli_moe_fp4_product(
-        fmt, C.byref(a), C.byref(w), k, _p(offsets), out_type, _p(out), ldo, _p(ws), _stream(stream)))
+        fmt, C.byref(a), C.byref(w), k, _p(offsets), out_type, _p(out), ldo, _p(ws),
+        _device_stream("coli_moe_fp4_product", stream, out)))
 
 
 def fp4_rows_for(codes, scales, row_scale=None) -> FP4Rows:

@@ -16,12 +16,13 @@
 //               tiles of a k-block are adjacent), and the rows' codes.
 //   warp 1      MMA issuer: copies the k-block's scales from shared to tensor memory
 //               (tcgen05.cp, 128 rows x 4 scales each) and issues 4 MMAs of K = 64.
-//   warp 2      scales of the rows: 4 bytes at a time from their rows into the tile order that
-//               tcgen05.cp reads, asynchronously, LAG k-blocks ahead of the fence that publishes them.
+//   warps 2-3   scales of the rows, every other k-block each: from their rows through registers (the
+//               next k-block's loads in flight meanwhile) into the tile order that tcgen05.cp reads.
 //   warps 4-7   epilogue, from two accumulators: one drains while the other fills.
 // Tensor memory: accumulators at columns [0, 256), scale stage s at 256 + s * SF_COLS.  A scale
 // stage goes with a ring stage, so it is written again only after the MMAs that read it have
 // completed (the ring's empty barrier).
+#include <atomic>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -37,9 +38,8 @@ namespace {
 constexpr int A_BYTES = 128 * 128;       // weight codes of a k-block
 constexpr int MAX_MATS = 1025;           // 1024 and a shared one
 constexpr int NBOX = 5;                  // box heights 16 << i rows
-constexpr int W_PROD = 0, W_MMA = 1, W_SF = 2, W_EPI0 = 4, N_EPI = 4;
+constexpr int W_PROD = 0, W_MMA = 1, W_SF = 2, N_SF = 2, W_EPI0 = 4, N_EPI = 4;
 constexpr int THREADS = 8 * 32;
-constexpr int LAG = 2;                   // k-blocks between a row-scale copy and its publication
 
 template <int FMT> struct Sf;            // scales of a k-block
 template <> struct Sf<COLI_FP4_NV> { static constexpr int ATOMS = 4; };  // 64 elements per 4 scales
@@ -57,7 +57,7 @@ struct Plan {
     static constexpr int FIT = (220 * 1024) / STAGE, TFIT = 256 / SF_COLS;
     static constexpr int S = FIT < TFIT ? FIT : TFIT;         // ring stages
     static constexpr size_t SMEM = static_cast<size_t>(S) * STAGE + 1024;
-    static_assert(S > LAG, "the publication lags behind the copies by less than the ring");
+    static_assert(S >= 3, "the ring covers the copies' latency");
 };
 
 // Instruction descriptor of block-scaled e2m1 products: A and B e2m1 (bits 7-9, 10-11 = 1), both
@@ -97,11 +97,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                  ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
-// 4 bytes, or 4 zero bytes
-__device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool real) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
-}
-
 struct GemmArgs {
     const uint8_t *wsf, *wsf_shared;         // scale tiles
     size_t wsf_stride;
@@ -118,7 +113,8 @@ struct GemmArgs {
 };
 struct GemmMaps {
     CUtensorMap a, as;     // weight codes {k / 2 bytes, n rows, matrices}
-    CUtensorMap b[NBOX];   // row codes {k / 2 bytes, rows}
+    CUtensorMap b[NBOX];   // row codes {k / 2 bytes, rows}, boxes of 16 << i rows
+    CUtensorMap sf, sfs;   // scale tiles {512 bytes, tiles, matrices} (pairs)
 };
 
 struct Tile {
@@ -150,13 +146,170 @@ __device__ __forceinline__ Tile tile_at(int t, const int *s_first, const GemmArg
     int row0, cnt;
     group_rows(p, lo, row0, cnt);
     const int nch = (cnt + NT - 1) / NT;
-    const int per = ((cnt + nch - 1) / nch + 15) & ~15;  // rows of a chunk: even shares
+    const int per = ((cnt + nch - 1) / nch + 31) & ~31;  // rows of a chunk: even shares
     const int i = t - s_first[lo];
     x.m = i / nch;
     const int c = i - x.m * nch;
     x.n0 = row0 + c * per;
     x.nr = min(per, cnt - c * per);
     return x;
+}
+
+// The tile list: s_first[e] = tiles before matrix e (an exclusive scan by the whole CTA); the number
+// of tiles.
+template <int NT, int THREADS_>
+__device__ __forceinline__ int tile_list(const GemmArgs &p, int W, int MB, int *s_first, int *s_scan) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int carry = 0;
+    for (int base = 0; base < W; base += THREADS_) {
+        const int e = base + threadIdx.x;
+        int lo = 0, cnt = 0;
+        if (e < W) group_rows(p, e, lo, cnt);
+        if (cnt < 0) {
+            cnt = 0;
+            if (blockIdx.x == 0) atomicOr(p.err, COLI_DEVERR_GROUPING);
+        }
+        const int tiles = (cnt + NT - 1) / NT * MB;
+        int inc = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        if (lane == 31) s_scan[warp] = inc;
+        __syncthreads();
+        int before = carry;
+        for (int w = 0; w < THREADS_ / 32; ++w) {
+            const int v = s_scan[w];
+            if (w < warp) before += v;
+            carry += v;
+        }
+        if (e < W) s_first[e] = before + inc - tiles;
+        __syncthreads();
+    }
+    return carry;
+}
+
+// A run of 32 rows x this warp's 32 weight rows: v holds the sums of weight row r, rx the row scale
+// of the run's row `lane`.
+template <int OUT>
+__device__ __forceinline__ void store_run(const GemmArgs &p, const Tile &x, const int *v, int g, int r, float rw, float rx, int lane) {
+    if (OUT == FP4_OUT_SWIGLU) {
+        const bool gate = lane < 16;
+        const int col = (r >> 5) * 16 + (lane & 15);
+        float d[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) d[j] = __int_as_float(v[j]) * (rw * __shfl_sync(0xffffffffu, rx, j));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            // gate lanes take rows 0-15 of the run, up lanes rows 16-31
+            const float other = __shfl_xor_sync(0xffffffffu, gate ? d[16 + i] : d[i], 16);
+            const float gv = gate ? d[i] : other, uv = gate ? other : d[16 + i];
+            const int j = g + (gate ? i : 16 + i);
+            if (j < x.nr && r < p.n)
+                static_cast<__nv_bfloat16 *>(p.out)[static_cast<size_t>(x.n0 + j) * p.ldo + col] = __float2bfloat16_rn(gv / (1.0f + expf(-gv)) * uv);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            if (g + j >= x.nr) break;  // the same for the whole warp
+            const float y = __int_as_float(v[j]) * (rw * __shfl_sync(0xffffffffu, rx, j));
+            if (r < p.n) {
+                const size_t at = static_cast<size_t>(x.n0 + g + j) * p.ldo + r;
+                if (OUT == FP4_OUT_F32) static_cast<float *>(p.out)[at] = y;
+                else static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(y);
+            }
+        }
+    }
+}
+
+// Row-scale warp `w` of N_SF: its k-blocks' scales of up to NT rows, from their rows (4 * ATOMS bytes
+// each) to the tile order of tcgen05.cp.  A lane takes rows 32 c + 8 i + l (c = lane / 8, l = lane % 8) of
+// each 128, so that its warp's 4-byte stores fall into 32 different banks and all its addresses are one
+// register and a constant.  Rows behind the tile's last repeat a row that exists: what they give is not
+// stored by the epilogue.  publish(stage) tells the MMA warp.  A k-block of 256 rows must not take much more
+// than 500 cycles, in which its products are done (with addresses and bounds worked out per store it took 900).
+template <int FMT, int NT, typename Publish>
+__device__ __forceinline__ void row_scales(const GemmArgs &p, int w, int first, int stride, int ntiles, int KT, const int *s_first, int W,
+                                           unsigned char *ssb, uint64_t *empty, int S, volatile int *abort, Publish publish) {
+    constexpr int ATOMS = Sf<FMT>::ATOMS, HALVES = (NT + 127) / 128, SLOTS = 4 * HALVES;
+    const int lane = threadIdx.x & 31;
+    const size_t pitch = fp4_pitch(FMT, p.k);
+    const int r0 = 32 * (lane >> 3) + (lane & 7);
+    const uint32_t dst0 = smem_u32(ssb) + (lane & 7) * 16 + (lane >> 3) * 4;
+    // DEPTH k-blocks of this warp in registers: a buffer is loaded again, for the k-block DEPTH turns on,
+    // as soon as it has been stored (buffers are named by the unrolled loop: a copy from one to another
+    // would wait for its loads)
+    constexpr int DEPTH = 3;
+    uint32_t v[DEPTH][SLOTS][ATOMS];
+    // the cursor of the loads: tile, k-block, the slots' addresses
+    int t = first, kb = w;
+    const uint8_t *src[SLOTS];
+    bool upper = false;  // the tile has more than 128 rows
+    auto tile = [&]() {
+        if (t >= ntiles) return;
+        const Tile x = tile_at<NT>(t, s_first, p, W);
+        upper = x.nr > 128;
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i) src[i] = p.xsf + static_cast<size_t>(x.n0 + min(128 * (i >> 2) + 8 * (i & 3) + r0, x.nr - 1)) * pitch;
+    };
+    auto step = [&]() {  // to the tile that holds k-block kb
+        if (kb < KT) return;
+        do {
+            kb -= KT;
+            t += stride;
+        } while (kb >= KT && t < ntiles);
+        tile();
+    };
+    auto load = [&](uint32_t (&d)[SLOTS][ATOMS]) {
+        if (t < ntiles) {
+            const int off = kb * (4 * ATOMS);
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i) {
+                if (i < 4 || upper) {
+                    if (ATOMS == 4) {
+                        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(src[i] + off));
+                        d[i][0] = q.x; d[i][1] = q.y; d[i][ATOMS - 2] = q.z; d[i][ATOMS - 1] = q.w;
+                    } else {
+                        const uint2 q = __ldg(reinterpret_cast<const uint2 *>(src[i] + off));
+                        d[i][0] = q.x; d[i][1] = q.y;
+                    }
+                }
+            }
+        }
+        kb += N_SF;
+        step();
+    };
+    tile();
+    step();
+    // k-blocks of this warp: every N_SF-th of the CTA's
+    const uint32_t all = first < ntiles ? static_cast<uint32_t>((ntiles - first + stride - 1) / stride) * KT : 0u;
+#pragma unroll
+    for (int b = 0; b < DEPTH; ++b) load(v[b]);
+    uint32_t s = w, phase = 1;
+    for (uint32_t it = w; it < all;) {
+#pragma unroll
+        for (int b = 0; b < DEPTH; ++b) {
+            if (it >= all) return;
+            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[s]), phase, abort, p.err))) return;
+            const uint32_t dst = dst0 + s * (ATOMS * 512 * HALVES);
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i)
+#pragma unroll
+                for (int j = 0; j < ATOMS; ++j)
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + (j * HALVES + (i >> 2)) * 512 + (i & 3) * 128), "r"(v[b][i][j]) : "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) publish(s);
+            load(v[b]);
+            it += N_SF;
+            s += N_SF;
+            if (s >= static_cast<uint32_t>(S)) {
+                s -= S;
+                phase ^= 1;
+            }
+        }
+    }
 }
 
 template <int FMT, int NT, int OUT>
@@ -191,35 +344,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
         s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    // the tile list: an exclusive scan of the matrices' tiles
-    int carry = 0;
-    for (int base = 0; base < W; base += THREADS) {
-        const int e = base + threadIdx.x;
-        int lo = 0, cnt = 0;
-        if (e < W) group_rows(p, e, lo, cnt);
-        if (cnt < 0) {
-            cnt = 0;
-            if (blockIdx.x == 0) atomicOr(p.err, COLI_DEVERR_GROUPING);
-        }
-        const int tiles = (cnt + NT - 1) / NT * MB;
-        int inc = tiles;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += v;
-        }
-        if (lane == 31) s_scan[warp] = inc;
-        __syncthreads();
-        int before = carry;
-        for (int w = 0; w < THREADS / 32; ++w) {
-            const int v = s_scan[w];
-            if (w < warp) before += v;
-            carry += v;
-        }
-        if (e < W) s_first[e] = before + inc - tiles;
-        __syncthreads();
-    }
-    const int ntiles = carry;
+    const int ntiles = tile_list<NT, THREADS>(p, W, MB, s_first, s_scan);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -227,8 +352,9 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
 
     if (warp == W_PROD) {
         // ------------------------------------------------------------------ TMA producer
-        // lane 0: weight codes and their scales; lane i < NBOX: the box of 16 << (NBOX - 1 - i) rows
-        // when that bit of the row count is set
+        // one elected lane issues with warp-uniform operands: weight codes, their scales, and a box of
+        // 16 << i rows for every bit i of the row count (from lanes that differ, or behind a test of the
+        // lane, a copy took the compiler's loop over lanes and 200 cycles)
         const size_t mtile = 128 * fp4_pitch(FMT, p.k);  // scale bytes of 128 weight rows
         uint32_t it = 0;
         for (int t = blockIdx.x; t < ntiles; t += gridDim.x) {
@@ -242,19 +368,17 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
                 const int s = it % P::S;
                 if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[s]), ((it / P::S) & 1) ^ 1, abort, p.err))) goto prod_done;
                 const uint32_t fb = smem_u32(&full[s]);
-                if (lane == 0) mbar_expect_tx(fb, A_BYTES + P::SFA_BYTES + n16 * 16 * 128);
-                __syncwarp();
-                if (lane == 0) {
+                if (elect_one()) {
+                    mbar_expect_tx(fb, A_BYTES + P::SFA_BYTES + n16 * 16 * 128);
                     tma_load_3d(smem_u32(sa + s * A_BYTES), ta, kb * 128, x.m * 128, ez, fb);
                     bulk_load(smem_u32(ssa + s * P::SFA_BYTES), wsf + static_cast<size_t>(kb) * P::SFA_BYTES, P::SFA_BYTES, fb);
-                }
-                if (lane < NBOX) {
-                    const int bit = NBOX - 1 - lane;
-                    if ((n16 >> bit) & 1) {
+#pragma unroll
+                    for (int bit = NBOX - 1; bit >= 0; --bit) {
                         const int row0 = 16 * ((n16 >> (bit + 1)) << (bit + 1));  // rows of the larger boxes
-                        tma_load_2d(smem_u32(sb + s * P::B_BYTES + row0 * 128), &maps.b[bit], kb * 128, x.n0 + row0, fb);
+                        if ((n16 >> bit) & 1) tma_load_2d(smem_u32(sb + s * P::B_BYTES + row0 * 128), &maps.b[bit], kb * 128, x.n0 + row0, fb);
                     }
                 }
+                __syncwarp();
             }
         }
     prod_done:
@@ -313,40 +437,11 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
         if (elect_one()) mma_commit(smem_u32(drain));
         __syncwarp();
         mbar_drain(smem_u32(drain), 0);
-    } else if (warp == W_SF) {
+    } else if (warp < W_EPI0) {
         // ------------------------------------------------------------------ scales of the rows
-        const size_t pitch = fp4_pitch(FMT, p.k);
-        uint32_t it = 0;
-        for (int t = blockIdx.x; t < ntiles; t += gridDim.x) {
-            const Tile x = tile_at<NT>(t, s_first, p, W);
-            const int nr16 = (x.nr + 15) & ~15;
-            for (int kb = 0; kb < KT; ++kb, ++it) {
-                const int s = it % P::S;
-                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[s]), ((it / P::S) & 1) ^ 1, abort, p.err))) goto sf_done;
-                const uint32_t dst = smem_u32(ssb + s * P::SFB_BYTES);
-                for (int r = lane; r < nr16; r += 32) {
-                    const bool real = x.n0 + r < p.rows;
-                    const uint8_t *src = p.xsf + static_cast<size_t>(real ? x.n0 + r : 0) * pitch + kb * (4 * P::ATOMS);
-                    const uint32_t at = dst + (r >> 7) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4;
-#pragma unroll
-                    for (int i = 0; i < P::ATOMS; ++i) copy4(at + i * 512 * P::HALVES, src + 4 * i, real);
-                }
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                if (it >= LAG) {
-                    asm volatile("cp.async.wait_group %0;" ::"n"(LAG) : "memory");
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sfull[(it - LAG) % P::S]));
-                }
-            }
-        }
-    sf_done:
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0 && !*abort)
-            for (uint32_t i = it > static_cast<uint32_t>(LAG) ? it - LAG : 0; i < it; ++i) mbar_arrive(smem_u32(&sfull[i % P::S]));
-    } else if (warp >= W_EPI0) {
+        row_scales<FMT, NT>(p, warp - W_SF, blockIdx.x, gridDim.x, ntiles, KT, s_first, W, ssb, empty, P::S, abort,
+                            [&](int st) { mbar_arrive(smem_u32(&sfull[st])); });
+    } else {
         // ------------------------------------------------------------------ epilogue
         const int q = warp - W_EPI0;  // TMEM lane quarter (warp % 4)
         uint32_t tl = 0;
@@ -363,32 +458,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
                 int v[32];
                 tmem_ld32(dt + g, v);
                 const float rx = p.xrow && g + lane < x.nr ? __ldg(p.xrow + x.n0 + g + lane) : 1.f;
-                if (OUT == FP4_OUT_SWIGLU) {
-                    const bool gate = lane < 16;
-                    const int col = (x.m * 128 + 32 * q) / 2 + (lane & 15);
-                    float d[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) d[j] = __int_as_float(v[j]) * (rw * __shfl_sync(0xffffffffu, rx, j));
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        // gate lanes take rows 0-15 of the run, up lanes rows 16-31
-                        const float other = __shfl_xor_sync(0xffffffffu, gate ? d[16 + i] : d[i], 16);
-                        const float gv = gate ? d[i] : other, uv = gate ? other : d[16 + i];
-                        const int j = g + (gate ? i : 16 + i);
-                        if (j < x.nr && r < p.n)
-                            static_cast<__nv_bfloat16 *>(p.out)[static_cast<size_t>(x.n0 + j) * p.ldo + col] = __float2bfloat16_rn(gv / (1.0f + expf(-gv)) * uv);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float y = __int_as_float(v[j]) * (rw * __shfl_sync(0xffffffffu, rx, j));
-                        if (g + j < x.nr && r < p.n) {
-                            const size_t at = static_cast<size_t>(x.n0 + g + j) * p.ldo + r;
-                            if (OUT == FP4_OUT_F32) static_cast<float *>(p.out)[at] = y;
-                            else static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(y);
-                        }
-                    }
-                }
+                store_run<OUT>(p, x, v, g, r, rw, rx, lane);
             }
             tc_fence_before();
             mbar_arrive(smem_u32(&dempty[acc]));
@@ -403,6 +473,338 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
     }
 }
 
+// ------------------------------------------------------------------ CTA pairs --------------
+// The same product with tiles of 256 weight rows x up to 256 rows on a pair of CTAs
+// (cta_group::2): each CTA fetches its own 128 weight rows and half of the tile's rows, the tensor
+// cores read both halves, so a byte of shared memory feeds twice the products of a 128 x 128 tile.
+// Both CTAs hold the scales of all rows of the tile.  One accumulator of 256 columns per CTA; the
+// epilogue's eight warps take it whole into registers before they store, so that the next
+// tile's products wait for the reads alone.
+constexpr int P_NT = 256;
+constexpr int P_EPI = 8, P_THREADS = (4 + P_EPI) * 32;
+
+constexpr int P_OUT = 8192;              // bytes of an epilogue half's staging buffer
+
+template <int FMT>
+struct PairPlan {
+    static constexpr int ATOMS = Sf<FMT>::ATOMS;
+    static constexpr int B_BYTES = P_NT / 2 * 128;
+    static constexpr int SFA_BYTES = ATOMS * 512, SFB_BYTES = ATOMS * 1024;
+    static constexpr int STAGE = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
+    static constexpr int SF_COLS = ATOMS * 12;
+    static constexpr int FIT = (220 * 1024 - 2 * P_OUT) / STAGE, TFIT = 256 / SF_COLS;
+    static constexpr int S = FIT < TFIT ? FIT : TFIT;
+    static constexpr size_t SMEM = static_cast<size_t>(S) * STAGE + 2 * P_OUT + 1024;
+    static_assert(S >= 3, "the ring covers the copies' latency");
+};
+
+__device__ __forceinline__ void half_sync(int half) {
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+}
+// A predicate OR-ed over the eight epilogue warps.
+__device__ __forceinline__ bool epi_or(bool pred) {
+    uint32_t r;
+    asm volatile("{ .reg .pred p, q; setp.ne.u32 p, %1, 0; bar.red.or.pred q, 3, %2, p; selp.u32 %0, 1, 0, q; }"
+                 : "=r"(r) : "r"(static_cast<uint32_t>(pred)), "n"(P_EPI * 32) : "memory");
+    return r != 0;
+}
+// A run of RUN rows x this CTA's 128 weight rows (64 columns of h with SwiGLU) through shared memory:
+// lanes hold a weight row each, out wants weight rows side by side.  Stored straight from the lanes, 2
+// bytes each, a tile's epilogue took 21,000 cycles against 12,000 of its products at k = 6144.
+// `buf`: the half's P_OUT bytes; vec: 16-byte stores are aligned.
+template <int OUT>
+__device__ __forceinline__ void staged_run(const GemmArgs &p, const Tile &x, const int *v, int g, int row0, float rw, float rx,
+                                           unsigned char *buf, int half, int q, int lane, bool vec) {
+    constexpr int ITEM = OUT == FP4_OUT_F32 ? 4 : 2;
+    constexpr int RUN = OUT == FP4_OUT_F32 ? 16 : 32;     // rows at a time
+    constexpr int COLS = OUT == FP4_OUT_SWIGLU ? 64 : 128;
+    constexpr int VPR = COLS * ITEM / 16;                 // 16-byte pieces of a row
+    const int tid = 32 * q + lane;
+#pragma unroll
+    for (int h = 0; h < 32 / RUN; ++h) {
+        if (g + RUN * h >= x.nr) return;                  // the same for all four warps
+        half_sync(half);                                  // the buffer's last run has been read
+        if (OUT == FP4_OUT_SWIGLU) {
+            const bool gate = lane < 16;
+            float d[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) d[j] = __int_as_float(v[j]) * (rw * __shfl_sync(0xffffffffu, rx, j));
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                // gate lanes take rows 0-15 of the run, up lanes rows 16-31
+                const float other = __shfl_xor_sync(0xffffffffu, gate ? d[16 + i] : d[i], 16);
+                const float gv = gate ? d[i] : other, uv = gate ? other : d[16 + i];
+                reinterpret_cast<__nv_bfloat16 *>(buf)[(gate ? i : 16 + i) * COLS + 16 * q + (lane & 15)] = __float2bfloat16_rn(gv / (1.0f + expf(-gv)) * uv);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < RUN; ++j) {
+                const float y = __int_as_float(v[RUN * h + j]) * (rw * __shfl_sync(0xffffffffu, rx, RUN * h + j));
+                if (OUT == FP4_OUT_F32) reinterpret_cast<float *>(buf)[j * COLS + tid] = y;
+                else reinterpret_cast<__nv_bfloat16 *>(buf)[j * COLS + tid] = __float2bfloat16_rn(y);
+            }
+        }
+        half_sync(half);
+        const int ncols = OUT == FP4_OUT_SWIGLU ? p.n / 2 : p.n, col0 = OUT == FP4_OUT_SWIGLU ? row0 / 2 : row0;
+#pragma unroll
+        for (int i = 0; i < RUN * VPR / 128; ++i) {
+            const int at = i * 128 + tid, j = at / VPR, c = col0 + (at % VPR) * (16 / ITEM);
+            const int row = g + RUN * h + j;
+            if (row >= x.nr || c >= ncols) continue;
+            unsigned char *dst = static_cast<unsigned char *>(p.out) + (static_cast<size_t>(x.n0 + row) * p.ldo + c) * ITEM;
+            const uint4 w = *reinterpret_cast<const uint4 *>(buf + 16 * at);
+            if (vec && c + 16 / ITEM <= ncols) {
+                *reinterpret_cast<uint4 *>(dst) = w;
+            } else {
+                const int n = min(16 / ITEM, ncols - c);
+                for (int e = 0; e < n; ++e) {
+                    if (ITEM == 4) reinterpret_cast<float *>(dst)[e] = reinterpret_cast<const float *>(buf + 16 * at)[e];
+                    else reinterpret_cast<uint16_t *>(dst)[e] = reinterpret_cast<const uint16_t *>(buf + 16 * at)[e];
+                }
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void remote_arrive(uint32_t a) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(a) : "memory");
+}
+__device__ __forceinline__ void remote_expect_tx(uint32_t a, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(a), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_cluster(uint32_t a, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok) : "r"(a), "r"(parity), "r"(20000u) : "memory");
+    return ok != 0;
+}
+// mbar_wait for a phase that the other CTA of the pair takes part in
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t a, uint32_t parity, volatile int *abort, int *err) {
+    if (mbar_try_cluster(a, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_cluster(a, parity)) {
+        if (*abort) return false;
+        if (clock64() - t0 > WAIT_CYCLES) {
+            *abort = 1;
+            atomicOr(err, COLI_DEVERR_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+// TMA loads of a pair's CTA: into its own shared memory, the barrier in the leader's.
+__device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap *m, int c0, int c1, int c2, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap *m, int c0, int c1, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(bar) : "memory");
+}
+template <int FMT>
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    if (FMT == COLI_FP4_NV)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n"
+                     ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n"
+                     ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void pair_sf_copy(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// arrive on the barrier at this address in both CTAs once the MMAs issued so far have completed
+__device__ __forceinline__ void pair_commit(uint32_t mbar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(mbar), "h"(static_cast<uint16_t>(3)) : "memory");
+}
+
+template <int FMT, int OUT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
+fp4_pair_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs p) {
+    using P = PairPlan<FMT>;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    // the same offset in both CTAs: the dynamic array starts at the same address in each
+    unsigned char *sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    unsigned char *sa = sm, *sb = sa + P::S * A_BYTES, *ssa = sb + P::S * P::B_BYTES, *ssb = ssa + P::S * P::SFA_BYTES;
+    __shared__ __align__(8) uint64_t bars[2 * P::S + 3];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    __shared__ int s_first[MAX_MATS], s_scan[P_THREADS / 32];
+    // full: the leader's, of both CTAs' copies; empty, dfull: in each CTA; dempty: the leader's
+    uint64_t *full = bars, *empty = full + P::S, *dfull = empty + P::S, *dempty = dfull + 1, *drain = dempty + 1;
+    volatile int *abort = &s_abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int MB = (p.n + 255) / 256, KT = (p.k + FP4_KB - 1) / FP4_KB;
+    const int W = p.E + p.S;
+
+    if (threadIdx.x == 32) {
+        for (int i = 0; i < P::S; ++i) {
+            mbar_init(smem_u32(&full[i]), 4);  // each CTA's producer and row-scale warp
+            mbar_init(smem_u32(&empty[i]), 1);
+        }
+        mbar_init(smem_u32(dfull), 1);
+        mbar_init(smem_u32(dempty), 2 * P_EPI);
+        mbar_init(smem_u32(drain), 1);
+        s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512u) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    const int ntiles = tile_list<P_NT, P_THREADS>(p, W, MB, s_first, s_scan);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tbase = s_tmem;
+
+    if (warp == W_PROD) {
+        // ------------------------------------------------------------------ TMA producer
+        const int atoms = static_cast<int>(fp4_pitch(FMT, p.k) / 4);  // scale tiles of 128 weight rows
+        uint32_t it = 0;
+        for (int t = pair; t < ntiles; t += pairs) {
+            const Tile x = tile_at<P_NT>(t, s_first, p, W);
+            const bool shared = x.e >= p.E;
+            const CUtensorMap *ta = shared ? &maps.as : &maps.a, *tsf = shared ? &maps.sfs : &maps.sf;
+            const int ez = shared ? 0 : x.e;
+            const int n32 = (x.nr + 31) / 32;                        // N / 32; this CTA's share is 16 * n32 rows
+            const int row_lo = x.n0 + static_cast<int>(rank) * 16 * n32;
+            for (int kb = 0; kb < KT; ++kb, ++it) {
+                const int s = it % P::S;
+                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[s]), ((it / P::S) & 1) ^ 1, abort, p.err))) goto prod_done;
+                const uint32_t fb = map_rank(smem_u32(&full[s]), 0);
+                if (elect_one()) {
+                    remote_expect_tx(fb, A_BYTES + P::SFA_BYTES + n32 * 16 * 128);
+                    pair_load_3d(smem_u32(sa + s * A_BYTES), ta, kb * 128, x.m * 256 + static_cast<int>(rank) * 128, ez, fb);
+                    pair_load_3d(smem_u32(ssa + s * P::SFA_BYTES), tsf, 0, (x.m * 2 + static_cast<int>(rank)) * atoms + kb * P::ATOMS, ez, fb);
+#pragma unroll
+                    for (int bit = NBOX - 2; bit >= 0; --bit) {
+                        const int row0 = 16 * ((n32 >> (bit + 1)) << (bit + 1));
+                        if ((n32 >> bit) & 1) pair_load_2d(smem_u32(sb + s * P::B_BYTES + row0 * 128), &maps.b[bit], kb * 128, row_lo + row0, fb);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    prod_done:
+        // a producer that gives up leaves its copies to land: the pair's barrier below waits for the
+        // leader, whose MMA warp waits for them (bounded)
+        ;
+    } else if (warp == W_MMA && rank == 0) {
+        // ------------------------------------------------------------------ MMA issuer (the pair's)
+        uint32_t it = 0, tl = 0;
+        const uint64_t adesc0 = smem_desc_sw128(smem_u32(sa)), bdesc0 = smem_desc_sw128(smem_u32(sb));
+        const uint64_t sadesc0 = smem_desc_sf(smem_u32(ssa)), sbdesc0 = smem_desc_sf(smem_u32(ssb));
+        for (int t = pair; t < ntiles; t += pairs, ++tl) {
+            const Tile x = tile_at<P_NT>(t, s_first, p, W);
+            const int n32 = (x.nr + 31) / 32;
+            const uint32_t idesc = (idesc_fp4<FMT>() & ~(3u << 27)) | (2u << 27) | (static_cast<uint32_t>(4 * n32) << 17);
+            if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(dempty), (tl & 1) ^ 1, abort, p.err))) goto mma_done;
+            tc_fence_after();
+            for (int kb = 0; kb < KT; ++kb, ++it) {
+                const int s = it % P::S;
+                if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&full[s]), (it / P::S) & 1, abort, p.err))) goto mma_done;
+                tc_fence_after();
+                const int steps = min(4, (p.k - kb * FP4_KB + 63) / 64);
+                if (elect_one()) {
+                    const uint32_t sfa = tbase + 256 + s * P::SF_COLS, sfb = sfa + 4 * P::ATOMS;
+                    const uint64_t ad = adesc0 + static_cast<uint64_t>(s * (A_BYTES >> 4)), bd = bdesc0 + static_cast<uint64_t>(s * (P::B_BYTES >> 4));
+                    const uint64_t sad = sadesc0 + static_cast<uint64_t>(s * (P::SFA_BYTES >> 4)), sbd = sbdesc0 + static_cast<uint64_t>(s * (P::SFB_BYTES >> 4));
+#pragma unroll
+                    for (int i = 0; i < P::ATOMS; ++i) {
+                        pair_sf_copy(sfa + 4 * i, sad + 32 * i);
+                        pair_sf_copy(sfb + 8 * i, sbd + 64 * i);
+                        pair_sf_copy(sfb + 8 * i + 4, sbd + 64 * i + 32);
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        if (kk < steps) {
+                            const int atom = FMT == COLI_FP4_NV ? kk : kk >> 1;
+                            const uint32_t id = FMT == COLI_FP4_NV ? 0u : 2u * (kk & 1);
+                            pair_mma<FMT>(tbase, ad + 2 * kk, bd + 2 * kk, idesc | (id << 4) | (id << 29), sfa + 4 * atom, sfb + 8 * atom, (kb | kk) != 0);
+                        }
+                    }
+                    pair_commit(smem_u32(&empty[s]));
+                }
+                __syncwarp();
+            }
+            if (elect_one()) pair_commit(smem_u32(dfull));
+            __syncwarp();
+        }
+    mma_done:
+        if (elect_one())
+            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(drain)) : "memory");
+        __syncwarp();
+        mbar_drain(smem_u32(drain), 0);
+        if (*abort)  // copies that are still in flight land before shared memory is released
+            for (uint32_t i = it; i < it + P::S; ++i) mbar_drain(smem_u32(&full[i % P::S]), (i / P::S) & 1);
+    } else if (warp == W_SF || warp == W_SF + 1) {
+        // ------------------------------------------------------------------ scales of the rows
+        row_scales<FMT, P_NT>(p, warp - W_SF, pair, pairs, ntiles, KT, s_first, W, ssb, empty, P::S, abort,
+                              [&](int st) { remote_arrive(map_rank(smem_u32(&full[st]), 0)); });
+    } else if (warp >= W_EPI0) {
+        // ------------------------------------------------------------------ epilogue
+        const int q = warp & 3, half = (warp - W_EPI0) >> 2;  // TMEM lane quarter, 128-column half
+        unsigned char *obuf = ssb + P::S * P::SFB_BYTES + half * P_OUT;
+        constexpr int ITEM = OUT == FP4_OUT_F32 ? 4 : 2;
+        const bool vec = ((reinterpret_cast<uintptr_t>(p.out) | (p.ldo * ITEM)) & 15) == 0;
+        uint32_t tl = 0;
+        for (int t = pair; t < ntiles; t += pairs, ++tl) {
+            const Tile x = tile_at<P_NT>(t, s_first, p, W);
+            const int r = x.m * 256 + static_cast<int>(rank) * 128 + 32 * q + lane;
+            const float *wrow = x.e >= p.E ? p.wrow_shared : (p.wrow ? p.wrow + static_cast<size_t>(x.e) * p.wrow_stride : nullptr);
+            const float rw = wrow && r < p.n ? __ldg(wrow + r) : 1.f;
+            float rx[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int j = 128 * half + 32 * g + lane;
+                rx[g] = p.xrow && j < x.nr ? __ldg(p.xrow + x.n0 + j) : 1.f;
+            }
+            // (all eight warps meet in the staging barriers: they give up together, or not at all)
+            if (epi_or(!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(dfull), tl & 1, abort, p.err)))) break;
+            tc_fence_after();
+            int v[4][32];
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                if (128 * half + 32 * g < x.nr) tmem_ld32(tbase + (static_cast<uint32_t>(32 * q) << 16) + 128 * half + 32 * g, v[g]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) remote_arrive(map_rank(smem_u32(dempty), 0));
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                if (128 * half + 32 * g < x.nr)
+                    staged_run<OUT>(p, x, v[g], 128 * half + 32 * g, x.m * 256 + static_cast<int>(rank) * 128, rw, rx[g], obuf, half, q, lane, vec);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    if (warp == 0) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(512u) : "memory");
+    }
+}
+
 // Weight codes of `count` matrices, boxes of 128 rows of a k-block.
 bool mats_map(CUtensorMap *m, const coli_fp4_mats &w, int k) {
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(k) / 2, static_cast<cuuint64_t>(w.n), static_cast<cuuint64_t>(w.count)};
@@ -410,21 +812,50 @@ bool mats_map(CUtensorMap *m, const coli_fp4_mats &w, int k) {
     const cuuint32_t box[3] = {128, 128, 1};
     return encode_u8(m, w.codes, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
+// Scale tiles of `count` matrices, boxes of a k-block's tiles.
+bool tiles_map(CUtensorMap *m, const coli_fp4_mats &w, int fmt, int k) {
+    const cuuint64_t bytes = fp4_scale_bytes(fmt, COLI_FP4_TILES, w.n, k);
+    const cuuint64_t dims[3] = {128, bytes / 512, static_cast<cuuint64_t>(w.count)};
+    const cuuint64_t strides[2] = {512, w.count > 1 ? w.scales_stride : bytes};
+    const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(FP4_KB / fp4_block(fmt) / 4), 1}, es[3] = {1, 1, 1};
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+    return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t *>(w.scales), dims, strides, box, es,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Row codes, boxes of 16 << i rows, as far as the rows reach.
 bool rows_maps(CUtensorMap *m, const coli_fp4_rows &a, int k) {
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k) / 2, static_cast<cuuint64_t>(a.rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(k) / 2};
     for (int i = 0; i < NBOX; ++i) {
-        const cuuint32_t box[2] = {128, 16u << i};
+        if (i && (8 << i) >= a.rows) {  // no group is that high: the box is never used
+            m[i] = m[i - 1];
+            continue;
+        }
+        const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(16 << i)};
         if (!encode_u8(m + i, a.codes, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return false;
     }
     return true;
+}
+
+// The kernel's shared-memory attribute lasts as long as the context: set once per device (twice is
+// harmless).
+template <typename K>
+cudaError_t allow_smem(K *kernel, size_t bytes, std::atomic<uint64_t> &ready) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (ready.load(std::memory_order_relaxed) >> dev & 1))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess && dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    return e;
 }
 
 template <int FMT, int NT, int OUT>
 cudaError_t launch_gemm(const GemmMaps &maps, const GemmArgs &g, cudaStream_t st) {
     using P = Plan<FMT, NT>;
     auto kernel = fp4_gemm_kernel<FMT, NT, OUT>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(P::SMEM));
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = allow_smem(kernel, P::SMEM, ready);
     if (e != cudaSuccess) return e;
     const long chunks = g.rows / NT + (g.rows < g.E + g.S ? g.rows : g.E + g.S);  // at most
     const long tiles = (chunks < 1 ? 1 : chunks) * ((g.n + 127) / 128);
@@ -433,8 +864,27 @@ cudaError_t launch_gemm(const GemmMaps &maps, const GemmArgs &g, cudaStream_t st
     return cudaGetLastError();
 }
 
+template <int FMT, int OUT>
+cudaError_t launch_pair(const GemmMaps &maps, const GemmArgs &g, cudaStream_t st) {
+    using P = PairPlan<FMT>;
+    auto kernel = fp4_pair_kernel<FMT, OUT>;
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = allow_smem(kernel, P::SMEM, ready);
+    if (e != cudaSuccess) return e;
+    const long chunks = g.rows / P_NT + (g.rows < g.E + g.S ? g.rows : g.E + g.S);
+    const long tiles = (chunks < 1 ? 1 : chunks) * ((g.n + 255) / 256);
+    const int pairs = device_sm_count() / 2;
+    kernel<<<2 * static_cast<int>(tiles < pairs ? tiles : pairs), P_THREADS, P::SMEM, st>>>(maps, g);
+    return cudaGetLastError();
+}
+
 template <int FMT>
-cudaError_t launch_fmt(const GemmMaps &maps, const GemmArgs &g, int out_kind, cudaStream_t st) {
+cudaError_t launch_fmt(const GemmMaps &maps, const GemmArgs &g, int out_kind, bool pairs, cudaStream_t st) {
+    if (pairs) {
+        if (out_kind == FP4_OUT_F32) return launch_pair<FMT, FP4_OUT_F32>(maps, g, st);
+        if (out_kind == FP4_OUT_BF16) return launch_pair<FMT, FP4_OUT_BF16>(maps, g, st);
+        return launch_pair<FMT, FP4_OUT_SWIGLU>(maps, g, st);
+    }
     if (out_kind == FP4_OUT_F32) return launch_gemm<FMT, 128, FP4_OUT_F32>(maps, g, st);
     if (out_kind == FP4_OUT_BF16) return launch_gemm<FMT, 128, FP4_OUT_BF16>(maps, g, st);
     return launch_gemm<FMT, 128, FP4_OUT_SWIGLU>(maps, g, st);
@@ -442,11 +892,18 @@ cudaError_t launch_fmt(const GemmMaps &maps, const GemmArgs &g, int out_kind, cu
 
 }  // namespace
 
+// Tiles of 256 x 256 on CTA pairs, or of 128 x 128 on single CTAs: pairs from PAIR_ROWS rows per matrix
+// on average.  Measured (4096 x 6144 matrices, NV, bf16 out; pairs against single CTAs, us): 64
+// matrices with 32 / 64 / 128 rows each 147 / 152 / 167 against 145 / 152 / 211; one matrix with 16 / 64 /
+// 256 / 2048 / 8192 rows 11.7 / 12.4 / 16.5 / 31.5 / 94 against 11.7 / 14.5 / 19.2 / 49 / 146.
+constexpr int PAIR_ROWS = 48;
+
 cudaError_t launch_fp4_product(int fmt, const Fp4ProductArgs &p, cudaStream_t st) {
     GemmMaps maps;
-    bool ok = mats_map(&maps.a, p.w, p.k) && rows_maps(maps.b, p.a, p.k);
-    if (ok && p.shared) ok = mats_map(&maps.as, *p.shared, p.k);
-    else maps.as = maps.a;
+    const bool pairs = p.a.rows / (p.w.count + (p.shared ? 1 : 0)) >= PAIR_ROWS;
+    bool ok = mats_map(&maps.a, p.w, p.k) && (!p.shared || mats_map(&maps.as, *p.shared, p.k));
+    ok = ok && rows_maps(maps.b, p.a, p.k);
+    if (pairs) ok = ok && tiles_map(&maps.sf, p.w, fmt, p.k) && (!p.shared || tiles_map(&maps.sfs, *p.shared, fmt, p.k));
     if (!ok) return cudaErrorInvalidValue;
     GemmArgs g;
     g.wsf = p.w.scales;
@@ -466,7 +923,7 @@ cudaError_t launch_fp4_product(int fmt, const Fp4ProductArgs &p, cudaStream_t st
     g.out = p.out;
     g.ldo = p.ldo;
     g.err = p.err;
-    return fmt == COLI_FP4_MX ? launch_fmt<COLI_FP4_MX>(maps, g, p.out_kind, st) : launch_fmt<COLI_FP4_NV>(maps, g, p.out_kind, st);
+    return fmt == COLI_FP4_MX ? launch_fmt<COLI_FP4_MX>(maps, g, p.out_kind, pairs, st) : launch_fmt<COLI_FP4_NV>(maps, g, p.out_kind, pairs, st);
 }
 
 }  // namespace coli
