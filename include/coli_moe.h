@@ -31,6 +31,15 @@
  *   consecutive columns of the row.  Records sit `expert_stride` bytes apart (a multiple of
  *   256) and the record base must be 256-byte aligned.
  *
+ *   Microscaled 4-bit containers (COLI_W_NVFP4, COLI_W_MXFP4; group_size 0): W1 codes [2 I][H] | Wd
+ *   codes [H][I] | scale tiles of W1 | scale tiles of Wd | with COLI_W_NVFP4 the float32 row scales
+ *   of W1 [2 I] and of Wd [H].  W1 holds 16 gate rows, the same 16 up rows, the next 16 gate rows and so on
+ *   (row 32 j + i is gate row 16 j + i, row 32 j + 16 + i up row 16 j + i, i < 16).  Codes, scales and tiles
+ *   as the microscaled 4-bit section below has them; coli_moe_fp4_pack_record writes a record.  With
+ *   these containers the layer quantises its activations too: x of every token, and h = SiLU(g) * u
+ *   rounded to bf16, as coli_moe_fp4_quantize does; y is rounded to bf16 before the combine, whose
+ *   order is fixed.
+ *
  * Tensor layouts (row-major):
  *   x        [T][H]   float32 (act = COLI_ACT_F32) or bfloat16 bits (COLI_ACT_BF16), 16-B aligned
  *   logits   [T][E]   float32
@@ -59,7 +68,13 @@ typedef enum {
     COLI_ERR_WORKSPACE = 7     /* workspace NULL, misaligned or smaller than required */
 } coli_status;
 
-typedef enum { COLI_W_INT2 = 2, COLI_W_INT4 = 4, COLI_W_INT8 = 8 } coli_wfmt;
+typedef enum {
+    COLI_W_INT2 = 2,
+    COLI_W_INT4 = 4,
+    COLI_W_INT8 = 8,
+    COLI_W_NVFP4 = 20,  /* e2m1, an e4m3 scale per 16 (COLI_FP4_NV below) */
+    COLI_W_MXFP4 = 36   /* e2m1, a power-of-two scale per 32 (COLI_FP4_MX below) */
+} coli_wfmt;
 typedef enum { COLI_ACT_F32 = 0, COLI_ACT_BF16 = 1 } coli_act;
 
 /* Device error word codes (bit flags, OR-ed together by the kernels). */
@@ -111,8 +126,8 @@ coli_status coli_moe_check_config(const coli_moe_config *cfg);
 coli_status coli_moe_workspace_size(const coli_moe_config *cfg, int max_tokens, size_t *bytes);
 
 /* Number of kernels coli_moe_layer launches for T tokens with this configuration (1 on the fused
- * decode path: one persistent kernel for the whole layer; 7 on the tensor-core path; 5
- * otherwise).  Host only. */
+ * decode path: one persistent kernel for the whole layer; 7 on the tensor-core path; 8 over records
+ * in 4-bit containers; 5 otherwise).  Host only. */
 coli_status coli_moe_layer_kernels(const coli_moe_config *cfg, int T, int *n_kernels);
 
 /* Zeroes the workspace header: the device error word and the counters (asynchronous). */
@@ -348,6 +363,13 @@ typedef struct {
 coli_status coli_moe_fp4_product(int fmt, const coli_fp4_rows *a, const coli_fp4_mats *w, int k,
                                  const int32_t *offsets, int out_type, void *out, size_t ldo,
                                  void *ws, void *stream);
+
+/* Quantises one expert's matrices (device, act: coli_act; gate and up [I][H], down [H][I], rows without
+ * padding, 16-byte aligned) into a record of cfg's 4-bit container (256-byte aligned,
+ * coli_moe_record_bytes bytes).  COLI_ERR_UNSUPPORTED for the integer containers.  Two kernels. */
+coli_status coli_moe_fp4_pack_record(const coli_moe_config *cfg, int act, const void *wg,
+                                     const void *wu, const void *wd, uint8_t *record, void *ws,
+                                     void *stream);
 
 #ifdef __cplusplus
 }

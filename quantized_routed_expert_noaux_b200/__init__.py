@@ -24,8 +24,8 @@ __all__ = [
     "config_for", "weights_for",
     "MoERouter", "coli_moe_check_router", "coli_moe_route_scores",
     "FP4Rows", "FP4Mats", "coli_moe_fp4_scale_pitch", "coli_moe_fp4_scale_bytes", "coli_moe_fp4_quantize",
-    "coli_moe_fp4_dequantize", "coli_moe_fp4_product", "fp4_rows_for", "fp4_mats_for",
-    "COLI_SCORE_SIGMOID", "COLI_SCORE_SOFTMAX", "COLI_GROUP_TOP2", "COLI_GROUP_MAX",
+    "coli_moe_fp4_dequantize", "coli_moe_fp4_product", "coli_moe_fp4_pack_record", "fp4_rows_for", "fp4_mats_for",
+    "COLI_W_NVFP4", "COLI_W_MXFP4", "COLI_SCORE_SIGMOID", "COLI_SCORE_SOFTMAX", "COLI_GROUP_TOP2", "COLI_GROUP_MAX",
     "COLI_FP4_MX", "COLI_FP4_NV", "COLI_FP4_ROWS", "COLI_FP4_TILES",
     "COLI_W_INT2", "COLI_W_INT4", "COLI_W_INT8", "COLI_ACT_F32", "COLI_ACT_BF16",
 ]
@@ -33,6 +33,7 @@ __all__ = [
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libcoli_moe.so")
 
 COLI_W_INT2, COLI_W_INT4, COLI_W_INT8 = 2, 4, 8
+COLI_W_NVFP4, COLI_W_MXFP4 = 20, 36
 COLI_ACT_F32, COLI_ACT_BF16 = 0, 1
 COLI_SCORE_SIGMOID, COLI_SCORE_SOFTMAX = 0, 1
 COLI_GROUP_TOP2, COLI_GROUP_MAX = 0, 1
@@ -123,6 +124,7 @@ def _load():
     L.coli_moe_fp4_scale_bytes.argtypes = [I, I, I, I, C.POINTER(S)]
     L.coli_moe_fp4_quantize.argtypes = [I, I, I, P, I, S, P, I, I, I, P, P, P, P, P]
     L.coli_moe_fp4_dequantize.argtypes = [I, I, P, P, P, I, I, I, P, S, P]
+    L.coli_moe_fp4_pack_record.argtypes = [cfgp, I, P, P, P, P, P, P]
     L.coli_moe_fp4_product.argtypes = [I, C.POINTER(FP4Rows), C.POINTER(FP4Mats), I, P, I, P, S, P, P]
     L.coli_moe_layer_kernels.restype = I
     L.coli_moe_layer_noalloc.restype = I
@@ -132,7 +134,7 @@ def _load():
                  "coli_moe_residual", "coli_moe_debug_set_wait", "coli_moe_set_dispatch_threshold",
                  "coli_moe_noalloc_error_word", "coli_moe_check_router", "coli_moe_route_scores",
                  "coli_moe_fp4_scale_pitch", "coli_moe_fp4_scale_bytes", "coli_moe_fp4_quantize",
-                 "coli_moe_fp4_dequantize", "coli_moe_fp4_product"):
+                 "coli_moe_fp4_dequantize", "coli_moe_fp4_product", "coli_moe_fp4_pack_record"):
         getattr(L, name).restype = I
     return L
 
@@ -361,6 +363,12 @@ def coli_moe_fp4_product(fmt, a: FP4Rows, w: FP4Mats, k, offsets, out_type, out,
     _check("coli_moe_fp4_product", lib.coli_moe_fp4_product(
         fmt, C.byref(a), C.byref(w), k, _p(offsets), out_type, _p(out), ldo, _p(ws),
         _device_stream("coli_moe_fp4_product", stream, out)))
+
+
+def coli_moe_fp4_pack_record(cfg: MoEConfig, act, wg, wu, wd, record, ws, stream=None) -> None:
+    """One expert's gate, up [I, H] and down [H, I] matrices into a record of cfg's 4-bit container."""
+    _check("coli_moe_fp4_pack_record", lib.coli_moe_fp4_pack_record(
+        C.byref(cfg), act, _p(wg), _p(wu), _p(wd), _p(record), _p(ws), _device_stream("coli_moe_fp4_pack_record", stream, wg)))
 
 
 def fp4_rows_for(codes, scales, row_scale=None) -> FP4Rows:

@@ -43,6 +43,16 @@ int row_bytes(int n, int fmt) { return n * fmt / 8; }
 // Batches beyond decode size take the tensor-core grouped GEMM when its shape rules hold.
 static bool use_tc(const coli_moe_config *c, int T) { return T > TC_MIN_TOKENS && tc_shape_ok(*c); }
 
+// Tokens that the path without the grouped integer GEMM takes at most.  Records in 4-bit containers: the
+// tiles of the grouped products are counted in 32 bits, whatever the offsets hold.
+static int max_tokens(const coli_moe_config *c) {
+    if (!fp4_wfmt(c->wfmt)) return gemv_max_tokens(*c);
+    const long mb = (2L * c->inter > c->hidden ? 2L * c->inter : c->hidden) / 128 + 1;
+    const long slots = (0x7fffffffL / (mb * (c->n_experts + 2)) - 1) * 16;
+    const long t = slots / (c->top_k + c->n_shared);
+    return static_cast<int>(t < 0 ? 0 : (t > (1L << 25) ? (1L << 25) : t));
+}
+
 int device_sm_count() {
     static int cached[64] = {0};
     int dev = 0;
@@ -89,7 +99,7 @@ WsLayout ws_layout(const coli_moe_config &c, int T) {
     L.unique = o;   o = align256(o + E * 4);
     L.nuniq = o;    o = align256(o + 4);
     const size_t slots = n + static_cast<size_t>(T) * c.n_shared;
-    L.h = o;        o = align256(o + slots * c.inter * 4);
+    L.h = o;        o = align256(o + slots * c.inter * (fp4_wfmt(c.wfmt) ? 2 : 4));
     const bool tc = use_tc(&c, T);
     const size_t H = static_cast<size_t>(c.hidden), I = static_cast<size_t>(c.inter);
     L.xq = o;       o = align256(o + (tc ? 2 * slots * H : 0));
@@ -100,6 +110,16 @@ WsLayout ws_layout(const coli_moe_config &c, int T) {
     L.w_of = o;     o = align256(o + (tc ? slots * 4 : 0));
     L.chunks = o;   o = align256(o + (tc ? static_cast<size_t>(tc_max_chunks(c, T)) * 16 : 0));
     L.n_chunks = o; o = align256(o + (tc ? 4 : 0));
+    const bool f4 = fp4_wfmt(c.wfmt);
+    const int f = fp4_of(c.wfmt);
+    L.f_xc = o;     o = align256(o + (f4 ? slots * H / 2 : 0));
+    L.f_xs = o;     o = align256(o + (f4 ? slots * fp4_pitch(f, c.hidden) : 0));
+    L.f_xr = o;     o = align256(o + (f4 ? slots * 4 : 0));
+    L.f_hc = o;     o = align256(o + (f4 ? slots * I / 2 : 0));
+    L.f_hs = o;     o = align256(o + (f4 ? slots * fp4_pitch(f, c.inter) : 0));
+    L.f_hr = o;     o = align256(o + (f4 ? slots * 4 : 0));
+    L.f_y = o;      o = align256(o + (f4 ? slots * H * 2 : 0));
+    L.f_inv = o;    o = align256(o + (f4 ? n * 4 : 0));
     L.total = o;
     return L;
 }
@@ -143,10 +163,15 @@ coli_status coli_moe_debug_set_wait(long long wait_cycles, int unreachable) {
 
 coli_status coli_moe_record_bytes(int hidden, int inter, int wfmt, int group_size, size_t *bytes) {
     if (!bytes) return COLI_ERR_INVALID_ARG;
-    if (wfmt != COLI_W_INT4 && wfmt != COLI_W_INT8 && wfmt != COLI_W_INT2) return COLI_ERR_INVALID_ARG;
+    if (wfmt != COLI_W_INT4 && wfmt != COLI_W_INT8 && wfmt != COLI_W_INT2 && !fp4_wfmt(wfmt)) return COLI_ERR_INVALID_ARG;
     if (group_size != 0 && group_size != 64) return COLI_ERR_INVALID_ARG;
     if (group_size && wfmt != COLI_W_INT4) return COLI_ERR_UNSUPPORTED;
     if (hidden <= 0 || inter <= 0) return COLI_ERR_SHAPE;
+    if (fp4_wfmt(wfmt)) {
+        if (hidden % 64 || inter % 64) return COLI_ERR_SHAPE;
+        *bytes = fp4_record(hidden, inter, wfmt).bytes;
+        return COLI_OK;
+    }
     if ((static_cast<long>(hidden) * wfmt) % 8 || (static_cast<long>(inter) * wfmt) % 8) return COLI_ERR_SHAPE;
     if (group_size && (hidden % group_size || inter % group_size)) return COLI_ERR_SHAPE;
     const size_t rh = static_cast<size_t>(hidden) * wfmt / 8, ri = static_cast<size_t>(inter) * wfmt / 8;
@@ -158,7 +183,7 @@ coli_status coli_moe_record_bytes(int hidden, int inter, int wfmt, int group_siz
 
 coli_status coli_moe_check_config(const coli_moe_config *c) {
     if (!c) return COLI_ERR_INVALID_ARG;
-    if (c->wfmt != COLI_W_INT4 && c->wfmt != COLI_W_INT8 && c->wfmt != COLI_W_INT2) return COLI_ERR_INVALID_ARG;
+    if (c->wfmt != COLI_W_INT4 && c->wfmt != COLI_W_INT8 && c->wfmt != COLI_W_INT2 && !fp4_wfmt(c->wfmt)) return COLI_ERR_INVALID_ARG;
     if (c->act != COLI_ACT_F32 && c->act != COLI_ACT_BF16) return COLI_ERR_INVALID_ARG;
     if (c->group_size != 0 && c->group_size != 64) return COLI_ERR_INVALID_ARG;
     if (c->group_size && c->wfmt != COLI_W_INT4) return COLI_ERR_UNSUPPORTED;
@@ -175,6 +200,7 @@ coli_status coli_moe_check_config(const coli_moe_config *c) {
     if (c->n_shared > 1) return COLI_ERR_UNSUPPORTED;
     if (c->n_shared == 1 && c->shared_inter != c->inter) return COLI_ERR_UNSUPPORTED;
     if (c->hidden % 64 || c->inter % 64) return COLI_ERR_SHAPE;
+    if (fp4_wfmt(c->wfmt)) return COLI_OK;
     if (!gemv_shape_ok(row_bytes(c->hidden, c->wfmt)) || !gemv_shape_ok(row_bytes(c->inter, c->wfmt)))
         return COLI_ERR_UNSUPPORTED;
     return COLI_OK;
@@ -210,6 +236,10 @@ coli_status coli_moe_layer_kernels(const coli_moe_config *c, int T, int *n_kerne
     coli_status s = coli_moe_check_config(c);
     if (s != COLI_OK) return s;
     if (T < 0) return COLI_ERR_SHAPE;
+    if (fp4_wfmt(c->wfmt)) {
+        *n_kernels = T == 0 ? 0 : 8;
+        return COLI_OK;
+    }
     DecodePlan pl;
     *n_kernels = T == 0 ? 0 : (decode_plan(*c, T, &pl) ? 1 : (use_tc(c, T) ? (g_dispatch.load() > 0 ? 9 : 7) : 5));
     return COLI_OK;
@@ -321,6 +351,20 @@ static DecodeParams make_decode(const coli_moe_config *c, const FfnParams &f, ch
 // The expert half for a given routing: the fused decode kernel when the shape allows it, else
 // the general GEMV kernels.
 static coli_status run_ffn(const coli_moe_config *c, const FfnParams &p, char *base, cudaStream_t st) {
+    if (fp4_wfmt(c->wfmt)) {
+        const WsLayout L = ws_layout(*c, p.T);
+        Fp4Buffers b;
+        b.xc = reinterpret_cast<uint8_t *>(base + L.f_xc);
+        b.xs = reinterpret_cast<uint8_t *>(base + L.f_xs);
+        b.xr = reinterpret_cast<float *>(base + L.f_xr);
+        b.h = base + L.h;
+        b.hc = reinterpret_cast<uint8_t *>(base + L.f_hc);
+        b.hs = reinterpret_cast<uint8_t *>(base + L.f_hs);
+        b.hr = reinterpret_cast<float *>(base + L.f_hr);
+        b.y = base + L.f_y;
+        b.inverse = reinterpret_cast<int32_t *>(base + L.f_inv);
+        return from_cuda(launch_ffn_fp4(p, c->wfmt, b, st));
+    }
     if (use_tc(c, p.T)) {
         const WsLayout L = ws_layout(*c, p.T);
         TcBuffers b;
@@ -358,7 +402,7 @@ coli_status coli_moe_ffn(const coli_moe_config *c, const coli_moe_weights *w, co
     if (s != COLI_OK) return s;
     if (!x || !topk_w || !offsets || !perm || !unique_ids || !n_unique || !out) return COLI_ERR_INVALID_ARG;
     if (!aligned(x, 16) || !aligned(out, 16)) return COLI_ERR_ALIGN;
-    if (T > gemv_max_tokens(*c) && !use_tc(c, T)) return COLI_ERR_UNSUPPORTED;
+    if (T > max_tokens(c) && !use_tc(c, T)) return COLI_ERR_UNSUPPORTED;
     const WsLayout L = ws_layout(*c, T);
     if (!ws || !aligned(ws, 256) || ws_bytes < L.total) return COLI_ERR_WORKSPACE;
     char *base = static_cast<char *>(ws);
@@ -379,7 +423,7 @@ coli_status coli::layer_args_status(const coli_moe_config *c, const coli_moe_wei
     if (!aligned(x, 16) || !aligned(out, 16)) return COLI_ERR_ALIGN;
     if ((topk_ids_out && !aligned(topk_ids_out, 4)) || (topk_w_out && !aligned(topk_w_out, 4)))
         return COLI_ERR_ALIGN;
-    if (T > gemv_max_tokens(*c) && !use_tc(c, T)) return COLI_ERR_UNSUPPORTED;
+    if (T > max_tokens(c) && !use_tc(c, T)) return COLI_ERR_UNSUPPORTED;
     return COLI_OK;
 }
 
@@ -569,6 +613,44 @@ coli_status coli_moe_fp4_product(int fmt, const coli_fp4_rows *a, const coli_fp4
     p.ldo = ldo;
     p.err = static_cast<int *>(ws);
     return from_cuda(launch_fp4_product(fmt, p, static_cast<cudaStream_t>(stream)));
+}
+
+coli_status coli_moe_fp4_pack_record(const coli_moe_config *c, int act, const void *wg, const void *wu, const void *wd,
+                                     uint8_t *record, void *ws, void *stream) {
+    coli_status s = coli_moe_check_config(c);
+    if (s != COLI_OK) return s;
+    if (!fp4_wfmt(c->wfmt)) return COLI_ERR_UNSUPPORTED;
+    if (act != COLI_ACT_F32 && act != COLI_ACT_BF16) return COLI_ERR_INVALID_ARG;
+    if (!wg || !wu || !wd || !record) return COLI_ERR_INVALID_ARG;
+    if (!aligned(wg, 16) || !aligned(wu, 16) || !aligned(wd, 16) || !aligned(record, 256)) return COLI_ERR_ALIGN;
+    if (!ws || !aligned(ws, 256)) return COLI_ERR_WORKSPACE;
+    const int fmt = fp4_of(c->wfmt);
+    const Fp4Record r = fp4_record(c->hidden, c->inter, c->wfmt);
+    Fp4QuantArgs a;
+    a.row_index = nullptr;
+    a.n_index = 0;
+    a.row_div = 1;
+    a.inverse = nullptr;
+    a.err = static_cast<int *>(ws);
+    a.x = wg;
+    a.x_up = wu;
+    a.rows = a.src_rows = 2 * c->inter;
+    a.k = c->hidden;
+    a.ldx = static_cast<size_t>(c->hidden);
+    a.codes = record + r.w1;
+    a.scales = record + r.s1;
+    a.row_scale = fmt == COLI_FP4_NV ? reinterpret_cast<float *>(record + r.r1) : nullptr;
+    cudaError_t e = launch_fp4_quantize(fmt, COLI_FP4_TILES, act, a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return from_cuda(e);
+    a.x = wd;
+    a.x_up = nullptr;
+    a.rows = a.src_rows = c->hidden;
+    a.k = c->inter;
+    a.ldx = static_cast<size_t>(c->inter);
+    a.codes = record + r.wd;
+    a.scales = record + r.sd;
+    a.row_scale = fmt == COLI_FP4_NV ? reinterpret_cast<float *>(record + r.rd) : nullptr;
+    return from_cuda(launch_fp4_quantize(fmt, COLI_FP4_TILES, act, a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

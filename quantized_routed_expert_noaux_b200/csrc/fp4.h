@@ -23,6 +23,7 @@ __host__ __device__ constexpr size_t fp4_scale_bytes(int fmt, int layout, int ro
 
 struct Fp4QuantArgs {
     const void *x;
+    const void *x_up = nullptr; // packing a record: rows 32 j + 16 + i come from row 16 j + i of x_up, 32 j + i of x
     int src_rows;
     size_t ldx;                 // elements
     const int32_t *row_index;   // source row of output row r: row_index[r] / row_div (nullptr: r)
@@ -53,5 +54,39 @@ struct Fp4ProductArgs {
     int *err;
 };
 cudaError_t launch_fp4_product(int fmt, const Fp4ProductArgs &p, cudaStream_t st);
+
+// Records in 4-bit containers: byte offsets of the parts, and the record's bytes.
+struct Fp4Record {
+    size_t w1, wd, s1, sd, r1, rd, bytes;
+};
+inline bool fp4_wfmt(int wfmt) { return wfmt == COLI_W_MXFP4 || wfmt == COLI_W_NVFP4; }
+inline int fp4_of(int wfmt) { return wfmt == COLI_W_MXFP4 ? COLI_FP4_MX : COLI_FP4_NV; }
+inline Fp4Record fp4_record(int hidden, int inter, int wfmt) {
+    const size_t H = hidden, I = inter;
+    const int f = fp4_of(wfmt);
+    const bool rows = f == COLI_FP4_NV;
+    Fp4Record r;
+    r.w1 = 0;
+    r.wd = r.w1 + I * H;
+    r.s1 = r.wd + H * I / 2;
+    r.sd = r.s1 + fp4_scale_bytes(f, COLI_FP4_TILES, 2 * inter, hidden);
+    r.r1 = r.sd + fp4_scale_bytes(f, COLI_FP4_TILES, hidden, inter);
+    r.rd = r.r1 + (rows ? 2 * I * 4 : 0);
+    r.bytes = r.rd + (rows ? H * 4 : 0);
+    return r;
+}
+
+// The expert half over such records (fp4_ffn.cu): buffers of the workspace.
+struct Fp4Buffers {
+    uint8_t *xc, *xs;  // [slots]: x of each slot's token
+    float *xr;
+    void *h;           // [slots][I] bf16
+    uint8_t *hc, *hs;
+    float *hr;
+    void *y;           // [slots][H] bf16
+    int32_t *inverse;  // [T*K]: position of a slot in the grouped order
+};
+struct FfnParams;
+cudaError_t launch_ffn_fp4(const FfnParams &f, int wfmt, const Fp4Buffers &b, cudaStream_t st);
 
 }  // namespace coli

@@ -190,6 +190,17 @@ __device__ __forceinline__ int tile_list(const GemmArgs &p, int W, int MB, int *
     return carry;
 }
 
+// SiLU(gate) * up for rows i (gate lanes, 0-15) and 16 + i (up lanes) of a run of 32 rows: the lane
+// exchanges the sum it does not use with its partner's.  Rounded to bf16: h is quantised to 4 bits next,
+// whose steps are 32 times as wide at least.
+__device__ __forceinline__ __nv_bfloat16 swiglu_pair(const int *v, int i, bool gate, float rw, float rx) {
+    const float lo = __int_as_float(v[i]) * (rw * __shfl_sync(0xffffffffu, rx, i));
+    const float hi = __int_as_float(v[16 + i]) * (rw * __shfl_sync(0xffffffffu, rx, 16 + i));
+    const float other = __shfl_xor_sync(0xffffffffu, gate ? hi : lo, 16);
+    const float gv = gate ? lo : other, uv = gate ? other : hi;
+    return __float2bfloat16_rn(gv / (1.0f + expf(-gv)) * uv);
+}
+
 // A run of 32 rows x this warp's 32 weight rows: v holds the sums of weight row r, rx the row scale
 // of the run's row `lane`.
 template <int OUT>
@@ -197,17 +208,11 @@ __device__ __forceinline__ void store_run(const GemmArgs &p, const Tile &x, cons
     if (OUT == FP4_OUT_SWIGLU) {
         const bool gate = lane < 16;
         const int col = (r >> 5) * 16 + (lane & 15);
-        float d[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) d[j] = __int_as_float(v[j]) * (rw * __shfl_sync(0xffffffffu, rx, j));
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            // gate lanes take rows 0-15 of the run, up lanes rows 16-31
-            const float other = __shfl_xor_sync(0xffffffffu, gate ? d[16 + i] : d[i], 16);
-            const float gv = gate ? d[i] : other, uv = gate ? other : d[16 + i];
+            const __nv_bfloat16 h = swiglu_pair(v, i, gate, rw, rx);
             const int j = g + (gate ? i : 16 + i);
-            if (j < x.nr && r < p.n)
-                static_cast<__nv_bfloat16 *>(p.out)[static_cast<size_t>(x.n0 + j) * p.ldo + col] = __float2bfloat16_rn(gv / (1.0f + expf(-gv)) * uv);
+            if (j < x.nr && r < p.n) static_cast<__nv_bfloat16 *>(p.out)[static_cast<size_t>(x.n0 + j) * p.ldo + col] = h;
         }
     } else {
 #pragma unroll
@@ -526,16 +531,9 @@ __device__ __forceinline__ void staged_run(const GemmArgs &p, const Tile &x, con
         half_sync(half);                                  // the buffer's last run has been read
         if (OUT == FP4_OUT_SWIGLU) {
             const bool gate = lane < 16;
-            float d[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) d[j] = __int_as_float(v[j]) * (rw * __shfl_sync(0xffffffffu, rx, j));
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                // gate lanes take rows 0-15 of the run, up lanes rows 16-31
-                const float other = __shfl_xor_sync(0xffffffffu, gate ? d[16 + i] : d[i], 16);
-                const float gv = gate ? d[i] : other, uv = gate ? other : d[16 + i];
-                reinterpret_cast<__nv_bfloat16 *>(buf)[(gate ? i : 16 + i) * COLS + 16 * q + (lane & 15)] = __float2bfloat16_rn(gv / (1.0f + expf(-gv)) * uv);
-            }
+            for (int i = 0; i < 16; ++i)
+                reinterpret_cast<__nv_bfloat16 *>(buf)[(gate ? i : 16 + i) * COLS + 16 * q + (lane & 15)] = swiglu_pair(v, i, gate, rw, rx);
         } else {
 #pragma unroll
             for (int j = 0; j < RUN; ++j) {

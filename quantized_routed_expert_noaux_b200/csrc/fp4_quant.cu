@@ -153,7 +153,12 @@ __global__ void __launch_bounds__(QT) fp4_quant_kernel(const Fp4QuantArgs a, int
         }
     }
     const bool read = live && src >= 0;
-    const In *row = static_cast<const In *>(a.x) + static_cast<size_t>(read ? src : 0) * a.ldx;
+    const void *base = a.x;
+    if (a.x_up) {
+        if (r & 16) base = a.x_up;
+        src = (r >> 5) * 16 + (r & 15);
+    }
+    const In *row = static_cast<const In *>(base) + static_cast<size_t>(read ? src : 0) * a.ldx;
     // every lane takes the same number of rounds: neighbours exchange their halves of an MX block
     const int rounds = (n + TPR - 1) / TPR;
     Chunk<In> held[HOLD];
@@ -193,7 +198,7 @@ __global__ void __launch_bounds__(QT) fp4_quant_kernel(const Fp4QuantArgs a, int
             rinv = __uint_as_float((254u - e) << 23);
         }
     }
-    if (live && i0 == 0) a.row_scale[r] = rs;
+    if (live && i0 == 0 && a.row_scale) a.row_scale[r] = rs;
     auto put = [&](const Chunk<In> &c, int i) {
         uint32_t m = c.amax();
         if (FMT == COLI_FP4_MX) m = max(m, __shfl_xor_sync(FULL, m, 1));

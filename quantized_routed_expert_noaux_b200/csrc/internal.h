@@ -132,6 +132,8 @@ struct WsLayout {
     size_t h;        // [(T*K+T*S)][I] f32 intermediate
     // tensor-core path only (zero size otherwise)
     size_t xq, hq, sx, sh, tok_of, w_of, chunks, n_chunks;
+    // records in 4-bit containers only (zero size otherwise); h is theirs too, in bf16
+    size_t f_xc, f_xs, f_xr, f_hc, f_hs, f_hr, f_y, f_inv;
     size_t total;
 };
 
