@@ -12,6 +12,7 @@
 // a float32, so another y differs from it by a unit in its last place, and the quotient from m by
 // more than half a unit of its own.  So rounding the correctly rounded quotient to a code equals
 // rounding the real one; the same holds for (largest |x| / r) / 6 and e4m3.
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -26,11 +27,50 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int QT = 128;   // threads per CTA
 constexpr int HOLD = 4;   // chunks a thread keeps in registers
 
+// Two float32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// 32 bytes by one thread: whole sectors in one request (both at 32-byte boundaries).
+__device__ __forceinline__ void load32(const void *p, uint32_t (&w)[8]) {
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "l"(p));
+}
+__device__ __forceinline__ void store32(void *p, const uint32_t *w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+}
+
 // 16 elements in their own type
 template <typename In> struct Chunk;
 template <> struct Chunk<float> {
     float v[16];
-    __device__ __forceinline__ void load(const float *p) {
+    __device__ __forceinline__ void load(const float *p, bool wide) {
+        if (wide) {
+            uint32_t a[8], b[8];
+            load32(p, a);
+            load32(p + 8, b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = __uint_as_float(a[i]);
+                v[8 + i] = __uint_as_float(b[i]);
+            }
+            return;
+        }
         const float4 *q = reinterpret_cast<const float4 *>(p);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -50,10 +90,15 @@ template <> struct Chunk<float> {
         return m;
     }
     __device__ __forceinline__ float at(int i) const { return v[i]; }
+    __device__ __forceinline__ uint64_t negated(int i) const { return pack2(-v[2 * i], -v[2 * i + 1]); }  // elements 2 i, 2 i + 1
 };
 template <> struct Chunk<uint16_t> {
     uint32_t w[8];
-    __device__ __forceinline__ void load(const uint16_t *p) {
+    __device__ __forceinline__ void load(const uint16_t *p, bool wide) {
+        if (wide) {
+            load32(p, w);
+            return;
+        }
         const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p)), b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
         w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w; w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
     }
@@ -70,24 +115,49 @@ template <> struct Chunk<uint16_t> {
     __device__ __forceinline__ float at(int i) const {
         return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
     }
+    __device__ __forceinline__ uint64_t negated(int i) const {
+        const uint32_t n = w[i] ^ 0x80008000u;
+        return pack2(__uint_as_float(n << 16), __uint_as_float(n & 0xffff0000u));
+    }
 };
 
 constexpr uint32_t INF_BITS = 0x7f800000u;
 
-// two values -> two e2m1 codes, `lo` in the low nibble (round to nearest even, saturating at 6)
-__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+// eight values -> eight e2m1 codes, the first in the lowest nibble (round to nearest even, saturating at 6)
+__device__ __forceinline__ uint32_t e2m1x8(const float *v) {
     uint32_t r;
-    asm("{ .reg .b8 c; cvt.rn.satfinite.e2m1x2.f32 c, %1, %2; cvt.u32.u8 %0, c; }" : "=r"(r) : "f"(hi), "f"(lo));
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r) : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
     return r;
+}
+// the two codes of byte `i` of w as two halves
+template <int I>
+__device__ __forceinline__ float2 e2m1x2_values(uint32_t w) {
+    uint32_t h;
+    if (I == 0) asm("{ .reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %1; cvt.rn.f16x2.e2m1x2 %0, a; }" : "=r"(h) : "r"(w));
+    if (I == 1) asm("{ .reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %1; cvt.rn.f16x2.e2m1x2 %0, b; }" : "=r"(h) : "r"(w));
+    if (I == 2) asm("{ .reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %1; cvt.rn.f16x2.e2m1x2 %0, c; }" : "=r"(h) : "r"(w));
+    if (I == 3) asm("{ .reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %1; cvt.rn.f16x2.e2m1x2 %0, d; }" : "=r"(h) : "r"(w));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 __device__ __forceinline__ uint32_t e4m3(float v) {  // v >= 0
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(v));
     return r & 0xffu;
 }
-__device__ __forceinline__ float e4m3_value(uint32_t b) {  // sign bit clear
-    const uint32_t e = b >> 3, m = b & 7u;
-    return e ? __uint_as_float(((e + 120u) << 23) | (m << 20)) : static_cast<float>(m) * 0.001953125f;
+__device__ __forceinline__ float e4m3_value(uint32_t b) {  // sign bit clear; 0x7f is NaN
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(b)));
+    return __low2float(*reinterpret_cast<const __half2 *>(&h));
+}
+// The correctly rounded x / s from z, the correctly rounded 1 / s (Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990); signs placed so that -0 stays -0.
+__device__ __forceinline__ float quotient(float x, float s, float z) {
+    const float q = x * z;
+    return fmaf(-fmaf(q, s, -x), z, q);
 }
 
 __device__ __forceinline__ size_t scale_at(int layout, size_t pitch, int r, int j) {
@@ -95,37 +165,42 @@ __device__ __forceinline__ size_t scale_at(int layout, size_t pitch, int r, int 
                                    : static_cast<size_t>(r >> 7) * 128 * pitch + static_cast<size_t>(j >> 2) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4 + (j & 3);
 }
 
-// One chunk: its block scale and codes.  `m`: bits of the block's largest magnitude; `rinv`: 1 / row
-// scale (NV).
+// One chunk: its block scale and codes.  `m`: bits of the block's largest magnitude; `rs`, `rinv`: the
+// row scale and its inverse (NV).
 template <int FMT, typename In>
-__device__ __forceinline__ void encode(const Chunk<In> &c, uint32_t m, float rinv, uint2 &codes, uint32_t &scale) {
+__device__ __forceinline__ void encode(const Chunk<In> &c, uint32_t m, float rs, float rinv, uint2 &codes, uint32_t &scale) {
     codes = make_uint2(0u, 0u);
     if (m >= INF_BITS) {  // a NaN or an infinity
         scale = FMT == COLI_FP4_MX ? 0xffu : 0x7fu;
         return;
     }
-    uint32_t w[2] = {0u, 0u};
+    float v[16];
     if (FMT == COLI_FP4_MX) {
         const int e = max(static_cast<int>(m >> 23) - 2, 0);
         scale = e;
         const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i >> 2] |= e2m1x2(c.at(2 * i) * inv, c.at(2 * i + 1) * inv) << (8 * (i & 3));
+        for (int i = 0; i < 16; ++i) v[i] = c.at(i) * inv;
     } else {
-        scale = e4m3(__fdiv_rn(__uint_as_float(m) * rinv, 6.0f));
+        scale = e4m3(quotient(__uint_as_float(m) * rinv, 6.0f, 1.0f / 6.0f));
         if (scale == 0u) return;
-        const float s = e4m3_value(scale);
-        const float z = __frcp_rn(s);
-        // the correctly rounded y / s from the correctly rounded 1 / s (Markstein, "Computation of
-        // elementary functions on the IBM RISC System/6000 processor", 1990)
-        auto quotient = [&](float x) {
-            const float y = x * rinv, q = y * z;
-            return fmaf(-fmaf(q, s, -y), z, q);  // (signs placed so that -0 stays -0)
-        };
+        const float s = e4m3_value(scale), z = __frcp_rn(s);
+        if (rinv > 1e-30f && rinv < 1e30f) {
+            // x / (r s): r is a power of two, so r s and 1 / (r s) are as exact as s and 1 / s
+            const float sr = s * rs, zr = z * rinv;
+            // two quotients at a time, from -x (the packed operations have no negated operand)
+            const uint64_t s2 = pack2(sr, sr), z2 = pack2(-zr, -zr);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i >> 2] |= e2m1x2(quotient(c.at(2 * i)), quotient(c.at(2 * i + 1))) << (8 * (i & 3));
+            for (int i = 0; i < 8; ++i) {
+                const uint64_t y = c.negated(i), q = mul2(y, z2);
+                unpack2(fma2(fma2(q, s2, y), z2, q), v[2 * i], v[2 * i + 1]);
+            }
+        } else {  // rows so large or small that r s or 1 / (r s) could leave float32's range
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = quotient(c.at(i) * rinv, s, z);
+        }
     }
-    codes = make_uint2(w[0], w[1]);
+    codes = make_uint2(e2m1x8(v), e2m1x8(v + 8));
 }
 
 // TPR threads per row, QT / TPR rows per CTA.
@@ -159,28 +234,32 @@ __global__ void __launch_bounds__(QT) fp4_quant_kernel(const Fp4QuantArgs a, int
         src = (r >> 5) * 16 + (r & 15);
     }
     const In *row = static_cast<const In *>(base) + static_cast<size_t>(read ? src : 0) * a.ldx;
+    const bool wide = ((reinterpret_cast<uintptr_t>(base) | a.ldx * sizeof(In)) & 31) == 0;
     // every lane takes the same number of rounds: neighbours exchange their halves of an MX block
     const int rounds = (n + TPR - 1) / TPR;
     Chunk<In> held[HOLD];
+    uint32_t most[HOLD];  // bits of their largest magnitudes
 #pragma unroll
     for (int h = 0; h < HOLD; ++h) {
         const int i = i0 + h * TPR;
-        if (read && i < n) held[h].load(row + 16 * static_cast<size_t>(i));
+        if (h >= rounds) break;
+        if (read && i < n) held[h].load(row + 16 * static_cast<size_t>(i), wide);
         else held[h].zero();
     }
     float rinv = 1.f, rs = 1.f;
     if (FMT == COLI_FP4_NV) {
         uint32_t top = 0u;
 #pragma unroll
-        for (int h = 0; h < HOLD; ++h) {
-            const uint32_t m = held[h].amax();
-            if (m < INF_BITS) top = max(top, m);
-        }
+        for (int h = 0; h < HOLD; ++h)
+            if (h < rounds) {
+                most[h] = held[h].amax();
+                if (most[h] < INF_BITS) top = max(top, most[h]);
+            }
         for (int h = HOLD; h < rounds; ++h) {
             const int i = i0 + h * TPR;
             if (read && i < n) {
                 Chunk<In> c;
-                c.load(row + 16 * static_cast<size_t>(i));
+                c.load(row + 16 * static_cast<size_t>(i), wide);
                 const uint32_t m = c.amax();
                 if (m < INF_BITS) top = max(top, m);
             }
@@ -199,26 +278,28 @@ __global__ void __launch_bounds__(QT) fp4_quant_kernel(const Fp4QuantArgs a, int
         }
     }
     if (live && i0 == 0 && a.row_scale) a.row_scale[r] = rs;
-    auto put = [&](const Chunk<In> &c, int i) {
-        uint32_t m = c.amax();
-        if (FMT == COLI_FP4_MX) m = max(m, __shfl_xor_sync(FULL, m, 1));
+    auto put = [&](const Chunk<In> &c, uint32_t m, int i) {
+        if (FMT == COLI_FP4_MX) {
+            m = c.amax();
+            m = max(m, __shfl_xor_sync(FULL, m, 1));
+        }
         if (!live || i >= n) return;
         uint2 codes;
         uint32_t scale;
-        encode<FMT, In>(c, m, rinv, codes, scale);
+        encode<FMT, In>(c, m, rs, rinv, codes, scale);
         *reinterpret_cast<uint2 *>(a.codes + static_cast<size_t>(r) * (a.k / 2) + 8 * static_cast<size_t>(i)) = codes;
         if (FMT == COLI_FP4_NV) a.scales[scale_at(layout, pitch, r, i)] = static_cast<uint8_t>(scale);
         else if (!(i & 1)) a.scales[scale_at(layout, pitch, r, i >> 1)] = static_cast<uint8_t>(scale);
     };
 #pragma unroll
     for (int h = 0; h < HOLD; ++h)
-        if (h < rounds) put(held[h], i0 + h * TPR);
+        if (h < rounds) put(held[h], most[h], i0 + h * TPR);
     for (int h = HOLD; h < rounds; ++h) {
         const int i = i0 + h * TPR;
         Chunk<In> c;
-        if (read && i < n) c.load(row + 16 * static_cast<size_t>(i));
+        if (read && i < n) c.load(row + 16 * static_cast<size_t>(i), wide);
         else c.zero();
-        put(c, i);
+        put(c, FMT == COLI_FP4_NV ? c.amax() : 0u, i);
     }
     // bytes behind the row's last block, and the rows that fill up the last tile
     if (r < out_rows)
@@ -227,50 +308,64 @@ __global__ void __launch_bounds__(QT) fp4_quant_kernel(const Fp4QuantArgs a, int
 }
 
 template <typename Out>
-__device__ __forceinline__ void store16(Out *p, const float *v);
+__device__ __forceinline__ void store16(Out *p, const float *v, bool wide);
 template <>
-__device__ __forceinline__ void store16<float>(float *p, const float *v) {
+__device__ __forceinline__ void store16<float>(float *p, const float *v, bool wide) {
+    if (wide) {
+        store32(p, reinterpret_cast<const uint32_t *>(v));
+        store32(p + 8, reinterpret_cast<const uint32_t *>(v + 8));
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) reinterpret_cast<float4 *>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
 }
 template <>
-__device__ __forceinline__ void store16<uint16_t>(uint16_t *p, const float *v) {
+__device__ __forceinline__ void store16<uint16_t>(uint16_t *p, const float *v, bool wide) {
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
         w[i] = *reinterpret_cast<const uint32_t *>(&b);
     }
+    if (wide) {
+        store32(p, w);
+        return;
+    }
     reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
     reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-// code 0..15 -> value: e2m1 magnitude from its bits (exponent 0: 0 or 0.5)
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-    const uint32_t e = (c >> 1) & 3u, m = c & 1u;
-    const uint32_t b = e ? ((e + 126u) << 23) | (m << 22) : (m ? 0x3f000000u : 0u);
-    return __uint_as_float(b | (c >> 3 << 31));
-}
-
-template <int FMT, typename Out>
+// TPR threads per row, QT / TPR rows per CTA at a time.
+template <int FMT, int TPR, typename Out>
 __global__ void __launch_bounds__(QT) fp4_dequant_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
                                                          const float *__restrict__ row_scale, int layout, int rows, int k,
                                                          Out *__restrict__ out, size_t ldo) {
     const int n = k / 16;
     const size_t pitch = fp4_pitch(FMT, k);
-    const size_t total = static_cast<size_t>(rows) * n;
-    for (size_t at = static_cast<size_t>(blockIdx.x) * QT + threadIdx.x; at < total; at += static_cast<size_t>(gridDim.x) * QT) {
-        const int r = static_cast<int>(at / n), i = static_cast<int>(at % n);
-        const uint2 c = __ldg(reinterpret_cast<const uint2 *>(codes) + at);
-        const uint32_t b = scales[scale_at(layout, pitch, r, FMT == COLI_FP4_NV ? i : i >> 1)];
-        float s;
-        if (FMT == COLI_FP4_MX) s = __uint_as_float(b == 0xffu ? 0x7fc00000u : (b ? b << 23 : 0x00400000u));
-        else s = (b & 0x7fu) == 0x7fu ? __uint_as_float(0x7fc00000u) : e4m3_value(b & 0x7fu);
+    const bool wide = ((reinterpret_cast<uintptr_t>(out) | ldo * sizeof(Out)) & 31) == 0;
+    for (int r = blockIdx.x * (QT / TPR) + threadIdx.x / TPR; r < rows; r += gridDim.x * (QT / TPR)) {
         const float rs = row_scale ? __ldg(row_scale + r) : 1.f;
-        float v[16];
+        const uint2 *row = reinterpret_cast<const uint2 *>(codes) + static_cast<size_t>(r) * n;
+        Out *o = out + static_cast<size_t>(r) * ldo;
+        for (int i = threadIdx.x % TPR; i < n; i += TPR) {
+            const uint2 c = __ldg(row + i);
+            const uint32_t b = __ldg(scales + scale_at(layout, pitch, r, FMT == COLI_FP4_NV ? i : i >> 1));
+            float s;
+            if (FMT == COLI_FP4_MX) s = __uint_as_float(b == 0xffu ? 0x7fc00000u : (b ? b << 23 : 0x00400000u));
+            else s = e4m3_value(b & 0x7fu);
+            float v[16];
+            auto four = [&](uint32_t w, float *d) {
+                const float2 e[4] = {e2m1x2_values<0>(w), e2m1x2_values<1>(w), e2m1x2_values<2>(w), e2m1x2_values<3>(w)};
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = e2m1_value(((j < 8 ? c.x : c.y) >> (4 * (j & 7))) & 15u) * s * rs;
-        store16<Out>(out + static_cast<size_t>(r) * ldo + 16 * static_cast<size_t>(i), v);
+                for (int j = 0; j < 4; ++j) {  // code * block scale is exact: one rounding, by the row scale
+                    d[2 * j] = e[j].x * s * rs;
+                    d[2 * j + 1] = e[j].y * s * rs;
+                }
+            };
+            four(c.x, v);
+            four(c.y, v + 8);
+            store16<Out>(o + 16 * static_cast<size_t>(i), v, wide);
+        }
     }
 }
 
@@ -285,6 +380,25 @@ cudaError_t launch_quant(int layout, const Fp4QuantArgs &a, cudaStream_t st) {
     return cudaGetLastError();
 }
 
+template <int FMT, int TPR>
+void launch_dequant_tpr(int layout, const uint8_t *codes, const uint8_t *scales, const float *row_scale, int rows, int k, int act,
+                        void *out, size_t ldo, cudaStream_t st) {
+    const int want = (rows + QT / TPR - 1) / (QT / TPR), most = device_sm_count() * 64;
+    const int grid = want < most ? want : most;
+    if (act == COLI_ACT_F32)
+        fp4_dequant_kernel<FMT, TPR, float><<<grid, QT, 0, st>>>(codes, scales, row_scale, layout, rows, k, static_cast<float *>(out), ldo);
+    else
+        fp4_dequant_kernel<FMT, TPR, uint16_t><<<grid, QT, 0, st>>>(codes, scales, row_scale, layout, rows, k, static_cast<uint16_t *>(out), ldo);
+}
+
+template <int FMT>
+cudaError_t launch_dequant(int layout, const uint8_t *codes, const uint8_t *scales, const float *row_scale, int rows, int k, int act,
+                           void *out, size_t ldo, cudaStream_t st) {
+    if (k <= 1024) launch_dequant_tpr<FMT, 32>(layout, codes, scales, row_scale, rows, k, act, out, ldo, st);
+    else launch_dequant_tpr<FMT, QT>(layout, codes, scales, row_scale, rows, k, act, out, ldo, st);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_fp4_quantize(int fmt, int layout, int act, const Fp4QuantArgs &a, cudaStream_t st) {
@@ -295,17 +409,8 @@ cudaError_t launch_fp4_quantize(int fmt, int layout, int act, const Fp4QuantArgs
 
 cudaError_t launch_fp4_dequantize(int fmt, int layout, const uint8_t *codes, const uint8_t *scales, const float *row_scale,
                                   int rows, int k, int act, void *out, size_t ldo, cudaStream_t st) {
-    const size_t total = static_cast<size_t>(rows) * (k / 16);
-    const size_t want = (total + QT - 1) / QT, most = static_cast<size_t>(device_sm_count()) * 16 * 4;
-    const int grid = static_cast<int>(want < most ? want : most);
-    if (fmt == COLI_FP4_MX) {
-        if (act == COLI_ACT_F32) fp4_dequant_kernel<COLI_FP4_MX, float><<<grid, QT, 0, st>>>(codes, scales, row_scale, layout, rows, k, static_cast<float *>(out), ldo);
-        else fp4_dequant_kernel<COLI_FP4_MX, uint16_t><<<grid, QT, 0, st>>>(codes, scales, row_scale, layout, rows, k, static_cast<uint16_t *>(out), ldo);
-    } else {
-        if (act == COLI_ACT_F32) fp4_dequant_kernel<COLI_FP4_NV, float><<<grid, QT, 0, st>>>(codes, scales, row_scale, layout, rows, k, static_cast<float *>(out), ldo);
-        else fp4_dequant_kernel<COLI_FP4_NV, uint16_t><<<grid, QT, 0, st>>>(codes, scales, row_scale, layout, rows, k, static_cast<uint16_t *>(out), ldo);
-    }
-    return cudaGetLastError();
+    return fmt == COLI_FP4_MX ? launch_dequant<COLI_FP4_MX>(layout, codes, scales, row_scale, rows, k, act, out, ldo, st)
+                              : launch_dequant<COLI_FP4_NV>(layout, codes, scales, row_scale, rows, k, act, out, ldo, st);
 }
 
 }  // namespace coli

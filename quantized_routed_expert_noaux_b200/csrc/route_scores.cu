@@ -51,12 +51,40 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t v) {
     return (static_cast<uint64_t>(mh) << 32) | ml;
 }
 
+__device__ __forceinline__ float load_one(const float *p) { return __ldg(p); }
+__device__ __forceinline__ float load_one(const uint16_t *p) { return __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16); }
+template <int N>
+__device__ __forceinline__ void load_run(const float *p, float (&d)[N]) {
+#pragma unroll
+    for (int i = 0; i + 4 <= N; i += 4) {
+        const float4 f = __ldg(reinterpret_cast<const float4 *>(p + i));
+        d[i] = f.x; d[i + 1] = f.y; d[i + 2] = f.z; d[i + 3] = f.w;
+    }
+}
+template <int N>
+__device__ __forceinline__ void load_run(const uint16_t *p, float (&d)[N]) {
+#pragma unroll
+    for (int i = 0; i + 8 <= N; i += 8) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p + i));
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            d[i + 2 * j] = __uint_as_float(w[j] << 16);
+            d[i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        }
+    }
+}
+
 struct RouteArgs {
     const void *logits;
     size_t ld;
     const float *bias;
     int T, E, K, G, TG;
     int softmax, group_max, renorm;
+    int fast;  // the groups are whole runs of lanes, 1 << seg_shift each
+    int gs, seg_shift;
+    float inv_gs;
+    int vec;   // rows (and the bias) allow 16-byte loads of a lane's experts
     float scaling;
     int32_t *ids;
     float *w;
@@ -78,40 +106,28 @@ __device__ __forceinline__ uint64_t shfl_xor<uint64_t>(uint64_t v, int o) {
     return __shfl_xor_sync(FULL, static_cast<unsigned long long>(v), o);
 }
 
-template <int VPL, bool BIAS, typename In>
-__global__ void __launch_bounds__(ROUTE_WARPS * 32) route_scores_kernel(const RouteArgs a) {
+// exp(l - top); the largest logit (+inf too) gives 1
+__device__ __forceinline__ double exp_above(float l, float top) { return l == top ? 1.0 : exp(static_cast<double>(l) - static_cast<double>(top)); }
+__device__ __forceinline__ float expf_above(float l, float top) { return l == top ? 1.0f : expf(l - top); }
+
+// A token's choice, compared exactly (64-bit keys of double scores with a bias, 32-bit keys of the logits
+// without).  Lane k gets the expert of slot k in my_id; `chosen` of the K were there to choose.
+template <int VPL, bool BIAS>
+__device__ __forceinline__ void choose_exact(const RouteArgs &a, const float (&l)[VPL], int e0, int lane, int &my_id, int &chosen, float &top, double &sum) {
     using Key = typename std::conditional<BIAS, uint64_t, uint32_t>::type;
-    const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x * ROUTE_WARPS + (threadIdx.x >> 5);
-    if (t >= a.T) return;
-    const In *row = static_cast<const In *>(a.logits) + static_cast<size_t>(t) * a.ld;
-    const int e0 = lane * VPL;
-    float l[VPL];
-#pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-        float x = -INFINITY;
-        if (e0 + v < a.E) {
-            if (sizeof(In) == 4) x = __ldg(reinterpret_cast<const float *>(row) + e0 + v);
-            else x = __uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t *>(row) + e0 + v)) << 16);
-        }
-        l[v] = x > -INFINITY ? x : -INFINITY;  // NaN masks as -inf does
-    }
+    top = -INFINITY;
+    sum = 1.0;
     // softmax: the row's maximum and float32 or double sum (double where biased scores are compared)
-    float top = -INFINITY;
-    double sum = 1.0;
     if (a.softmax) {
 #pragma unroll
         for (int v = 0; v < VPL; ++v) top = fmaxf(top, l[v]);
         top = unkey32(warp_max(key32(top)));  // NaN when every expert is masked: nothing is read from it then
     }
-    // exp(l - top); the largest logit (+inf too) gives 1
-    auto expd = [&](float x) { return x == top ? 1.0 : exp(static_cast<double>(x) - static_cast<double>(top)); };
-    auto expf_ = [&](float x) { return x == top ? 1.0f : expf(x - top); };
     Key key[VPL];
     if (BIAS) {
         double s[VPL];
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) s[v] = l[v] == -INFINITY ? 0.0 : (a.softmax ? expd(l[v]) : sigmoid(l[v]));
+        for (int v = 0; v < VPL; ++v) s[v] = l[v] == -INFINITY ? 0.0 : (a.softmax ? exp_above(l[v], top) : sigmoid(l[v]));
         if (a.softmax) {
             sum = 0.0;
 #pragma unroll
@@ -129,7 +145,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_scores_kernel(const Ro
         if (a.softmax && !a.renorm) {
             float fs = 0.f;
 #pragma unroll
-            for (int v = 0; v < VPL; ++v) fs += l[v] == -INFINITY ? 0.f : expf_(l[v]);
+            for (int v = 0; v < VPL; ++v) fs += l[v] == -INFINITY ? 0.f : expf_above(l[v], top);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) fs += __shfl_xor_sync(FULL, fs, o);
             sum = static_cast<double>(fs);
@@ -139,7 +155,8 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_scores_kernel(const Ro
     }
     // ---- groups: drop the keys of those that are not kept
     if (a.TG < a.G) {
-        const int gs = a.E / a.G;
+        // the group of expert e < 1024: e + 1/2 is further than a rounding from a multiple of gs
+        auto group_of = [&](int e) { return static_cast<int>((static_cast<float>(e) + 0.5f) * a.inv_gs); };
         // what a group with the keys b1 >= b2 is ranked by, as a 64-bit key (0: nothing to choose)
         auto rank_of = [&](Key b1, Key b2) -> uint64_t {
             if (b1 == 0) return 0ull;
@@ -149,18 +166,18 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_scores_kernel(const Ro
                 r = unkey64(b1) + (b2 ? unkey64(b2) : 0.0);
             } else {
                 const float f1 = unkey32(static_cast<uint32_t>(b1));
-                r = a.softmax ? expd(f1) : sigmoid(f1);
+                r = a.softmax ? exp_above(f1, top) : sigmoid(f1);
                 if (b2) {
                     const float f2 = unkey32(static_cast<uint32_t>(b2));
-                    r += a.softmax ? expd(f2) : sigmoid(f2);
+                    r += a.softmax ? exp_above(f2, top) : sigmoid(f2);
                 }
             }
             return key64(r);
         };
         uint32_t kept = 0u;
         uint64_t mine = 0ull;  // rank of group `lane`
-        const int seg = gs / VPL;  // lanes of a group
-        if (gs % VPL == 0 && (seg & (seg - 1)) == 0) {
+        if (a.fast) {
+            const int seg = 1 << a.seg_shift;  // lanes of a group
             Key b1 = 0, b2 = 0;
 #pragma unroll
             for (int v = 0; v < VPL; ++v) merge2<Key>(b1, b2, key[v], Key(0));
@@ -176,7 +193,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_scores_kernel(const Ro
                 Key b1 = 0, b2 = 0;
 #pragma unroll
                 for (int v = 0; v < VPL; ++v)
-                    if ((e0 + v) / gs == g) merge2<Key>(b1, b2, key[v], Key(0));
+                    if (group_of(e0 + v) == g) merge2<Key>(b1, b2, key[v], Key(0));
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const Key c1 = shfl_xor<Key>(b1, o), c2 = shfl_xor<Key>(b2, o);
@@ -195,42 +212,214 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_scores_kernel(const Ro
         kept = __ballot_sync(FULL, lane < a.G && before < a.TG);
 #pragma unroll
         for (int v = 0; v < VPL; ++v)
-            if (e0 + v < a.E && !((kept >> ((e0 + v) / gs)) & 1u)) key[v] = 0;
+            if (e0 + v < a.E && !((kept >> group_of(e0 + v)) & 1u)) key[v] = 0;
     }
     // ---- K picks; lane k keeps the expert of slot k
-    int my_id = -1;
+    my_id = -1;
     uint32_t taken = 0u;  // of this lane's experts (VPL <= 32)
     int n = 0;
     for (; n < a.K; ++n) {
         Key best = 0;
-        int at = 0;
 #pragma unroll
-        for (int v = 0; v < VPL; ++v)
-            if (key[v] > best) { best = key[v]; at = v; }
+        for (int v = 0; v < VPL; ++v) best = key[v] > best ? key[v] : best;
         const Key m = warp_max(best);
         if (m == 0) break;
-        const int id = __reduce_min_sync(FULL, best == m ? static_cast<unsigned>(e0 + at) : 0xffffffffu);
-        if (id / VPL == lane) {
-            taken |= 1u << (id % VPL);
+        // lanes hold runs of experts: the lowest lane, and its lowest place, has the lowest id
+        const int owner = __ffs(__ballot_sync(FULL, best == m)) - 1;
+        int at = 0;
+        if (lane == owner) {
+#pragma unroll
+            for (int v = VPL - 1; v >= 0; --v)
+                if (key[v] == m) at = v;
 #pragma unroll
             for (int v = 0; v < VPL; ++v)
-                if (v == id % VPL) key[v] = 0;
+                if (v == at) key[v] = 0;
+            taken |= 1u << at;
         }
+        const int id = __shfl_sync(FULL, e0 + at, owner);
         if (lane == n) my_id = id;
     }
-    const int chosen = n;
+    chosen = n;
     for (; n < a.K; ++n) {  // too few: the lowest ids that are left
         unsigned low = 0xffffffffu;
 #pragma unroll
         for (int v = VPL - 1; v >= 0; --v)
             if (e0 + v < a.E && !((taken >> v) & 1u)) low = e0 + v;
         const int id = __reduce_min_sync(FULL, low);
-        if (id / VPL == lane) taken |= 1u << (id % VPL);
+        if (id / VPL == lane) taken |= 1u << (id % VPL);  // (VPL is a power of two)
         if (lane == n) my_id = id;
     }
+}
+
+// Descending order of a lane's keys (Batcher's odd-even merge sort; VPL a power of two).
+template <int VPL>
+__device__ __forceinline__ void sort_keys(uint32_t (&k)[VPL]) {
+#pragma unroll
+    for (int p = 1; p < VPL; p *= 2)
+#pragma unroll
+        for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+            for (int j = q % p; j + q < VPL; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (i + j + q < VPL && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                        const uint32_t hi = max(k[i + j], k[i + j + q]), lo = min(k[i + j], k[i + j + q]);
+                        k[i + j] = hi;
+                        k[i + j + q] = lo;
+                    }
+}
+
+// The same choice in float32 where its errors cannot change it: false where two values that are compared
+// lie too close (with random float32 logits about one token in a hundred), or fewer than K can be chosen.
+// The place of an expert among its lane's is kept in the last bits of its key, VPL - 1 - place, so a
+// lane's keys can be sorted; a pick is then one redux.sync of the first keys and a shift in one lane.
+// Errors in units of 2^-24.  With a bias: sigmoid, __expf's (2 + 1.17 |l|) 2^-23 of exp(-l), of which s takes
+// s (1 - s), and the division's 2^-22 make 8; softmax, expf's 4, its argument's rounding 1, a sum of VPL
+// terms per lane and 5 rounds VPL + 5 of s; the sum with the bias 1 of c.  The place costs 2 VPL units of |c|, or
+// of |l| without a bias; of bf16 logits it takes bits that are zero, and equal logits come in the order of
+// their ids.  Groups by two scores without a bias: the scores' errors alone.
+template <int VPL, bool BIAS, typename In>
+__device__ __forceinline__ bool choose_fast(const RouteArgs &a, const float (&l)[VPL], int e0, int lane, int &my_id, float &top, double &sum) {
+    constexpr bool EXACT = !BIAS && sizeof(In) == 2;
+    constexpr float UNIT = 5.9604644775390625e-8f;  // 2^-24
+    const bool groups = a.TG < a.G, top2 = groups && !a.group_max;
+    float c[VPL], most = 0.f, smax = 1.f;
+    if (a.softmax) {
+        top = l[0];
+#pragma unroll
+        for (int v = 1; v < VPL; ++v) top = fmaxf(top, l[v]);
+        top = unkey32(warp_max(key32(top)));
+        if (!(fabsf(top) < INFINITY)) return false;  // +inf, or every expert masked
+    }
+    if (a.softmax && (BIAS || !a.renorm || top2)) {
+        float fs = 0.f;
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            c[v] = expf(l[v] - top);
+            fs += c[v];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) fs += __shfl_xor_sync(FULL, fs, o);
+        sum = static_cast<double>(fs);
+        smax = 1.0f / fs;
+    } else if (!a.softmax && (BIAS || top2)) {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) c[v] = __fdividef(1.0f, 1.0f + __expf(-fmaxf(l[v], -60.0f)));
+    }
+    if (BIAS) {
+        float bias[VPL];
+        if (VPL >= 4 && a.vec) {
+            load_run<VPL>(a.bias + e0, bias);
+        } else {
+#pragma unroll
+            for (int v = 0; v < VPL; ++v) bias[v] = __ldg(a.bias + min(e0 + v, a.E - 1));
+        }
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            const float f = (a.softmax ? c[v] * smax : c[v]) + bias[v];  // (l is -inf behind the last expert)
+            c[v] = l[v] > -INFINITY && f > -INFINITY ? f : -INFINITY;
+        }
+    }
+    auto value = [&](int v) { return BIAS ? c[v] : l[v]; };
+    if (!EXACT) {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) most = fmaxf(most, value(v) > -INFINITY ? fabsf(value(v)) : 0.f);
+        most = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(most)));
+    }
+    const float tol = UNIT * ((BIAS ? (VPL + 16) * (smax + most) : 0.f) + 2 * VPL * most);
+    bool mine = true;  // this lane's experts are of a group that is kept
+    if (groups) {
+        // a group's lanes: 1 << seg_shift of them (the launcher's rule)
+        float b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            const float f = BIAS || !top2 ? value(v) : (l[v] > -INFINITY ? c[v] : -INFINITY);
+            b2 = fmaxf(b2, fminf(b1, f));
+            b1 = fmaxf(b1, f);
+        }
+        for (int o = 1; o < (1 << a.seg_shift); o <<= 1) {
+            const float c1 = __shfl_xor_sync(FULL, b1, o), c2 = __shfl_xor_sync(FULL, b2, o);
+            b2 = fmaxf(fmaxf(b2, c2), fminf(b1, c1));
+            b1 = fmaxf(b1, c1);
+        }
+        const int g = lane >> a.seg_shift;
+        const float r = g >= a.G ? -INFINITY : (top2 && b2 > -INFINITY ? b1 + b2 : b1);
+        // sums of softmax numerators: relative to the largest, 1
+        const float gtol = BIAS ? 4.0f * tol : (top2 ? 4.0f * UNIT * (VPL + 16) : 0.f);
+        int above = 0, near = 0;  // groups certainly before this one; groups too close to tell
+        for (int o = 0; o < a.G; ++o) {
+            const float q = __shfl_sync(FULL, r, o << a.seg_shift);
+            above += q > r + gtol;
+            near += o != g && fabsf(q - r) <= gtol;
+            if (!BIAS && !top2) {  // the logits themselves: ties go to the lower group
+                above += q == r && o < g;
+                near = 0;
+            }
+        }
+        mine = above + near < a.TG;
+        // a close group that could push this one across the border, or a kept group without an expert
+        // to choose: leave the token to the exact choice
+        if (__any_sync(FULL, g < a.G && ((near > 0 && above < a.TG && !mine) || (mine && r == -INFINITY)))) return false;
+    }
+    uint32_t key[VPL];
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+        key[v] = mine && value(v) > -INFINITY ? (key32(value(v)) & ~static_cast<uint32_t>(VPL - 1)) | static_cast<uint32_t>(VPL - 1 - v) : 0u;
+    sort_keys<VPL>(key);
+    uint32_t got = 0u;  // lane n: key of pick n
+    my_id = -1;
+    for (int n = 0; n < a.K; ++n) {
+        const uint32_t m = __reduce_max_sync(FULL, key[0]);
+        // (equal logits: the lowest lane has the lowest id, whatever the place in the key says)
+        constexpr uint32_t SAME = EXACT ? ~static_cast<uint32_t>(VPL - 1) : FULL;
+        const int owner = __ffs(__ballot_sync(FULL, (key[0] & SAME) == (m & SAME))) - 1;
+        const uint32_t k = EXACT ? __shfl_sync(FULL, key[0], owner) : m;
+        if (lane == n) {
+            got = k;
+            my_id = owner * VPL + (VPL - 1 - static_cast<int>(k & (VPL - 1)));
+        }
+        if (lane == owner) {
+#pragma unroll
+            for (int v = 0; v + 1 < VPL; ++v) key[v] = key[v + 1];
+            key[VPL - 1] = 0u;
+        }
+    }
+    if (EXACT) return !__any_sync(FULL, lane < a.K && got == 0u);
+    // every pick has to be clear of the next one, and the last of the best that was left
+    const uint32_t left = __reduce_max_sync(FULL, key[0]);
+    uint32_t next = __shfl_down_sync(FULL, got, 1);
+    if (lane == a.K - 1) next = left;
+    const bool clear = lane >= a.K || (got != 0u && (next == 0u || unkey32(got) - unkey32(next) > 2.0f * tol));
+    return __all_sync(FULL, clear);
+}
+
+template <int VPL, bool BIAS, typename In>
+__global__ void __launch_bounds__(ROUTE_WARPS * 32) route_scores_kernel(const RouteArgs a) {
+    const int lane = threadIdx.x & 31;
+    const int t = blockIdx.x * ROUTE_WARPS + (threadIdx.x >> 5);
+    if (t >= a.T) return;
+    const In *row = static_cast<const In *>(a.logits) + static_cast<size_t>(t) * a.ld;
+    const int e0 = lane * VPL;
+    float l[VPL];
+    if (VPL * sizeof(In) >= 16 && a.vec) {  // 16-byte loads: E = 32 VPL and rows are aligned
+        load_run<VPL>(row + e0, l);
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) l[v] = l[v] > -INFINITY ? l[v] : -INFINITY;
+    } else {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            const float x = load_one(row + min(e0 + v, a.E - 1));
+            l[v] = e0 + v < a.E && x > -INFINITY ? x : -INFINITY;  // NaN masks as -inf does
+        }
+    }
+    int my_id, chosen = a.K;
+    float top;
+    double sum;
+    if (!a.fast || !choose_fast<VPL, BIAS, In>(a, l, e0, lane, my_id, top, sum))
+        choose_exact<VPL, BIAS>(a, l, e0, lane, my_id, chosen, top, sum);
     // ---- weights of the chosen, one per lane.  Renormalised softmax: relative to the largest
-    // chosen logit, so that a row whose maximum was masked by its group keeps its digits;
-    // sigmoid: in double, so that a row of very negative logits does.
+    // chosen logit, so that a row whose maximum was masked by its group keeps its digits; sigmoid of
+    // very negative logits alone: in double, for the same reason.
     float x = -INFINITY;
     if (lane < chosen) {
         if (sizeof(In) == 4) x = __ldg(reinterpret_cast<const float *>(row) + my_id);
@@ -239,7 +428,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_scores_kernel(const Ro
     float wt = 0.f;
     if (a.softmax) {
         if (a.renorm) top = unkey32(__reduce_max_sync(FULL, key32(x)));
-        float s = lane < chosen ? expf_(x) : 0.f;
+        float s = lane < chosen ? expf_above(x, top) : 0.f;
         if (a.renorm) {
             float d = s;
 #pragma unroll
@@ -248,15 +437,19 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_scores_kernel(const Ro
         } else {
             wt = lane < chosen ? static_cast<float>(static_cast<double>(s) / sum) : 0.f;
         }
+    } else if (a.renorm && !__any_sync(FULL, x > -40.0f)) {
+        double s = lane < chosen ? sigmoid(x) : 0.0, d = s;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(FULL, d, o);
+        wt = d > 0.0 ? static_cast<float>(s / d) : 0.f;
     } else {
-        double s = lane < chosen ? sigmoid(x) : 0.0;
+        wt = lane < chosen ? 1.0f / (1.0f + expf(-x)) : 0.f;
         if (a.renorm) {
-            double d = s;
+            float d = wt;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(FULL, d, o);
-            s = d > 0.0 ? s / d : 0.0;
+            wt = wt / d;
         }
-        wt = static_cast<float>(s);
     }
     if (lane < a.K) {
         a.ids[static_cast<size_t>(t) * a.K + lane] = my_id;
@@ -265,7 +458,15 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_scores_kernel(const Ro
 }
 
 template <int VPL>
-void launch_vpl(const RouteArgs &a, int act, cudaStream_t st) {
+void launch_vpl(RouteArgs a, int act, cudaStream_t st) {
+    const int gs = a.E / a.G, seg = gs / VPL;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(a.logits) | (a.bias ? reinterpret_cast<uintptr_t>(a.bias) : 0) | (a.ld * (act == COLI_ACT_F32 ? 4 : 2));
+    a.vec = a.E == 32 * VPL && at % 16 == 0;
+    a.fast = a.TG == a.G || (gs % VPL == 0 && (seg & (seg - 1)) == 0);
+    a.gs = gs;
+    a.inv_gs = 1.0f / static_cast<float>(gs);
+    a.seg_shift = 0;
+    while ((2 << a.seg_shift) <= seg) ++a.seg_shift;
     const int grid = (a.T + ROUTE_WARPS - 1) / ROUTE_WARPS;
     if (a.bias) {
         if (act == COLI_ACT_F32) route_scores_kernel<VPL, true, float><<<grid, ROUTE_WARPS * 32, 0, st>>>(a);

@@ -137,6 +137,26 @@ def test_ties_and_masks(score, biased, group):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("score", [SIG, SOFT])
+@pytest.mark.parametrize("E,G,TG,K", [(256, 8, 4, 8), (64, 1, 1, 6), (1024, 16, 2, 32), (40, 5, 2, 3)])
+@pytest.mark.parametrize("group", [TOP2, MAXG])
+def test_scores_closer_than_float32(score, E, G, TG, K, group):
+    """Biases that bring every s + b to within float32's last bits of one value: the choice between
+    experts and between groups is double's; some tokens have clear experts beside them."""
+    g = torch.Generator().manual_seed(E)
+    l = torch.randn(1, E, generator=g)
+    l64 = l.double()
+    s = torch.softmax(l64, 1)[0] if score == SOFT else torch.sigmoid(l64)[0]
+    bias = (0.75 - s).float()
+    rows = l.repeat(6, 1)
+    rows[1, ::7] += 1e-6
+    rows[2] = l[0].flip(0)
+    rows[4, :: E // G] += 3.0
+    check(rows, bias, router(E, K, G, TG, score, group, 1))
+    check(rows, torch.zeros(E), router(E, K, G, TG, score, group, 0))
+
+
+@pytest.mark.gpu
 def test_every_row_can_be_grouped():
     """Masked rows still hold K different ids, so the batch goes on through coli_moe_group."""
     import synth
