@@ -162,23 +162,24 @@ def _stream(stream) -> Optional[int]:
 
 def _current_stream() -> int:
     """Handle of the current device's current torch stream.  The handle alone: building torch's Stream
-    object takes longer (3.3 us against 0.3) than launching a small kernel."""
+    object takes longer (3.3 us against 0.1) than launching a small kernel."""
     import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None:
+    raw, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or dev is None or not torch.cuda.is_initialized():
         return torch.cuda.current_stream().cuda_stream
-    return raw(torch.cuda.current_device())
+    return raw(dev())
 
 
 def _device_stream(fn: str, stream, t) -> Optional[int]:
     """_stream for a call whose tensors must live on the current device: t is one of them."""
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
+    st = _current_stream()
     if t is not None and not isinstance(t, int):
         import torch
-        if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        if t.get_device() != torch.cuda.current_device():  # (-1: not a CUDA tensor)
             raise ColiError(fn, 1)
-    return _current_stream()
+    return st
 
 
 def _check(fn: str, status: int) -> None:

@@ -131,6 +131,31 @@ def test_quantize_gather_and_strides(fmt):
 @pytest.mark.gpu
 @pytest.mark.parametrize("fmt", [0, 1])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,div,k", [(257, 4, 288), (600, 8, 64), (130, 9, 6144), (3, 500, 1056)])
+def test_quantize_many_copies(fmt, dtype, T, div, k):
+    """Enough rows per source row that each source row is quantised once: as a permutation of the slots; with
+    one source row taken by most; with bad indices among them."""
+    g = torch.Generator().manual_seed(T + k)
+    x = (torch.randn(T, k, generator=g) * 3).to(DT[dtype])
+    x[1, 5] = float("nan")
+    n = T * div
+    for index in (torch.randperm(n, generator=g), torch.where(torch.rand(n, generator=g) < 0.8, div * (T // 2), torch.randint(0, n, (n,), generator=g))):
+        index = index.to(torch.int32)
+        got = run_quantize(x.cuda(), fmt, 0, index.cuda(), div, n)
+        check_quantized(got, x[(index // div).long()].double().numpy(), fmt, 0, k)
+    index[[0, n // 2, n - 1]] = torch.tensor([-1, n, -2 ** 31], dtype=torch.int64).to(torch.int32)
+    codes, scales, row, w = run_quantize(x.cuda(), fmt, 0, index.cuda(), div, n)
+    x64 = x[(index // div).clamp(0, T - 1).long()].double().numpy()
+    x64[[0, n // 2, n - 1]] = 0.0
+    code, byte, rs = ref.quantize(x64, fmt)
+    assert np.array_equal(ref.unpack(codes.cpu().numpy()), code) and np.array_equal(row.cpu().numpy(), rs)
+    assert np.array_equal(scales.cpu().numpy(), ref.rows_layout(byte, fmt, k).reshape(-1))
+    assert q.coli_moe_error_word(w) == q.DEVERR_GROUPING
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("layout", [0, 1])
 def test_dequantize(fmt, dtype, layout):
     """Every code under every scale byte; a row scale that is no power of two; rows further apart."""
