@@ -36,6 +36,8 @@ namespace coli {
 namespace {
 
 constexpr int A_BYTES = 128 * 128;       // weight codes of a k-block
+constexpr int P_NT = 256;                // rows of a CTA pair's tile
+constexpr int BAND = 8;
 constexpr int MAX_MATS = 1025;           // 1024 and a shared one
 constexpr int NBOX = 5;                  // box heights 16 << i rows
 constexpr int W_PROD = 0, W_MMA = 1, W_SF = 2, N_SF = 2, W_EPI0 = 4, N_EPI = 4;
@@ -135,6 +137,7 @@ __device__ __forceinline__ void group_rows(const GemmArgs &p, int e, int &lo, in
 // Tile t of the list; s_first[e]: tiles before matrix e.
 template <int NT>
 __device__ __forceinline__ Tile tile_at(int t, const int *s_first, const GemmArgs &p, int W) {
+    const int MB = (p.n + (NT == P_NT ? 255 : 127)) / (NT == P_NT ? 256 : 128);
     int lo = 0, hi = W;  // the last e with s_first[e] <= t
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -147,9 +150,11 @@ __device__ __forceinline__ Tile tile_at(int t, const int *s_first, const GemmArg
     group_rows(p, lo, row0, cnt);
     const int nch = (cnt + NT - 1) / NT;
     const int per = ((cnt + nch - 1) / nch + 31) & ~31;  // rows of a chunk: even shares
+    // bands of BAND weight blocks: a wave of tiles is BAND blocks times several chunks
     const int i = t - s_first[lo];
-    x.m = i / nch;
-    const int c = i - x.m * nch;
+    const int band = i / (BAND * nch), j = i - band * (BAND * nch), high = min(BAND, MB - band * BAND);
+    const int c = j / high;
+    x.m = band * BAND + (j - c * high);
     x.n0 = row0 + c * per;
     x.nr = min(per, cnt - c * per);
     return x;
@@ -229,19 +234,18 @@ __device__ __forceinline__ void store_run(const GemmArgs &p, const Tile &x, cons
 }
 
 // Row-scale warp `w` of N_SF: its k-blocks' scales of up to NT rows, from their rows (4 * ATOMS bytes
-// each) to the tile order of tcgen05.cp.  A lane takes rows 32 c + 8 i + l (c = lane / 8, l = lane % 8) of
-// each 128, so that its warp's 4-byte stores fall into 32 different banks and all its addresses are one
-// register and a constant.  Rows behind the tile's last repeat a row that exists: what they give is not
-// stored by the epilogue.  publish(stage) tells the MMA warp.  A k-block of 256 rows must not take much more
-// than 500 cycles, in which its products are done (with addresses and bounds worked out per store it took 900).
+// each) to the tile order of tcgen05.cp.  A lane takes rows lane + 32 c of each 128: word j of its four rows is
+// one 16-byte piece of tile j, so a k-block of 128 rows is ATOMS stores of 16 bytes per lane (shared memory is
+// nearly used up by the products' operands: 4-byte stores, four times as many, took 780 of the 730 cycles that
+// a k-block of 256 rows then needed per warp and other k-block).  Rows behind the tile's last repeat a row
+// that exists: what they give is not stored by the epilogue.  publish(stage) tells the MMA warp.
 template <int FMT, int NT, typename Publish>
 __device__ __forceinline__ void row_scales(const GemmArgs &p, int w, int first, int stride, int ntiles, int KT, const int *s_first, int W,
                                            unsigned char *ssb, uint64_t *empty, int S, volatile int *abort, Publish publish) {
     constexpr int ATOMS = Sf<FMT>::ATOMS, HALVES = (NT + 127) / 128, SLOTS = 4 * HALVES;
     const int lane = threadIdx.x & 31;
     const size_t pitch = fp4_pitch(FMT, p.k);
-    const int r0 = 32 * (lane >> 3) + (lane & 7);
-    const uint32_t dst0 = smem_u32(ssb) + (lane & 7) * 16 + (lane >> 3) * 4;
+    const uint32_t dst0 = smem_u32(ssb) + lane * 16;
     // DEPTH k-blocks of this warp in registers: a buffer is loaded again, for the k-block DEPTH turns on,
     // as soon as it has been stored (buffers are named by the unrolled loop: a copy from one to another
     // would wait for its loads)
@@ -256,7 +260,7 @@ __device__ __forceinline__ void row_scales(const GemmArgs &p, int w, int first, 
         const Tile x = tile_at<NT>(t, s_first, p, W);
         upper = x.nr > 128;
 #pragma unroll
-        for (int i = 0; i < SLOTS; ++i) src[i] = p.xsf + static_cast<size_t>(x.n0 + min(128 * (i >> 2) + 8 * (i & 3) + r0, x.nr - 1)) * pitch;
+        for (int i = 0; i < SLOTS; ++i) src[i] = p.xsf + static_cast<size_t>(x.n0 + min(32 * i + lane, x.nr - 1)) * pitch;
     };
     auto step = [&]() {  // to the tile that holds k-block kb
         if (kb < KT) return;
@@ -299,10 +303,11 @@ __device__ __forceinline__ void row_scales(const GemmArgs &p, int w, int first, 
             if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[s]), phase, abort, p.err))) return;
             const uint32_t dst = dst0 + s * (ATOMS * 512 * HALVES);
 #pragma unroll
-            for (int i = 0; i < SLOTS; ++i)
+            for (int h = 0; h < HALVES; ++h)
 #pragma unroll
                 for (int j = 0; j < ATOMS; ++j)
-                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + (j * HALVES + (i >> 2)) * 512 + (i & 3) * 128), "r"(v[b][i][j]) : "memory");
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                                 ::"r"(dst + (j * HALVES + h) * 512), "r"(v[b][4 * h][j]), "r"(v[b][4 * h + 1][j]), "r"(v[b][4 * h + 2][j]), "r"(v[b][4 * h + 3][j]) : "memory");
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) publish(s);
@@ -485,7 +490,6 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
 // Both CTAs hold the scales of all rows of the tile.  One accumulator of 256 columns per CTA; the
 // epilogue's eight warps take it whole into registers before they store, so that the next
 // tile's products wait for the reads alone.
-constexpr int P_NT = 256;
 constexpr int P_EPI = 8, P_THREADS = (4 + P_EPI) * 32;
 
 constexpr int P_OUT = 8192;              // bytes of an epilogue half's staging buffer
