@@ -42,6 +42,7 @@ constexpr int MAX_MATS = 1025;           // 1024 and a shared one
 constexpr int NBOX = 5;                  // box heights 16 << i rows
 constexpr int W_PROD = 0, W_MMA = 1, W_SF = 2, N_SF = 2, W_EPI0 = 4, N_EPI = 4;
 constexpr int THREADS = 8 * 32;
+constexpr int MAX_SPLIT = 4;             // CTAs that share a tile's k-blocks at most
 
 template <int FMT> struct Sf;            // scales of a k-block
 template <> struct Sf<COLI_FP4_NV> { static constexpr int ATOMS = 4; };  // 64 elements per 4 scales
@@ -56,9 +57,10 @@ struct Plan {
     static constexpr int SFB_BYTES = ATOMS * 512 * HALVES;
     static constexpr int STAGE = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
     static constexpr int SF_COLS = ATOMS * 4 * (1 + HALVES);
-    static constexpr int FIT = (220 * 1024) / STAGE, TFIT = 256 / SF_COLS;
+    static constexpr int PART = NT <= 32 ? (MAX_SPLIT - 1) * 32 * 128 * 4 : 0;  // split k: the other ranks' sums
+    static constexpr int FIT = (216 * 1024 - PART) / STAGE, TFIT = 256 / SF_COLS;
     static constexpr int S = FIT < TFIT ? FIT : TFIT;         // ring stages
-    static constexpr size_t SMEM = static_cast<size_t>(S) * STAGE + 1024;
+    static constexpr size_t SMEM = static_cast<size_t>(S) * STAGE + PART + 1024;
     static_assert(S >= 3, "the ring covers the copies' latency");
 };
 
@@ -99,6 +101,50 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                  ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void remote_arrive(uint32_t a) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(a) : "memory");
+}
+__device__ __forceinline__ void remote_expect_tx(uint32_t a, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(a), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_cluster(uint32_t a, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok) : "r"(a), "r"(parity), "r"(20000u) : "memory");
+    return ok != 0;
+}
+// mbar_wait for a phase that the other CTA of the pair takes part in
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t a, uint32_t parity, volatile int *abort, int *err) {
+    if (mbar_try_cluster(a, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_cluster(a, parity)) {
+        if (*abort) return false;
+        if (clock64() - t0 > WAIT_CYCLES) {
+            *abort = 1;
+            atomicOr(err, COLI_DEVERR_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
 struct GemmArgs {
     const uint8_t *wsf, *wsf_shared;         // scale tiles
     size_t wsf_stride;
@@ -123,35 +169,41 @@ struct Tile {
     int e, m, n0, nr;      // matrix, block of 128 weight rows, first row, rows
 };
 
+// What every role looks tiles up in, in shared memory: tiles before each matrix, and the offsets.
+struct TileList {
+    int first[MAX_MATS + 31 & ~31];
+    int off[MAX_MATS];
+};
+
 // First row and row count of matrix e's group; count -1 when the offsets are not ascending in range.
-__device__ __forceinline__ void group_rows(const GemmArgs &p, int e, int &lo, int &cnt) {
+__device__ __forceinline__ void group_rows(const GemmArgs &p, const TileList &l, int e, int &lo, int &cnt) {
     lo = 0;
     cnt = p.rows;
     if (p.offsets) {
-        lo = __ldg(p.offsets + e);
-        const int hi = e < p.E ? __ldg(p.offsets + e + 1) : p.rows;
+        lo = l.off[e];
+        const int hi = e < p.E ? l.off[e + 1] : p.rows;
         cnt = lo < 0 || hi < lo || hi > p.rows ? -1 : hi - lo;
     }
 }
 
-// Tile t of the list; s_first[e]: tiles before matrix e.
+// Tile t of the list, by a whole warp: two ballots find the last matrix whose first tile is not behind t.
 template <int NT>
-__device__ __forceinline__ Tile tile_at(int t, const int *s_first, const GemmArgs &p, int W) {
+__device__ __forceinline__ Tile tile_at(int t, const TileList &l, const GemmArgs &p, int W) {
     const int MB = (p.n + (NT == P_NT ? 255 : 127)) / (NT == P_NT ? 256 : 128);
-    int lo = 0, hi = W;  // the last e with s_first[e] <= t
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s_first[mid] <= t) lo = mid;
-        else hi = mid;
-    }
+    const int lane = threadIdx.x & 31;
+    const int most = min(W, 1024), blocks = (most + 31) / 32;
+    const int run = 31 - __clz(__ballot_sync(0xffffffffu, lane < blocks && l.first[min(32 * lane, MAX_MATS - 1)] <= t) | 1u);
+    int e = 32 * run + 31 - __clz(__ballot_sync(0xffffffffu, 32 * run + lane < most && l.first[32 * run + lane] <= t) | 1u);
+    if (W > 1024 && l.first[1024] <= t) e = 1024;
     Tile x;
-    x.e = lo;
+    x.e = e;
     int row0, cnt;
-    group_rows(p, lo, row0, cnt);
+    group_rows(p, l, e, row0, cnt);
     const int nch = (cnt + NT - 1) / NT;
     const int per = ((cnt + nch - 1) / nch + 31) & ~31;  // rows of a chunk: even shares
-    // bands of BAND weight blocks: a wave of tiles is BAND blocks times several chunks
-    const int i = t - s_first[lo];
+    // bands of BAND weight blocks: a wave of tiles is BAND blocks times several chunks (against all chunks of
+    // one block after another: 2048 rows, 6144 x 2048, 25 us against 29)
+    const int i = t - l.first[e];
     const int band = i / (BAND * nch), j = i - band * (BAND * nch), high = min(BAND, MB - band * BAND);
     const int c = j / high;
     x.m = band * BAND + (j - c * high);
@@ -160,16 +212,19 @@ __device__ __forceinline__ Tile tile_at(int t, const int *s_first, const GemmArg
     return x;
 }
 
-// The tile list: s_first[e] = tiles before matrix e (an exclusive scan by the whole CTA); the number
-// of tiles.
+// Fills the tile list (an exclusive scan of the matrices' tiles by the whole CTA); the number of tiles.
 template <int NT, int THREADS_>
-__device__ __forceinline__ int tile_list(const GemmArgs &p, int W, int MB, int *s_first, int *s_scan) {
+__device__ __forceinline__ int tile_list(const GemmArgs &p, int W, int MB, TileList &l, int *s_scan) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (p.offsets) {
+        for (int e = threadIdx.x; e <= p.E; e += THREADS_) l.off[e] = __ldg(p.offsets + e);
+        __syncthreads();
+    }
     int carry = 0;
     for (int base = 0; base < W; base += THREADS_) {
         const int e = base + threadIdx.x;
         int lo = 0, cnt = 0;
-        if (e < W) group_rows(p, e, lo, cnt);
+        if (e < W) group_rows(p, l, e, lo, cnt);
         if (cnt < 0) {
             cnt = 0;
             if (blockIdx.x == 0) atomicOr(p.err, COLI_DEVERR_GROUPING);
@@ -189,7 +244,7 @@ __device__ __forceinline__ int tile_list(const GemmArgs &p, int W, int MB, int *
             if (w < warp) before += v;
             carry += v;
         }
-        if (e < W) s_first[e] = before + inc - tiles;
+        if (e < W) l.first[e] = before + inc - tiles;
         __syncthreads();
     }
     return carry;
@@ -240,9 +295,9 @@ __device__ __forceinline__ void store_run(const GemmArgs &p, const Tile &x, cons
 // a k-block of 256 rows then needed per warp and other k-block).  Rows behind the tile's last repeat a row
 // that exists: what they give is not stored by the epilogue.  publish(stage) tells the MMA warp.
 template <int FMT, int NT, typename Publish>
-__device__ __forceinline__ void row_scales(const GemmArgs &p, int w, int first, int stride, int ntiles, int KT, const int *s_first, int W,
-                                           unsigned char *ssb, uint64_t *empty, int S, volatile int *abort, Publish publish) {
-    constexpr int ATOMS = Sf<FMT>::ATOMS, HALVES = (NT + 127) / 128, SLOTS = 4 * HALVES;
+__device__ __forceinline__ void row_scales(const GemmArgs &p, int w, int first, int stride, int ntiles, int KT, const TileList &list, int W,
+                                           unsigned char *ssb, uint64_t *empty, int S, int kb0, volatile int *abort, Publish publish) {
+    constexpr int ATOMS = Sf<FMT>::ATOMS, HALVES = (NT + 127) / 128, SLOTS = NT <= 32 ? 1 : 4 * HALVES;
     const int lane = threadIdx.x & 31;
     const size_t pitch = fp4_pitch(FMT, p.k);
     const uint32_t dst0 = smem_u32(ssb) + lane * 16;
@@ -257,7 +312,7 @@ __device__ __forceinline__ void row_scales(const GemmArgs &p, int w, int first, 
     bool upper = false;  // the tile has more than 128 rows
     auto tile = [&]() {
         if (t >= ntiles) return;
-        const Tile x = tile_at<NT>(t, s_first, p, W);
+        const Tile x = tile_at<NT>(t, list, p, W);
         upper = x.nr > 128;
 #pragma unroll
         for (int i = 0; i < SLOTS; ++i) src[i] = p.xsf + static_cast<size_t>(x.n0 + min(32 * i + lane, x.nr - 1)) * pitch;
@@ -272,7 +327,7 @@ __device__ __forceinline__ void row_scales(const GemmArgs &p, int w, int first, 
     };
     auto load = [&](uint32_t (&d)[SLOTS][ATOMS]) {
         if (t < ntiles) {
-            const int off = kb * (4 * ATOMS);
+            const int off = (kb0 + kb) * (4 * ATOMS);
 #pragma unroll
             for (int i = 0; i < SLOTS; ++i) {
                 if (i < 4 || upper) {
@@ -306,8 +361,9 @@ __device__ __forceinline__ void row_scales(const GemmArgs &p, int w, int first, 
             for (int h = 0; h < HALVES; ++h)
 #pragma unroll
                 for (int j = 0; j < ATOMS; ++j)
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
-                                 ::"r"(dst + (j * HALVES + h) * 512), "r"(v[b][4 * h][j]), "r"(v[b][4 * h + 1][j]), "r"(v[b][4 * h + 2][j]), "r"(v[b][4 * h + 3][j]) : "memory");
+                    if (SLOTS == 1) asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + j * 512), "r"(v[b][0][j]) : "memory");
+                    else asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                                 ::"r"(dst + (j * HALVES + h) * 512), "r"(v[b][4 * h][j]), "r"(v[b][(4 * h + 1) % SLOTS][j]), "r"(v[b][(4 * h + 2) % SLOTS][j]), "r"(v[b][(4 * h + 3) % SLOTS][j]) : "memory");
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) publish(s);
@@ -322,21 +378,67 @@ __device__ __forceinline__ void row_scales(const GemmArgs &p, int w, int first, 
     }
 }
 
+// Split k, one epilogue warp's 32 weight rows: ranks above 0 send their sums to rank 0's shared memory by
+// stores that count on its barrier as they land (no fence: with one, and whole-cluster barriers in the
+// kernel's way, a split took 3.5 us), rank 0 adds them in the order of the ranks.  A weight row's 32 sums
+// are 8 pieces of 16 bytes, piece i at i ^ (row % 8).  tl counts the tiles; `last`: no tile follows.
+// False when a wait gave up.
+__device__ __forceinline__ bool split_sum(int (&v)[32], int nr, int C, int rank, int q, int lane, uint32_t tl, bool last, float *part,
+                                          uint64_t *pfull, uint64_t *pfree, volatile int *abort, int *err) {
+    const int row = 32 * q + lane, pieces = (nr + 3) / 4;
+    if (rank != 0) {
+        if (tl > 0 && !__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(pfree), (tl & 1) ^ 1, abort, err))) return false;
+        const uint32_t to = map_rank(smem_u32(part) + ((rank - 1) * 128 + row) * 128, 0), bar = map_rank(smem_u32(pfull), 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < pieces)
+                asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];"
+                             ::"r"(to + ((i ^ (lane & 7)) << 4)), "r"(v[4 * i]), "r"(v[4 * i + 1]), "r"(v[4 * i + 2]), "r"(v[4 * i + 3]), "r"(bar) : "memory");
+    } else {
+        if (lane == 0) mbar_expect_tx(smem_u32(pfull), (C - 1) * 32 * pieces * 16);  // this warp's rows
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(pfull), tl & 1, abort, err))) return false;
+        for (int c = 1; c < C; ++c) {
+            const float4 *from = reinterpret_cast<const float4 *>(part + ((c - 1) * 128 + row) * 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < pieces) {
+                    const float4 f = from[i ^ (lane & 7)];
+                    v[4 * i] = __float_as_int(__int_as_float(v[4 * i]) + f.x);
+                    v[4 * i + 1] = __float_as_int(__int_as_float(v[4 * i + 1]) + f.y);
+                    v[4 * i + 2] = __float_as_int(__int_as_float(v[4 * i + 2]) + f.z);
+                    v[4 * i + 3] = __float_as_int(__int_as_float(v[4 * i + 3]) + f.w);
+                }
+        }
+        __syncwarp();
+        if (lane == 0 && !last)
+            for (int c = 1; c < C; ++c) remote_arrive(map_rank(smem_u32(pfree), c));
+    }
+    return true;
+}
+
 template <int FMT, int NT, int OUT>
 __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs p) {
     using P = Plan<FMT, NT>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char *sa = sm, *sb = sa + P::S * A_BYTES, *ssa = sb + P::S * P::B_BYTES, *ssb = ssa + P::S * P::SFA_BYTES;
-    __shared__ __align__(8) uint64_t bars[3 * P::S + 5];
+    constexpr bool SPLIT = NT <= 32;
+    __shared__ __align__(8) uint64_t bars[3 * P::S + 7];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
-    __shared__ int s_first[MAX_MATS], s_scan[THREADS / 32];
+    __shared__ TileList list;
+    __shared__ int s_scan[THREADS / 32];
     uint64_t *full = bars, *sfull = full + P::S, *empty = sfull + P::S;
     uint64_t *dfull = empty + P::S, *dempty = dfull + 2, *drain = dempty + 2;
+    uint64_t *pfull = drain + 1, *pfree = pfull + 1;  // split k: partial sums there; their place free again
+    float *part = reinterpret_cast<float *>(ssb + P::S * P::SFB_BYTES);
+    // split k: the CTAs of a cluster take a share of the k-blocks each; rank 0 adds and stores
+    const int C = SPLIT ? static_cast<int>(cluster_size()) : 1, rank = SPLIT ? static_cast<int>(cluster_rank()) : 0;
+    const int first = blockIdx.x / C, stride = gridDim.x / C;
     volatile int *abort = &s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int MB = (p.n + 127) / 128, KT = (p.k + FP4_KB - 1) / FP4_KB;
+    const int MB = (p.n + 127) / 128, KALL = (p.k + FP4_KB - 1) / FP4_KB;
+    const int kb0 = KALL * rank / C, KT = KALL * (rank + 1) / C - kb0;
     const int W = p.E + p.S;
 
     if (warp == 0) tmem_alloc(smem_u32(&s_tmem), 512);
@@ -351,12 +453,16 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
             mbar_init(smem_u32(&dempty[i]), N_EPI * 32);
         }
         mbar_init(smem_u32(drain), 1);
+        mbar_init(smem_u32(pfull), N_EPI);
+        mbar_init(smem_u32(pfree), N_EPI);
         s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    const int ntiles = tile_list<NT, THREADS>(p, W, MB, s_first, s_scan);
+    const int ntiles = tile_list<NT, THREADS>(p, W, MB, list, s_scan);
     tc_fence_before();
     __syncthreads();
+    // the cluster's barriers are set up: waited for where another CTA's memory is first touched
+    if (SPLIT && C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     tc_fence_after();
     const uint32_t tbase = s_tmem;
 
@@ -367,8 +473,8 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
         // lane, a copy took the compiler's loop over lanes and 200 cycles)
         const size_t mtile = 128 * fp4_pitch(FMT, p.k);  // scale bytes of 128 weight rows
         uint32_t it = 0;
-        for (int t = blockIdx.x; t < ntiles; t += gridDim.x) {
-            const Tile x = tile_at<NT>(t, s_first, p, W);
+        for (int t = first; t < ntiles; t += stride) {
+            const Tile x = tile_at<NT>(t, list, p, W);
             const bool shared = x.e >= p.E;
             const CUtensorMap *ta = shared ? &maps.as : &maps.a;
             const int ez = shared ? 0 : x.e;
@@ -380,12 +486,12 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
                 const uint32_t fb = smem_u32(&full[s]);
                 if (elect_one()) {
                     mbar_expect_tx(fb, A_BYTES + P::SFA_BYTES + n16 * 16 * 128);
-                    tma_load_3d(smem_u32(sa + s * A_BYTES), ta, kb * 128, x.m * 128, ez, fb);
-                    bulk_load(smem_u32(ssa + s * P::SFA_BYTES), wsf + static_cast<size_t>(kb) * P::SFA_BYTES, P::SFA_BYTES, fb);
+                    tma_load_3d(smem_u32(sa + s * A_BYTES), ta, (kb0 + kb) * 128, x.m * 128, ez, fb);
+                    bulk_load(smem_u32(ssa + s * P::SFA_BYTES), wsf + static_cast<size_t>(kb0 + kb) * P::SFA_BYTES, P::SFA_BYTES, fb);
 #pragma unroll
-                    for (int bit = NBOX - 1; bit >= 0; --bit) {
+                    for (int bit = NT <= 32 ? 1 : NBOX - 2; bit >= 0; --bit) {
                         const int row0 = 16 * ((n16 >> (bit + 1)) << (bit + 1));  // rows of the larger boxes
-                        if ((n16 >> bit) & 1) tma_load_2d(smem_u32(sb + s * P::B_BYTES + row0 * 128), &maps.b[bit], kb * 128, x.n0 + row0, fb);
+                        if ((n16 >> bit) & 1) tma_load_2d(smem_u32(sb + s * P::B_BYTES + row0 * 128), &maps.b[bit], (kb0 + kb) * 128, x.n0 + row0, fb);
                     }
                 }
                 __syncwarp();
@@ -402,8 +508,8 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
         uint32_t it = 0, tl = 0;
         const uint64_t adesc0 = smem_desc_sw128(smem_u32(sa)), bdesc0 = smem_desc_sw128(smem_u32(sb));
         const uint64_t sadesc0 = smem_desc_sf(smem_u32(ssa)), sbdesc0 = smem_desc_sf(smem_u32(ssb));
-        for (int t = blockIdx.x; t < ntiles; t += gridDim.x, ++tl) {
-            const Tile x = tile_at<NT>(t, s_first, p, W);
+        for (int t = first; t < ntiles; t += stride, ++tl) {
+            const Tile x = tile_at<NT>(t, list, p, W);
             const int n16 = (x.nr + 15) / 16;
             const uint32_t idesc = idesc_fp4<FMT>() | (static_cast<uint32_t>(2 * n16) << 17);
             const int acc = tl & 1;
@@ -415,7 +521,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
                 if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[s]), (it / P::S) & 1, abort, p.err))) goto mma_done;
                 if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sfull[s]), (it / P::S) & 1, abort, p.err))) goto mma_done;
                 tc_fence_after();
-                const int steps = min(4, (p.k - kb * FP4_KB + 63) / 64);  // K = 64 steps that hold elements
+                const int steps = min(4, (p.k - (kb0 + kb) * FP4_KB + 63) / 64);  // K = 64 steps that hold elements
                 if (elect_one()) {
                     const uint32_t sfa = tbase + 256 + s * P::SF_COLS, sfb = sfa + 4 * P::ATOMS;
                     const uint64_t ad = adesc0 + static_cast<uint64_t>(s * (A_BYTES >> 4)), bd = bdesc0 + static_cast<uint64_t>(s * (P::B_BYTES >> 4));
@@ -449,14 +555,15 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
         mbar_drain(smem_u32(drain), 0);
     } else if (warp < W_EPI0) {
         // ------------------------------------------------------------------ scales of the rows
-        row_scales<FMT, NT>(p, warp - W_SF, blockIdx.x, gridDim.x, ntiles, KT, s_first, W, ssb, empty, P::S, abort,
+        row_scales<FMT, NT>(p, warp - W_SF, first, stride, ntiles, KT, list, W, ssb, empty, P::S, kb0, abort,
                             [&](int st) { mbar_arrive(smem_u32(&sfull[st])); });
     } else {
         // ------------------------------------------------------------------ epilogue
         const int q = warp - W_EPI0;  // TMEM lane quarter (warp % 4)
         uint32_t tl = 0;
-        for (int t = blockIdx.x; t < ntiles; t += gridDim.x, ++tl) {
-            const Tile x = tile_at<NT>(t, s_first, p, W);
+        if (SPLIT && C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        for (int t = first; t < ntiles; t += stride, ++tl) {
+            const Tile x = tile_at<NT>(t, list, p, W);
             const int acc = tl & 1;
             const int r = x.m * 128 + 32 * q + lane;
             const float *wrow = x.e >= p.E ? p.wrow_shared : (p.wrow ? p.wrow + static_cast<size_t>(x.e) * p.wrow_stride : nullptr);
@@ -467,6 +574,10 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
             for (int g = 0; g < x.nr; g += 32) {
                 int v[32];
                 tmem_ld32(dt + g, v);
+                if (SPLIT && C > 1) {
+                    if (!split_sum(v, x.nr, C, rank, q, lane, tl, t + stride >= ntiles, part, pfull, pfree, abort, p.err)) break;
+                    if (rank != 0) break;
+                }
                 const float rx = p.xrow && g + lane < x.nr ? __ldg(p.xrow + x.n0 + g + lane) : 1.f;
                 store_run<OUT>(p, x, v, g, r, rw, rx, lane);
             }
@@ -475,8 +586,13 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
         }
     }
 
+    if (SPLIT && C > 1 && warp < W_EPI0) {
+        __syncwarp();
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
     tc_fence_before();
     __syncthreads();
+    if (SPLIT && C > 1) cluster_sync_all();  // no CTA leaves while another may still write to it
     if (warp == 0) {
         tc_fence_after();
         tmem_dealloc(tbase, 512);
@@ -501,7 +617,7 @@ struct PairPlan {
     static constexpr int SFA_BYTES = ATOMS * 512, SFB_BYTES = ATOMS * 1024;
     static constexpr int STAGE = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
     static constexpr int SF_COLS = ATOMS * 12;
-    static constexpr int FIT = (220 * 1024 - 2 * P_OUT) / STAGE, TFIT = 256 / SF_COLS;
+    static constexpr int FIT = (216 * 1024 - 2 * P_OUT) / STAGE, TFIT = 256 / SF_COLS;
     static constexpr int S = FIT < TFIT ? FIT : TFIT;
     static constexpr size_t SMEM = static_cast<size_t>(S) * STAGE + 2 * P_OUT + 1024;
     static_assert(S >= 3, "the ring covers the copies' latency");
@@ -568,45 +684,6 @@ __device__ __forceinline__ void staged_run(const GemmArgs &p, const Tile &x, con
     }
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void remote_arrive(uint32_t a) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(a) : "memory");
-}
-__device__ __forceinline__ void remote_expect_tx(uint32_t a, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(a), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_cluster(uint32_t a, uint32_t parity) {
-    uint32_t ok;
-    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
-                 : "=r"(ok) : "r"(a), "r"(parity), "r"(20000u) : "memory");
-    return ok != 0;
-}
-// mbar_wait for a phase that the other CTA of the pair takes part in
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t a, uint32_t parity, volatile int *abort, int *err) {
-    if (mbar_try_cluster(a, parity)) return true;
-    const long long t0 = clock64();
-    while (!mbar_try_cluster(a, parity)) {
-        if (*abort) return false;
-        if (clock64() - t0 > WAIT_CYCLES) {
-            *abort = 1;
-            atomicOr(err, COLI_DEVERR_TIMEOUT);
-            return false;
-        }
-    }
-    return true;
-}
 // TMA loads of a pair's CTA: into its own shared memory, the barrier in the leader's.
 __device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap *m, int c0, int c1, int c2, uint32_t bar) {
     asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
@@ -647,7 +724,8 @@ fp4_pair_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs p) {
     __shared__ __align__(8) uint64_t bars[2 * P::S + 3];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
-    __shared__ int s_first[MAX_MATS], s_scan[P_THREADS / 32];
+    __shared__ TileList list;
+    __shared__ int s_scan[P_THREADS / 32];
     // full: the leader's, of both CTAs' copies; empty, dfull: in each CTA; dempty: the leader's
     uint64_t *full = bars, *empty = full + P::S, *dfull = empty + P::S, *dempty = dfull + 1, *drain = dempty + 1;
     volatile int *abort = &s_abort;
@@ -672,7 +750,7 @@ fp4_pair_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs p) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512u) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
-    const int ntiles = tile_list<P_NT, P_THREADS>(p, W, MB, s_first, s_scan);
+    const int ntiles = tile_list<P_NT, P_THREADS>(p, W, MB, list, s_scan);
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();
@@ -684,7 +762,7 @@ fp4_pair_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs p) {
         const int atoms = static_cast<int>(fp4_pitch(FMT, p.k) / 4);  // scale tiles of 128 weight rows
         uint32_t it = 0;
         for (int t = pair; t < ntiles; t += pairs) {
-            const Tile x = tile_at<P_NT>(t, s_first, p, W);
+            const Tile x = tile_at<P_NT>(t, list, p, W);
             const bool shared = x.e >= p.E;
             const CUtensorMap *ta = shared ? &maps.as : &maps.a, *tsf = shared ? &maps.sfs : &maps.sf;
             const int ez = shared ? 0 : x.e;
@@ -717,7 +795,7 @@ fp4_pair_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs p) {
         const uint64_t adesc0 = smem_desc_sw128(smem_u32(sa)), bdesc0 = smem_desc_sw128(smem_u32(sb));
         const uint64_t sadesc0 = smem_desc_sf(smem_u32(ssa)), sbdesc0 = smem_desc_sf(smem_u32(ssb));
         for (int t = pair; t < ntiles; t += pairs, ++tl) {
-            const Tile x = tile_at<P_NT>(t, s_first, p, W);
+            const Tile x = tile_at<P_NT>(t, list, p, W);
             const int n32 = (x.nr + 31) / 32;
             const uint32_t idesc = (idesc_fp4<FMT>() & ~(3u << 27)) | (2u << 27) | (static_cast<uint32_t>(4 * n32) << 17);
             if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(dempty), (tl & 1) ^ 1, abort, p.err))) goto mma_done;
@@ -761,7 +839,7 @@ fp4_pair_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs p) {
             for (uint32_t i = it; i < it + P::S; ++i) mbar_drain(smem_u32(&full[i % P::S]), (i / P::S) & 1);
     } else if (warp == W_SF || warp == W_SF + 1) {
         // ------------------------------------------------------------------ scales of the rows
-        row_scales<FMT, P_NT>(p, warp - W_SF, pair, pairs, ntiles, KT, s_first, W, ssb, empty, P::S, abort,
+        row_scales<FMT, P_NT>(p, warp - W_SF, pair, pairs, ntiles, KT, list, W, ssb, empty, P::S, 0, abort,
                               [&](int st) { remote_arrive(map_rank(smem_u32(&full[st]), 0)); });
     } else if (warp >= W_EPI0) {
         // ------------------------------------------------------------------ epilogue
@@ -771,7 +849,7 @@ fp4_pair_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs p) {
         const bool vec = ((reinterpret_cast<uintptr_t>(p.out) | (p.ldo * ITEM)) & 15) == 0;
         uint32_t tl = 0;
         for (int t = pair; t < ntiles; t += pairs, ++tl) {
-            const Tile x = tile_at<P_NT>(t, s_first, p, W);
+            const Tile x = tile_at<P_NT>(t, list, p, W);
             const int r = x.m * 256 + static_cast<int>(rank) * 128 + 32 * q + lane;
             const float *wrow = x.e >= p.E ? p.wrow_shared : (p.wrow ? p.wrow + static_cast<size_t>(x.e) * p.wrow_stride : nullptr);
             const float rw = wrow && r < p.n ? __ldg(wrow + r) : 1.f;
@@ -840,6 +918,10 @@ bool rows_maps(CUtensorMap *m, const coli_fp4_rows &a, int k) {
     return true;
 }
 
+// Clusters of c CTAs, one CTA per SM, that run at once: with c = 4 some SMs of a GPC are left over (33
+// clusters on B200's 148 SMs, by cudaOccupancyMaxActiveClusters).
+int cluster_count(int c, int sms) { return c <= 2 ? sms / c : (sms - 16) / 4; }
+
 // The kernel's shared-memory attribute lasts as long as the context: set once per device (twice is
 // harmless).
 template <typename K>
@@ -852,18 +934,55 @@ cudaError_t allow_smem(K *kernel, size_t bytes, std::atomic<uint64_t> &ready) {
     return e;
 }
 
-template <int FMT, int NT, int OUT>
+template <int FMT, int OUT>
 cudaError_t launch_gemm(const GemmMaps &maps, const GemmArgs &g, cudaStream_t st) {
-    using P = Plan<FMT, NT>;
-    auto kernel = fp4_gemm_kernel<FMT, NT, OUT>;
+    using P = Plan<FMT, 128>;
+    auto kernel = fp4_gemm_kernel<FMT, 128, OUT>;
     static std::atomic<uint64_t> ready{0};
     const cudaError_t e = allow_smem(kernel, P::SMEM, ready);
     if (e != cudaSuccess) return e;
-    const long chunks = g.rows / NT + (g.rows < g.E + g.S ? g.rows : g.E + g.S);  // at most
+    const long chunks = g.rows / 128 + (g.rows < g.E + g.S ? g.rows : g.E + g.S);  // at most
     const long tiles = (chunks < 1 ? 1 : chunks) * ((g.n + 127) / 128);
     const int sms = device_sm_count();
     kernel<<<static_cast<int>(tiles < sms ? tiles : sms), THREADS, P::SMEM, st>>>(maps, g);
     return cudaGetLastError();
+}
+
+// At most 32 rows: tiles of 128 weight rows x all rows of a matrix, their k-blocks split over clusters of 1, 2
+// or 4 CTAs, whichever leaves the busiest CTA the least (the matrices that have rows are at most as many as
+// rows).  One row, 4096 x 6144: 8.5 us against 11.3 unsplit.
+template <int FMT, int OUT>
+cudaError_t launch_split(const GemmMaps &maps, const GemmArgs &g, cudaStream_t st) {
+    using P = Plan<FMT, 32>;
+    auto kernel = fp4_gemm_kernel<FMT, 32, OUT>;
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = allow_smem(kernel, P::SMEM, ready);
+    if (e != cudaSuccess) return e;
+    const int sms = device_sm_count(), kt = (g.k + FP4_KB - 1) / FP4_KB;
+    const int tiles = (g.rows < g.E + g.S ? g.rows : g.E + g.S) * ((g.n + 127) / 128);
+    int C = 1;
+    long best = 0;
+    for (int c = 1; c <= MAX_SPLIT && c <= kt; c *= 2) {
+        const int clusters = cluster_count(c, sms);
+        const long cost = static_cast<long>((tiles + clusters - 1) / clusters) * ((kt + c - 1) / c);  // k-blocks of the busiest CTA
+        if (c == 1 || 16 * cost < 15 * best) {
+            best = cost;
+            C = c;
+        }
+    }
+    const int clusters = cluster_count(C, sms);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(C * (tiles < clusters ? tiles : clusters));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = P::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = C;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = C > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, maps, g);
 }
 
 template <int FMT, int OUT>
@@ -880,16 +999,17 @@ cudaError_t launch_pair(const GemmMaps &maps, const GemmArgs &g, cudaStream_t st
     return cudaGetLastError();
 }
 
+template <int FMT, int OUT>
+cudaError_t launch_out(const GemmMaps &maps, const GemmArgs &g, bool pairs, cudaStream_t st) {
+    if (pairs) return launch_pair<FMT, OUT>(maps, g, st);
+    return g.rows <= 32 ? launch_split<FMT, OUT>(maps, g, st) : launch_gemm<FMT, OUT>(maps, g, st);
+}
+
 template <int FMT>
 cudaError_t launch_fmt(const GemmMaps &maps, const GemmArgs &g, int out_kind, bool pairs, cudaStream_t st) {
-    if (pairs) {
-        if (out_kind == FP4_OUT_F32) return launch_pair<FMT, FP4_OUT_F32>(maps, g, st);
-        if (out_kind == FP4_OUT_BF16) return launch_pair<FMT, FP4_OUT_BF16>(maps, g, st);
-        return launch_pair<FMT, FP4_OUT_SWIGLU>(maps, g, st);
-    }
-    if (out_kind == FP4_OUT_F32) return launch_gemm<FMT, 128, FP4_OUT_F32>(maps, g, st);
-    if (out_kind == FP4_OUT_BF16) return launch_gemm<FMT, 128, FP4_OUT_BF16>(maps, g, st);
-    return launch_gemm<FMT, 128, FP4_OUT_SWIGLU>(maps, g, st);
+    if (out_kind == FP4_OUT_F32) return launch_out<FMT, FP4_OUT_F32>(maps, g, pairs, st);
+    if (out_kind == FP4_OUT_BF16) return launch_out<FMT, FP4_OUT_BF16>(maps, g, pairs, st);
+    return launch_out<FMT, FP4_OUT_SWIGLU>(maps, g, pairs, st);
 }
 
 }  // namespace

@@ -112,7 +112,7 @@ def group(cfg, ids, T, ws):
 @pytest.mark.gpu
 @pytest.mark.parametrize("wfmt", [20, 36])
 @pytest.mark.parametrize("T,H,I,E,K,shared,act", [(1, 256, 128, 8, 3, 1, 1), (3, 192, 320, 5, 2, 0, 0), (17, 256, 64, 16, 4, 1, 0),
-                                                  (90, 320, 192, 4, 2, 1, 1), (300, 256, 192, 2, 2, 1, 1), (5, 256, 128, 64, 8, 1, 1)])
+                                                  (90, 320, 192, 4, 2, 1, 1), (300, 256, 192, 2, 2, 1, 1), (5, 256, 128, 64, 8, 1, 1), (3, 64, 64, 1024, 8, 1, 1)])
 def test_expert_half(wfmt, T, H, I, E, K, shared, act):
     cfg = config(wfmt, H, I, E, K, shared, act)
     ex = Experts(cfg)
