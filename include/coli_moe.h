@@ -38,7 +38,7 @@
  *   as the microscaled 4-bit section below has them; coli_moe_fp4_pack_record writes a record.  With
  *   these containers the layer quantises its activations too: x of every token, and h = SiLU(g) * u
  *   rounded to bf16, as coli_moe_fp4_quantize does; y is rounded to bf16 before the combine, whose
- *   order is fixed.
+ *   order is fixed.  coli_moe_layer routes by coli_moe_route_scores (sigmoid, groups by two, renormalised).
  *
  * Tensor layouts (row-major):
  *   x        [T][H]   float32 (act = COLI_ACT_F32) or bfloat16 bits (COLI_ACT_BF16), 16-B aligned

@@ -472,7 +472,14 @@ coli_status coli_moe_layer(const coli_moe_config *c, const coli_moe_weights *w, 
         return from_cuda(launch_ffn_decode(d, pl, st));
     }
     cudaError_t e = launch_gate(*c, w->router_w, x, T, logits, st);
-    if (e == cudaSuccess) e = launch_route(*c, logits, w->router_bias, T, ids, wts, st);
+    if (e == cudaSuccess) {
+        if (fp4_wfmt(c->wfmt)) {  // the general router as the noaux_tc one
+            const coli_moe_router r = {c->n_experts, c->top_k, c->n_group, c->topk_group, COLI_SCORE_SIGMOID, COLI_GROUP_TOP2, 1, COLI_ACT_F32, c->routed_scaling};
+            e = launch_route_scores(r, logits, static_cast<size_t>(c->n_experts), w->router_bias, T, ids, wts, st);
+        } else {
+            e = launch_route(*c, logits, w->router_bias, T, ids, wts, st);
+        }
+    }
     if (e == cudaSuccess) e = launch_group(*c, ids, T, counts, offsets, perm, uniq, nu, err, st);
     if (e != cudaSuccess) return from_cuda(e);
     return run_ffn(c, p, base, st);

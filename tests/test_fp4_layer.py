@@ -144,8 +144,9 @@ def test_expert_half(wfmt, T, H, I, E, K, shared, act):
 @pytest.mark.parametrize("wfmt", [20, 36])
 @pytest.mark.parametrize("T", [1, 6, 130])
 def test_whole_layer(wfmt, T):
-    """The layer is its parts: routing as coli_moe_route gives it, the expert half on that routing, bit for
-    bit; replayed from a graph with new activations too; and without allocation."""
+    """The layer is its parts: routing as coli_moe_route_scores gives it (and coli_moe_route, but for the last
+    bits of its weights), the expert half on that routing, bit for bit; replayed from a graph with new
+    activations too; and without allocation."""
     cfg = config(wfmt)
     assert q.coli_moe_layer_kernels(cfg, T) == 8
     ex = Experts(cfg)
@@ -160,6 +161,13 @@ def test_whole_layer(wfmt, T):
         i, v, out = torch.empty_like(ids), torch.empty_like(w), torch.empty(T, H, device="cuda")
         q.coli_moe_gate(cfg, ex.Wr, x, T, logits)
         q.coli_moe_route(cfg, logits, ex.bias, T, i, v)
+        i0, v0 = i.clone(), v.clone()
+        q.coli_moe_route_scores(q.MoERouter(cfg.n_experts, K, cfg.n_group, cfg.topk_group, q.COLI_SCORE_SIGMOID, q.COLI_GROUP_TOP2, 1, 0,
+                                            cfg.routed_scaling), logits, 0, ex.bias, T, i, v)
+        assert torch.equal(i, i0) and torch.allclose(v, v0, rtol=(cfg.n_experts + 8) * 2.0 ** -24, atol=0)
+        # the gate's sums are double: its float32 logits are the exact dot products' roundings, or a neighbour's
+        exact = x.double() @ ex.Wr.double().T
+        assert (torch.abs(logits.double() - exact) <= 2.0 ** -24 * 1.001 * exact.abs() + 1e-12).all()
         _, offsets, perm, uniq, nu = group(cfg, i, T, ws)
         q.coli_moe_ffn(cfg, ex.weights, x, T, v, offsets, perm, uniq, nu, out, ws)
         return i, v, out
