@@ -12,6 +12,7 @@
 
 #include "fp4.h"
 #include "internal.h"
+#include "pdl.h"
 
 namespace coli {
 
@@ -22,6 +23,7 @@ constexpr int CT = 128;  // threads: 8 columns each
 __global__ void __launch_bounds__(CT) fp4_combine_kernel(const __nv_bfloat16 *__restrict__ y, const float *__restrict__ w,
                                                          const int32_t *__restrict__ inverse, const int32_t *__restrict__ perm,
                                                          int T, int K, int S, int H, float *__restrict__ out) {
+    wait_for_previous();
     const int t = blockIdx.x, c = (blockIdx.y * CT + threadIdx.x) * 8;
     if (c >= H) return;
     const int TK = T * K;
@@ -117,9 +119,8 @@ cudaError_t launch_ffn_fp4(const FfnParams &f, int wfmt, const Fp4Buffers &b, cu
     p.ldo = static_cast<size_t>(f.H);
     if ((e = launch_fp4_product(fmt, p, st)) != cudaSuccess) return e;
 
-    fp4_combine_kernel<<<dim3(f.T, (f.H / 8 + CT - 1) / CT), CT, 0, st>>>(static_cast<const __nv_bfloat16 *>(b.y), f.topk_w, b.inverse, f.perm, f.T, f.K, f.S,
-                                                                   f.H, f.out);
-    return cudaGetLastError();
+    return launch_early(fp4_combine_kernel, dim3(f.T, (f.H / 8 + CT - 1) / CT), CT, 0, st, 1, static_cast<const __nv_bfloat16 *>(b.y), f.topk_w, b.inverse,
+                        f.perm, f.T, f.K, f.S, f.H, f.out);
 }
 
 }  // namespace coli

@@ -29,6 +29,7 @@
 
 #include "fp4.h"
 #include "internal.h"
+#include "pdl.h"
 #include "tc_ptx.h"
 
 namespace coli {
@@ -458,6 +459,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
         s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    wait_for_previous();
     const int ntiles = tile_list<NT, THREADS>(p, W, MB, list, s_scan);
     tc_fence_before();
     __syncthreads();
@@ -586,6 +588,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
         }
     }
 
+    dependents_may_launch();
     if (SPLIT && C > 1 && warp < W_EPI0) {
         __syncwarp();
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -714,8 +717,7 @@ __device__ __forceinline__ void pair_commit(uint32_t mbar) {
 }
 
 template <int FMT, int OUT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
-fp4_pair_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs p) {
+__global__ void __launch_bounds__(P_THREADS, 1) fp4_pair_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs p) {  // clusters of 2
     using P = PairPlan<FMT>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     // the same offset in both CTAs: the dynamic array starts at the same address in each
@@ -750,6 +752,7 @@ fp4_pair_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs p) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512u) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    wait_for_previous();
     const int ntiles = tile_list<P_NT, P_THREADS>(p, W, MB, list, s_scan);
     tc_fence_before();
     __syncthreads();
@@ -876,6 +879,7 @@ fp4_pair_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs p) {
         }
     }
 
+    dependents_may_launch();
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();
@@ -944,8 +948,7 @@ cudaError_t launch_gemm(const GemmMaps &maps, const GemmArgs &g, cudaStream_t st
     const long chunks = g.rows / 128 + (g.rows < g.E + g.S ? g.rows : g.E + g.S);  // at most
     const long tiles = (chunks < 1 ? 1 : chunks) * ((g.n + 127) / 128);
     const int sms = device_sm_count();
-    kernel<<<static_cast<int>(tiles < sms ? tiles : sms), THREADS, P::SMEM, st>>>(maps, g);
-    return cudaGetLastError();
+    return launch_early(kernel, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), THREADS, P::SMEM, st, 1, maps, g);
 }
 
 // At most 32 rows: tiles of 128 weight rows x all rows of a matrix, their k-blocks split over clusters of 1, 2
@@ -971,18 +974,7 @@ cudaError_t launch_split(const GemmMaps &maps, const GemmArgs &g, cudaStream_t s
         }
     }
     const int clusters = cluster_count(C, sms);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(C * (tiles < clusters ? tiles : clusters));
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = P::SMEM;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = C;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = C > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, maps, g);
+    return launch_early(kernel, dim3(C * (tiles < clusters ? tiles : clusters)), THREADS, P::SMEM, st, C, maps, g);
 }
 
 template <int FMT, int OUT>
@@ -995,8 +987,7 @@ cudaError_t launch_pair(const GemmMaps &maps, const GemmArgs &g, cudaStream_t st
     const long chunks = g.rows / P_NT + (g.rows < g.E + g.S ? g.rows : g.E + g.S);
     const long tiles = (chunks < 1 ? 1 : chunks) * ((g.n + 255) / 256);
     const int pairs = device_sm_count() / 2;
-    kernel<<<2 * static_cast<int>(tiles < pairs ? tiles : pairs), P_THREADS, P::SMEM, st>>>(maps, g);
-    return cudaGetLastError();
+    return launch_early(kernel, dim3(2 * static_cast<unsigned>(tiles < pairs ? tiles : pairs)), P_THREADS, P::SMEM, st, 2, maps, g);
 }
 
 template <int FMT, int OUT>

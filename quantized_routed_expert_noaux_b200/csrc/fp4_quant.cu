@@ -18,6 +18,7 @@
 
 #include "fp4.h"
 #include "internal.h"
+#include "pdl.h"
 
 namespace coli {
 
@@ -283,6 +284,7 @@ __device__ __forceinline__ float quantize_row(const In *row, bool live, bool rea
 template <int FMT, int TPR, typename In>
 __global__ void __launch_bounds__(QT) fp4_quant_kernel(const Fp4QuantArgs a, int layout, int out_rows) {
     __shared__ uint32_t s_max[QT / 32];
+    wait_for_previous();
     const int r = blockIdx.x * (QT / TPR) + threadIdx.x / TPR, i0 = threadIdx.x % TPR;
     const size_t pitch = fp4_pitch(FMT, a.k);
     const bool live = r < a.rows;
@@ -332,6 +334,7 @@ template <int FMT, int TPR, typename In>
 __global__ void __launch_bounds__(ST) fp4_spread_kernel(const Fp4QuantArgs a, int per) {
     extern __shared__ __align__(16) unsigned char sm[];
     __shared__ uint32_t s_max[ST / 32];
+    wait_for_previous();
     const int tid = threadIdx.x;
     const int pitch = static_cast<int>(fp4_pitch(FMT, a.k)), half = a.k / 2;
     const int each = half + ((pitch + 15) & ~15);      // bytes of a row in shared memory
@@ -424,6 +427,7 @@ template <int FMT, int TPR, typename Out>
 __global__ void __launch_bounds__(QT) fp4_dequant_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
                                                          const float *__restrict__ row_scale, int layout, int rows, int k,
                                                          Out *__restrict__ out, size_t ldo) {
+    wait_for_previous();
     const int n = k / 16;
     const size_t pitch = fp4_pitch(FMT, k);
     const bool wide = ((reinterpret_cast<uintptr_t>(out) | ldo * sizeof(Out)) & 31) == 0;
@@ -470,39 +474,32 @@ cudaError_t launch_spread(const Fp4QuantArgs &a, int per, cudaStream_t st) {
     const size_t smem = (per + 1) * (a.k / 2 + ((fp4_pitch(FMT, a.k) + 15) & ~static_cast<size_t>(15)) + sizeof(float));
     const cudaError_t e = cudaFuncSetAttribute(fp4_spread_kernel<FMT, TPR, In>, cudaFuncAttributeMaxDynamicSharedMemorySize, SPREAD_SMEM);
     if (e != cudaSuccess) return e;
-    fp4_spread_kernel<FMT, TPR, In><<<(a.src_rows + per - 1) / per, ST, smem, st>>>(a, per);
-    return cudaGetLastError();
+    return launch_early(fp4_spread_kernel<FMT, TPR, In>, dim3((a.src_rows + per - 1) / per), ST, smem, st, 1, a, per);
 }
 
 template <int FMT, typename In>
 cudaError_t launch_quant(int layout, const Fp4QuantArgs &a, cudaStream_t st) {
     if (const int per = spread_rows<FMT>(layout, a)) return a.k <= 2048 ? launch_spread<FMT, 32, In>(a, per, st) : launch_spread<FMT, QT, In>(a, per, st);
     const int out_rows = layout == COLI_FP4_TILES ? (a.rows + 127) / 128 * 128 : a.rows;
-    if (a.k <= 2048) {
-        fp4_quant_kernel<FMT, 32, In><<<(out_rows + QT / 32 - 1) / (QT / 32), QT, 0, st>>>(a, layout, out_rows);
-    } else {
-        fp4_quant_kernel<FMT, QT, In><<<out_rows, QT, 0, st>>>(a, layout, out_rows);
-    }
-    return cudaGetLastError();
+    if (a.k <= 2048) return launch_early(fp4_quant_kernel<FMT, 32, In>, dim3((out_rows + QT / 32 - 1) / (QT / 32)), QT, 0, st, 1, a, layout, out_rows);
+    return launch_early(fp4_quant_kernel<FMT, QT, In>, dim3(out_rows), QT, 0, st, 1, a, layout, out_rows);
 }
 
 template <int FMT, int TPR>
-void launch_dequant_tpr(int layout, const uint8_t *codes, const uint8_t *scales, const float *row_scale, int rows, int k, int act,
+cudaError_t launch_dequant_tpr(int layout, const uint8_t *codes, const uint8_t *scales, const float *row_scale, int rows, int k, int act,
                         void *out, size_t ldo, cudaStream_t st) {
     const int want = (rows + QT / TPR - 1) / (QT / TPR), most = device_sm_count() * 64;
     const int grid = want < most ? want : most;
     if (act == COLI_ACT_F32)
-        fp4_dequant_kernel<FMT, TPR, float><<<grid, QT, 0, st>>>(codes, scales, row_scale, layout, rows, k, static_cast<float *>(out), ldo);
-    else
-        fp4_dequant_kernel<FMT, TPR, uint16_t><<<grid, QT, 0, st>>>(codes, scales, row_scale, layout, rows, k, static_cast<uint16_t *>(out), ldo);
+        return launch_early(fp4_dequant_kernel<FMT, TPR, float>, dim3(grid), QT, 0, st, 1, codes, scales, row_scale, layout, rows, k, static_cast<float *>(out), ldo);
+    return launch_early(fp4_dequant_kernel<FMT, TPR, uint16_t>, dim3(grid), QT, 0, st, 1, codes, scales, row_scale, layout, rows, k, static_cast<uint16_t *>(out), ldo);
 }
 
 template <int FMT>
 cudaError_t launch_dequant(int layout, const uint8_t *codes, const uint8_t *scales, const float *row_scale, int rows, int k, int act,
                            void *out, size_t ldo, cudaStream_t st) {
-    if (k <= 1024) launch_dequant_tpr<FMT, 32>(layout, codes, scales, row_scale, rows, k, act, out, ldo, st);
-    else launch_dequant_tpr<FMT, QT>(layout, codes, scales, row_scale, rows, k, act, out, ldo, st);
-    return cudaGetLastError();
+    if (k <= 1024) return launch_dequant_tpr<FMT, 32>(layout, codes, scales, row_scale, rows, k, act, out, ldo, st);
+    return launch_dequant_tpr<FMT, QT>(layout, codes, scales, row_scale, rows, k, act, out, ldo, st);
 }
 
 }  // namespace

@@ -15,6 +15,7 @@
 #include <type_traits>
 
 #include "internal.h"
+#include "pdl.h"
 
 namespace coli {
 
@@ -395,6 +396,7 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs &a, const float (&l)
 
 template <int VPL, bool BIAS, typename In>
 __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_scores_kernel(const RouteArgs a) {
+    wait_for_previous();
     const int lane = threadIdx.x & 31;
     const int t = blockIdx.x * ROUTE_WARPS + (threadIdx.x >> 5);
     if (t >= a.T) return;
@@ -458,7 +460,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_scores_kernel(const Ro
 }
 
 template <int VPL>
-void launch_vpl(RouteArgs a, int act, cudaStream_t st) {
+cudaError_t launch_vpl(RouteArgs a, int act, cudaStream_t st) {
     const int gs = a.E / a.G, seg = gs / VPL;
     const uintptr_t at = reinterpret_cast<uintptr_t>(a.logits) | (a.bias ? reinterpret_cast<uintptr_t>(a.bias) : 0) | (a.ld * (act == COLI_ACT_F32 ? 4 : 2));
     a.vec = a.E == 32 * VPL && at % 16 == 0;
@@ -468,13 +470,9 @@ void launch_vpl(RouteArgs a, int act, cudaStream_t st) {
     a.seg_shift = 0;
     while ((2 << a.seg_shift) <= seg) ++a.seg_shift;
     const int grid = (a.T + ROUTE_WARPS - 1) / ROUTE_WARPS;
-    if (a.bias) {
-        if (act == COLI_ACT_F32) route_scores_kernel<VPL, true, float><<<grid, ROUTE_WARPS * 32, 0, st>>>(a);
-        else route_scores_kernel<VPL, true, uint16_t><<<grid, ROUTE_WARPS * 32, 0, st>>>(a);
-    } else {
-        if (act == COLI_ACT_F32) route_scores_kernel<VPL, false, float><<<grid, ROUTE_WARPS * 32, 0, st>>>(a);
-        else route_scores_kernel<VPL, false, uint16_t><<<grid, ROUTE_WARPS * 32, 0, st>>>(a);
-    }
+    auto go = [&](auto kernel) { return launch_early(kernel, dim3(grid), ROUTE_WARPS * 32, 0, st, 1, a); };
+    if (a.bias) return act == COLI_ACT_F32 ? go(route_scores_kernel<VPL, true, float>) : go(route_scores_kernel<VPL, true, uint16_t>);
+    return act == COLI_ACT_F32 ? go(route_scores_kernel<VPL, false, float>) : go(route_scores_kernel<VPL, false, uint16_t>);
 }
 
 }  // namespace
@@ -497,13 +495,12 @@ cudaError_t launch_route_scores(const coli_moe_router &r, const void *logits, si
     a.ids = ids;
     a.w = w;
     const int vpl = (a.E + 31) / 32;
-    if (vpl <= 1) launch_vpl<1>(a, r.logits, st);
-    else if (vpl <= 2) launch_vpl<2>(a, r.logits, st);
-    else if (vpl <= 4) launch_vpl<4>(a, r.logits, st);
-    else if (vpl <= 8) launch_vpl<8>(a, r.logits, st);
-    else if (vpl <= 16) launch_vpl<16>(a, r.logits, st);
-    else launch_vpl<32>(a, r.logits, st);
-    return cudaGetLastError();
+    if (vpl <= 1) return launch_vpl<1>(a, r.logits, st);
+    if (vpl <= 2) return launch_vpl<2>(a, r.logits, st);
+    if (vpl <= 4) return launch_vpl<4>(a, r.logits, st);
+    if (vpl <= 8) return launch_vpl<8>(a, r.logits, st);
+    if (vpl <= 16) return launch_vpl<16>(a, r.logits, st);
+    return launch_vpl<32>(a, r.logits, st);
 }
 
 }  // namespace coli

@@ -12,6 +12,7 @@
 
 #include "fp4.h"
 #include "internal.h"
+#include "pdl.h"
 
 namespace coli {
 
@@ -87,6 +88,7 @@ template <int ACT>
 __global__ void __launch_bounds__(128) gate_few_kernel(const float *__restrict__ Wr, const void *__restrict__ x, int T, int H, int E,
                                                        float *__restrict__ logits) {
     __shared__ double s_part[4][GATE_TT];
+    wait_for_previous();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int e = blockIdx.x, t0 = blockIdx.y * GATE_TT;
     const float *wrow = Wr + static_cast<size_t>(e) * H;
@@ -484,8 +486,7 @@ cudaError_t launch_gate(const coli_moe_config &c, const float *Wr, const void *x
     const int H = c.hidden, E = c.n_experts;
     if (T <= GATE_FEW && fp4_wfmt(c.wfmt)) {
         const dim3 grid(E, (T + GATE_TT - 1) / GATE_TT);
-        if (c.act == COLI_ACT_F32) gate_few_kernel<COLI_ACT_F32><<<grid, 128, 0, st>>>(Wr, x, T, H, E, logits);
-        else gate_few_kernel<COLI_ACT_BF16><<<grid, 128, 0, st>>>(Wr, x, T, H, E, logits);
+        return launch_early(c.act == COLI_ACT_F32 ? gate_few_kernel<COLI_ACT_F32> : gate_few_kernel<COLI_ACT_BF16>, grid, 128, 0, st, 1, Wr, x, T, H, E, logits);
     } else if (T <= 16) {
         dim3 grid((E + 3) / 4);
         if (c.act == COLI_ACT_F32)
