@@ -166,6 +166,14 @@ struct GemmMaps {
     CUtensorMap sf, sfs;   // scale tiles {512 bytes, tiles, matrices} (pairs)
 };
 
+// The tensor maps the kernel starts with, on their way before their first use.
+__device__ __forceinline__ void prefetch_maps(const GemmMaps &m, int shared) {
+    auto one = [](const CUtensorMap *t) { asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(t)) : "memory"); };
+    one(&m.a);
+    one(&m.b[0]);
+    if (shared) one(&m.as);
+}
+
 struct Tile {
     int e, m, n0, nr;      // matrix, block of 128 weight rows, first row, rows
 };
@@ -213,17 +221,19 @@ __device__ __forceinline__ Tile tile_at(int t, const TileList &l, const GemmArgs
     return x;
 }
 
-// Fills the tile list (an exclusive scan of the matrices' tiles by the whole CTA); the number of tiles.
-template <int NT, int THREADS_>
+// Fills the tile list, by the N threads of the epilogue warps (named barrier 1) while the others set up the
+// rest: the offsets, and an exclusive scan of the matrices' tiles.  The number of tiles.
+template <int NT, int N>
 __device__ __forceinline__ int tile_list(const GemmArgs &p, int W, int MB, TileList &l, int *s_scan) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tid = threadIdx.x - W_EPI0 * 32, warp = tid >> 5, lane = tid & 31;
+    auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory"); };
     if (p.offsets) {
-        for (int e = threadIdx.x; e <= p.E; e += THREADS_) l.off[e] = __ldg(p.offsets + e);
-        __syncthreads();
+        for (int e = tid; e <= p.E; e += N) l.off[e] = __ldg(p.offsets + e);
+        sync();
     }
     int carry = 0;
-    for (int base = 0; base < W; base += THREADS_) {
-        const int e = base + threadIdx.x;
+    for (int base = 0; base < W; base += N) {
+        const int e = base + tid;
         int lo = 0, cnt = 0;
         if (e < W) group_rows(p, l, e, lo, cnt);
         if (cnt < 0) {
@@ -238,15 +248,15 @@ __device__ __forceinline__ int tile_list(const GemmArgs &p, int W, int MB, TileL
             if (lane >= o) inc += v;
         }
         if (lane == 31) s_scan[warp] = inc;
-        __syncthreads();
+        sync();
         int before = carry;
-        for (int w = 0; w < THREADS_ / 32; ++w) {
+        for (int w = 0; w < N / 32; ++w) {
             const int v = s_scan[w];
             if (w < warp) before += v;
             carry += v;
         }
         if (e < W) l.first[e] = before + inc - tiles;
-        __syncthreads();
+        sync();
     }
     return carry;
 }
@@ -426,7 +436,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
     constexpr bool SPLIT = NT <= 32;
     __shared__ __align__(8) uint64_t bars[3 * P::S + 7];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort;
+    __shared__ int s_abort, s_tiles;
     __shared__ TileList list;
     __shared__ int s_scan[THREADS / 32];
     uint64_t *full = bars, *sfull = full + P::S, *empty = sfull + P::S;
@@ -442,7 +452,6 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
     const int kb0 = KALL * rank / C, KT = KALL * (rank + 1) / C - kb0;
     const int W = p.E + p.S;
 
-    if (warp == 0) tmem_alloc(smem_u32(&s_tmem), 512);
     if (threadIdx.x == 32) {
         for (int i = 0; i < P::S; ++i) {
             mbar_init(smem_u32(&full[i]), 1);
@@ -459,14 +468,20 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
         s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (warp == W_SF) tmem_alloc(smem_u32(&s_tmem), 512);
+    if (warp == W_PROD && elect_one()) prefetch_maps(maps, p.S);
     wait_for_previous();
-    const int ntiles = tile_list<NT, THREADS>(p, W, MB, list, s_scan);
+    if (warp >= W_EPI0) {
+        const int n = tile_list<NT, N_EPI * 32>(p, W, MB, list, s_scan);
+        if (threadIdx.x == W_EPI0 * 32) s_tiles = n;
+    }
     tc_fence_before();
     __syncthreads();
     // the cluster's barriers are set up: waited for where another CTA's memory is first touched
     if (SPLIT && C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     tc_fence_after();
     const uint32_t tbase = s_tmem;
+    const int ntiles = s_tiles;
 
     if (warp == W_PROD) {
         // ------------------------------------------------------------------ TMA producer
@@ -596,7 +611,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
     tc_fence_before();
     __syncthreads();
     if (SPLIT && C > 1) cluster_sync_all();  // no CTA leaves while another may still write to it
-    if (warp == 0) {
+    if (warp == W_SF) {
         tc_fence_after();
         tmem_dealloc(tbase, 512);
     }
@@ -725,7 +740,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) fp4_pair_kernel(const __grid_con
     unsigned char *sa = sm, *sb = sa + P::S * A_BYTES, *ssa = sb + P::S * P::B_BYTES, *ssb = ssa + P::S * P::SFA_BYTES;
     __shared__ __align__(8) uint64_t bars[2 * P::S + 3];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort;
+    __shared__ int s_abort, s_tiles;
     __shared__ TileList list;
     __shared__ int s_scan[P_THREADS / 32];
     // full: the leader's, of both CTAs' copies; empty, dfull: in each CTA; dempty: the leader's
@@ -748,17 +763,22 @@ __global__ void __launch_bounds__(P_THREADS, 1) fp4_pair_kernel(const __grid_con
         s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 0) {
+    if (warp == W_SF) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512u) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    if (warp == W_PROD && elect_one()) prefetch_maps(maps, p.S);
     wait_for_previous();
-    const int ntiles = tile_list<P_NT, P_THREADS>(p, W, MB, list, s_scan);
+    if (warp >= W_EPI0) {
+        const int n = tile_list<P_NT, P_EPI * 32>(p, W, MB, list, s_scan);
+        if (threadIdx.x == W_EPI0 * 32) s_tiles = n;
+    }
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tbase = s_tmem;
+    const int ntiles = s_tiles;
 
     if (warp == W_PROD) {
         // ------------------------------------------------------------------ TMA producer
@@ -883,7 +903,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) fp4_pair_kernel(const __grid_con
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();
-    if (warp == 0) {
+    if (warp == W_SF) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(512u) : "memory");
     }
