@@ -143,11 +143,7 @@ lib = _load()
 
 
 def _p(t) -> Optional[int]:
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return t if t is None or t.__class__ is int else t.data_ptr()
 
 
 def _nbytes(t) -> int:
@@ -160,14 +156,19 @@ def _stream(stream) -> Optional[int]:
     return _current_stream()
 
 
+# torch's own functions for the current device and the handle of its current stream.  The handle alone:
+# building torch's Stream object takes longer (3.3 us against 0.1) than launching a small kernel.
+_torch_device = _torch_stream = None
+
+
 def _current_stream() -> int:
-    """Handle of the current device's current torch stream.  The handle alone: building torch's Stream
-    object takes longer (3.3 us against 0.1) than launching a small kernel."""
-    import torch
-    raw, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
-    if raw is None or dev is None or not torch.cuda.is_initialized():
-        return torch.cuda.current_stream().cuda_stream
-    return raw(dev())
+    global _torch_device, _torch_stream
+    if _torch_device is None:
+        import torch
+        if not torch.cuda.is_initialized() or not hasattr(torch._C, "_cuda_getCurrentRawStream"):
+            return torch.cuda.current_stream().cuda_stream
+        _torch_device, _torch_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    return _torch_stream(_torch_device())
 
 
 def _device_stream(fn: str, stream, t) -> Optional[int]:
@@ -176,8 +177,8 @@ def _device_stream(fn: str, stream, t) -> Optional[int]:
         return stream if isinstance(stream, int) else stream.cuda_stream
     st = _current_stream()
     if t is not None and not isinstance(t, int):
-        import torch
-        if t.get_device() != torch.cuda.current_device():  # (-1: not a CUDA tensor)
+        # (a first call on a tensor that is not on a GPU: torch's functions are not looked up then)
+        if _torch_device is None or t.get_device() != _torch_device():
             raise ColiError(fn, 1)
     return st
 
@@ -380,5 +381,6 @@ def fp4_rows_for(codes, scales, row_scale=None) -> FP4Rows:
 def fp4_mats_for(codes, scales, row_scale=None) -> FP4Mats:
     """FP4Mats over device tensors: codes [count, n, k/2] uint8, scales [count, bytes] uint8 in tiles,
     row_scale [count, n]."""
-    return FP4Mats(_p(codes), _p(scales), _p(row_scale), codes.shape[0], codes.shape[1], codes.stride(0), scales.stride(0),
+    count, n, _ = codes.shape
+    return FP4Mats(codes.data_ptr(), scales.data_ptr(), _p(row_scale), count, n, codes.stride(0), scales.stride(0),
                    0 if row_scale is None else row_scale.stride(0))

@@ -508,6 +508,7 @@ coli_status coli_moe_route_scores(const coli_moe_router *r, const void *logits, 
     if (T < 0) return COLI_ERR_SHAPE;
     if (ld == 0) ld = static_cast<size_t>(r->n_experts);
     if (ld < static_cast<size_t>(r->n_experts)) return COLI_ERR_SHAPE;
+    if (T > (1 << 30)) return COLI_ERR_UNSUPPORTED;
     if (T == 0) return COLI_OK;
     if (!logits || !topk_ids || !topk_w) return COLI_ERR_INVALID_ARG;
     if (!aligned(logits, r->logits == COLI_ACT_F32 ? 4 : 2) || (bias && !aligned(bias, 4)) || !aligned(topk_ids, 4) || !aligned(topk_w, 4))

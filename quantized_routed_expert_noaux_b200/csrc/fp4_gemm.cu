@@ -5,20 +5,24 @@
 // The block scales are applied by the tensor core (tcgen05.mma with block scales from tensor
 // memory), the row scales by the epilogue; sums are float32.
 //
-// Swap-AB: 128 weight rows of one matrix are the MMA's M side, up to NT rows of the matrix's group
-// its N side, so a weight tile is fetched once per NT rows.  Few rows per matrix are the rule (a
-// batch spread over many experts): the kernel is then a stream of weights from HBM, and the ring of
-// k-blocks (128 x 128 bytes of codes and their scales) is what keeps it full.
+// Swap-AB: weight rows of one matrix are the MMA's M side, rows of the matrix's group its N side, so a
+// weight tile is fetched once for as many rows as a tile has.  Few rows per matrix are the rule (a batch
+// spread over many experts): the kernel is then a stream of weights from HBM, and the ring of k-blocks
+// (128 x 128 bytes of codes and their scales) is what keeps it full.  Three tiles, chosen on the host:
+//   at most 32 rows in all      128 weight rows x 32, k split over a cluster where tiles are few
+//   fewer than PAIR_ROWS each   128 weight rows x 128
+//   more                        256 weight rows x 256 on a pair of CTAs
+// 64 matrices of 4096 x 6144 (NV) with 4 to 32 rows each stream at 6.4 to 6.6 TB/s, the copy peak; 8192
+// rows of one run at 4.3 to 4.9 PFLOP/s, where L2 gives a pair its operands at about 58 bytes per cycle and SM.
 //
-// One persistent CTA per SM, warp-specialised; tiles (matrix, 128 weight rows, chunk of rows; the
-// chunk fastest, so that a weight tile's second use comes from L2) are taken round-robin:
+// One persistent CTA per SM, warp-specialised; tiles are taken round-robin:
 //   warp 0      TMA producer: weight codes (128-byte swizzle), their scale tiles (one bulk copy: the
 //               tiles of a k-block are adjacent), and the rows' codes.
 //   warp 1      MMA issuer: copies the k-block's scales from shared to tensor memory
 //               (tcgen05.cp, 128 rows x 4 scales each) and issues 4 MMAs of K = 64.
 //   warps 2-3   scales of the rows, every other k-block each: from their rows through registers (the
-//               next k-block's loads in flight meanwhile) into the tile order that tcgen05.cp reads.
-//   warps 4-7   epilogue, from two accumulators: one drains while the other fills.
+//               next k-blocks' loads in flight meanwhile) into the tile order that tcgen05.cp reads.
+//   warps 4-7   epilogue, from two accumulators: one drains while the other fills (pairs: below).
 // Tensor memory: accumulators at columns [0, 256), scale stage s at 256 + s * SF_COLS.  A scale
 // stage goes with a ring stage, so it is written again only after the MMAs that read it have
 // completed (the ring's empty barrier).
@@ -38,7 +42,7 @@ namespace {
 
 constexpr int A_BYTES = 128 * 128;       // weight codes of a k-block
 constexpr int P_NT = 256;                // rows of a CTA pair's tile
-constexpr int BAND = 8;
+constexpr int BAND = 8;                  // weight blocks side by side in the order of the tiles
 constexpr int MAX_MATS = 1025;           // 1024 and a shared one
 constexpr int NBOX = 5;                  // box heights 16 << i rows
 constexpr int W_PROD = 0, W_MMA = 1, W_SF = 2, N_SF = 2, W_EPI0 = 4, N_EPI = 4;

@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(128) gate_rows_kernel(const float *__restrict_
 
 // The same sums for layers over 4-bit records, whose expert half leaves the gate little time: a CTA of 4
 // warps per expert row instead of a warp (GATE_TT tokens at a time; lanes, then warps, added in a fixed
-// order).  1 / 16 / 64 tokens, 256 experts, H 6144: 5 / 10 / GATE64 us against 36 / 159 / 96 (the kernel below, at 64).
+// order).  1 / 16 / 64 tokens, 256 experts, H 6144: 5 / 10 / 32 us against 36 / 159 / 96 (at 64: the
+// kernel below).
 constexpr int GATE_TT = 4, GATE_FEW = 64;
 
 template <int ACT>

@@ -222,6 +222,7 @@ def test_bad_calls_are_refused():
         assert ei.value.status == status
     refused(2, 256, 0, None, -1, 512, 1024)
     refused(2, 256, 63, None, 4, 512, 1024)
+    refused(4, 256, 0, None, (1 << 30) + 1, 512, 1024)
     refused(1, None, 0, None, 4, 512, 1024)
     refused(1, 256, 0, None, 4, None, 1024)
     refused(1, 256, 0, None, 4, 512, None)
