@@ -212,16 +212,21 @@ __device__ __forceinline__ Tile tile_at(int t, const TileList &l, const GemmArgs
     x.e = e;
     int row0, cnt;
     group_rows(p, l, e, row0, cnt);
-    const int nch = (cnt + NT - 1) / NT;
-    const int per = ((cnt + nch - 1) / nch + 31) & ~31;  // rows of a chunk: even shares
-    // bands of BAND weight blocks: a wave of tiles is BAND blocks times several chunks (against all chunks of
-    // one block after another: 2048 rows, 6144 x 2048, 25 us against 29)
     const int i = t - l.first[e];
-    const int band = i / (BAND * nch), j = i - band * (BAND * nch), high = min(BAND, MB - band * BAND);
-    const int c = j / high;
-    x.m = band * BAND + (j - c * high);
-    x.n0 = row0 + c * per;
-    x.nr = min(per, cnt - c * per);
+    x.m = i;
+    x.n0 = row0;
+    x.nr = cnt;
+    if (cnt > NT) {
+        const int nch = (cnt + NT - 1) / NT;
+        const int per = ((cnt + nch - 1) / nch + 31) & ~31;  // rows of a chunk: even shares
+        // bands of BAND weight blocks: a wave of tiles is BAND blocks times several chunks (against all chunks
+        // of one block after another: 2048 rows, 6144 x 2048, 25 us against 29)
+        const int band = i / (BAND * nch), j = i - band * (BAND * nch), high = min(BAND, MB - band * BAND);
+        const int c = j / high;
+        x.m = band * BAND + (j - c * high);
+        x.n0 = row0 + c * per;
+        x.nr = min(per, cnt - c * per);
+    }
     return x;
 }
 
