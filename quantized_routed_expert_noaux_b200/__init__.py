@@ -175,11 +175,14 @@ def _device_stream(fn: str, stream, t) -> Optional[int]:
     """_stream for a call whose tensors must live on the current device: t is one of them."""
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
+    if t is None or isinstance(t, int):
+        return _current_stream()
+    at = t.get_device()
+    if at < 0:  # not a CUDA tensor
+        raise ColiError(fn, 1)
     st = _current_stream()
-    if t is not None and not isinstance(t, int):
-        # (a first call on a tensor that is not on a GPU: torch's functions are not looked up then)
-        if _torch_device is None or t.get_device() != _torch_device():
-            raise ColiError(fn, 1)
+    if _torch_device is not None and at != _torch_device():
+        raise ColiError(fn, 1)
     return st
 
 

@@ -465,3 +465,95 @@ def test_product_refusals():
     refused(4, f, *call(a=A(rows=1 << 30), w=W(n=6144, codes_stride=6144 * 32, scales_stride=6144 * 16), ldo=6144))
     refused(7, f, *call(wsp=None))
     f(*call(a=A(rows=0, codes=None)), stream=0)
+
+
+# ------------------------------------------------------------------ the calls a user may make beside these
+
+
+@pytest.mark.gpu
+def test_far_apart():
+    """Matrices, rows of x and rows of out that lie more than 2^32 bytes apart."""
+    fmt, n, k, far = 1, 72, 96, 5 << 30
+    p = Product(fmt, [2, 1], n, k, exact=True)
+    codes = torch.empty(far + n * k // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(far + 128 * ref.pitch(fmt, k), dtype=torch.uint8, device="cuda")
+    for e in range(2):
+        codes[e * far:][:n * k // 2] = p.dev[3][e].reshape(-1)
+        scales[e * far:][:128 * ref.pitch(fmt, k)] = p.dev[4][e]
+    w = q.FP4Mats(codes.data_ptr(), scales.data_ptr(), p.dev[5].data_ptr(), 2, n, far, far, n)
+    ldo = (1 << 30) + 12
+    out = torch.empty(2 * ldo + n, device="cuda")
+    q.coli_moe_fp4_product(fmt, q.fp4_rows_for(*p.dev[:3]), w, k, p.dev_offsets, 0, out, ldo, ws())
+    y, _ = p.want()
+    for i in range(3):
+        assert np.array_equal(out[i * ldo:][:n].cpu().numpy().astype(np.float64), y[i])
+    del out, codes, scales
+    ldx = (1 << 31) + 32
+    x = torch.empty(2 * ldx + 64, dtype=torch.bfloat16, device="cuda")
+    rows = torch.randn(3, 64, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    for i in range(3):
+        x[i * ldx:][:64] = rows[i].cuda()
+    codes, scales, row = torch.empty(3, 32, dtype=torch.uint8, device="cuda"), torch.empty(3, 16, dtype=torch.uint8, device="cuda"), torch.empty(3, device="cuda")
+    w = ws()
+    q.coli_moe_fp4_quantize(1, 0, 1, x, 3, ldx, None, 1, 3, 64, codes, scales, row, w)
+    check_quantized((codes, scales.reshape(-1), row, w), rows.double().numpy(), 1, 0, 64)
+    q.coli_moe_fp4_dequantize(1, 0, codes, scales, row, 3, 64, 1, x, ldx)
+    code, byte, rs = ref.quantize(rows.double().numpy(), 1)
+    for i in range(3):  # at most 6 bits: exact in bf16
+        assert np.array_equal(x[i * ldx:][:64].double().cpu().numpy(), ref.values(code, byte, rs, 1)[i])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_two_streams_at_once(fmt):
+    """Products of different sizes on two streams, the weights shared, each with its own workspace and output."""
+    big, small = Product(fmt, [300, 0, 200], 512, 1024, exact=True), Product(fmt, [3], 512, 1024, exact=True, seed=7)
+    want = [p.want()[0] for p in (big, small)]
+    st = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[torch.zeros(p.rows, 512, device="cuda") for _ in range(8)] for p in (big, small)]
+    wss = [ws(), ws()]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for j, p in enumerate((big, small)):
+            with torch.cuda.stream(st[j]):
+                p.call(outs[j][i], 0, w=wss[j])
+    torch.cuda.synchronize()
+    for j in range(2):
+        for o in outs[j]:
+            assert np.array_equal(o.cpu().numpy().astype(np.float64), want[j])
+        assert q.coli_moe_error_word(wss[j]) == 0
+
+
+@pytest.mark.gpu
+def test_chained_on_one_stream():
+    """Kernels that are set up while the one before still runs see what it wrote: quantise, multiply, quantise
+    the result, multiply, many times over the same buffers, against the same steps one by one."""
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(40, 512, generator=g).to(torch.bfloat16).cuda()
+    w = (torch.randn(512, 512, generator=g) * 512 ** -0.5).to(torch.bfloat16).cuda()
+    wc, wsc, wr, _ = run_quantize(w, 1, layout=1)
+    mats = q.fp4_mats_for(wc[None], wsc[None], wr[None])
+
+    def chain(wait):
+        y = x.clone()
+        codes, scales, row = torch.empty(40, 256, dtype=torch.uint8, device="cuda"), torch.empty(40, 32, dtype=torch.uint8, device="cuda"), torch.empty(40, device="cuda")
+        rows = q.fp4_rows_for(codes, scales, row)
+        W = ws()
+        for _ in range(30):
+            q.coli_moe_fp4_quantize(1, 0, 1, y, 40, 512, None, 1, 40, 512, codes, scales, row, W)
+            wait()
+            q.coli_moe_fp4_product(1, rows, mats, 512, None, 1, y, 512, W)
+            wait()
+        torch.cuda.synchronize()
+        return y.cpu()
+    one = chain(torch.cuda.synchronize)
+    assert torch.isfinite(one.float()).all() and one.float().abs().max() > 0
+    for _ in range(5):
+        assert torch.equal(chain(lambda: None), one)
+
+
+def test_tensors_off_the_gpu_are_refused():
+    x = torch.zeros(1, 64)
+    with pytest.raises(q.ColiError) as ei:
+        q.coli_moe_fp4_quantize(1, 0, 0, x, 1, 64, None, 1, 1, 64, x, x, x, 256)
+    assert ei.value.status == 1
