@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(QT) fp4_quant_kernel(const Fp4QuantArgs a, int
 // Rows of an index that takes every source row several times (the slots of a token's experts): a CTA
 // quantises `per` source rows once, ST / TPR at a time, into shared memory, then goes through the whole index;
 // a thread that meets one of them starts its bulk copies to the row that asks for it.  The index is read
-// gridDim.x times, from L2.  Rows whose index is bad are the first CTA's, copies of a row of zeros.  16,384 rows of 6144 bf16 elements from 2048 (NV): 29 us against
+// gridDim.x times, from L2.  Rows whose index is bad are the first CTA's, copies of a row of zeros.  16,384 rows of 6144 bf16 elements from 2048 (NV): 22 us against
 // 49 with every row quantised by itself; 4096 rows from 512, 7 against 14.
 constexpr int ST = 256, SEG = 4096;
 constexpr int SPREAD_SMEM = 88 * 1024;  // two CTAs per SM at least
@@ -331,7 +331,7 @@ constexpr int SPREAD_MIN = 1024;        // rows
 constexpr int SPREAD_CTAS = 512;        // at most, about: what the passes over the index cost
 
 template <int FMT, int TPR, typename In>
-__global__ void __launch_bounds__(ST) fp4_spread_kernel(const Fp4QuantArgs a, int per) {
+__global__ void __launch_bounds__(ST, sizeof(In) == 2 ? 4 : 2) fp4_spread_kernel(const Fp4QuantArgs a, int per) {
     extern __shared__ __align__(16) unsigned char sm[];
     __shared__ uint32_t s_max[ST / 32];
     wait_for_previous();
