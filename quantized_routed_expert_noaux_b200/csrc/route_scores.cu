@@ -252,6 +252,14 @@ __device__ __forceinline__ void choose_exact(const RouteArgs &a, const float (&l
     }
 }
 
+// 1 / (1 + 2^(-l log2 e)) by the approximate instructions: ex2 within 2^-22, rcp within 2^-23 of their results.
+__device__ __forceinline__ float sigmoid_fast(float l) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
+
 // Descending order of a lane's keys (Batcher's odd-even merge sort; VPL a power of two).
 template <int VPL>
 __device__ __forceinline__ void sort_keys(uint32_t (&k)[VPL]) {
@@ -274,8 +282,8 @@ __device__ __forceinline__ void sort_keys(uint32_t (&k)[VPL]) {
 // lie too close (with random float32 logits about one token in a hundred), or fewer than K can be chosen.
 // The place of an expert among its lane's is kept in the last bits of its key, VPL - 1 - place, so a
 // lane's keys can be sorted; a pick is then one redux.sync of the first keys and a shift in one lane.
-// Errors in units of 2^-24.  With a bias: sigmoid, __expf's (2 + 1.17 |l|) 2^-23 of exp(-l), of which s takes
-// s (1 - s), and the division's 2^-22 make 8; softmax, expf's 4, its argument's rounding 1, a sum of VPL
+// Errors in units of 2^-24.  With a bias: sigmoid, (4 + 1.5 |l|) of exp(-l), of which s takes s (1 - s), the
+// sum's 1 and the reciprocal's 2 make 5; softmax, expf's 4, its argument's rounding 1, a sum of VPL
 // terms per lane and 5 rounds VPL + 5 of s; the sum with the bias 1 of c.  The place costs 2 VPL units of |c|, or
 // of |l| without a bias; of bf16 logits it takes bits that are zero, and equal logits come in the order of
 // their ids.  Groups by two scores without a bias: the scores' errors alone.
@@ -284,7 +292,7 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs &a, const float (&l)
     constexpr bool EXACT = !BIAS && sizeof(In) == 2;
     constexpr float UNIT = 5.9604644775390625e-8f;  // 2^-24
     const bool groups = a.TG < a.G, top2 = groups && !a.group_max;
-    float c[VPL], most = 0.f, smax = 1.f;
+    float c[VPL], smax = 1.f;
     if (a.softmax) {
         top = l[0];
 #pragma unroll
@@ -305,7 +313,7 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs &a, const float (&l)
         smax = 1.0f / fs;
     } else if (!a.softmax && (BIAS || top2)) {
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) c[v] = __fdividef(1.0f, 1.0f + __expf(-fmaxf(l[v], -60.0f)));
+        for (int v = 0; v < VPL; ++v) c[v] = sigmoid_fast(fmaxf(l[v], -60.0f));
     }
     if (BIAS) {
         float bias[VPL];
@@ -317,17 +325,13 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs &a, const float (&l)
         }
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
-            const float f = (a.softmax ? c[v] * smax : c[v]) + bias[v];  // (l is -inf behind the last expert)
-            c[v] = l[v] > -INFINITY && f > -INFINITY ? f : -INFINITY;
+            const float f = fmaxf((a.softmax ? c[v] * smax : c[v]) + bias[v], -INFINITY);  // NaN: not to be chosen
+            c[v] = l[v] > -INFINITY ? f : -INFINITY;  // (l is -inf behind the last expert)
         }
     }
     auto value = [&](int v) { return BIAS ? c[v] : l[v]; };
-    if (!EXACT) {
-#pragma unroll
-        for (int v = 0; v < VPL; ++v) most = fmaxf(most, value(v) > -INFINITY ? fabsf(value(v)) : 0.f);
-        most = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(most)));
-    }
-    const float tol = UNIT * ((BIAS ? (VPL + 16) * (smax + most) : 0.f) + 2 * VPL * most);
+    // how far a float32 value of magnitude m may be off
+    auto off = [&](float m) { return UNIT * ((BIAS ? (VPL + 16) * (smax + m) : 0.f) + 2 * VPL * m); };
     bool mine = true;  // this lane's experts are of a group that is kept
     if (groups) {
         // a group's lanes: 1 << seg_shift of them (the launcher's rule)
@@ -345,16 +349,29 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs &a, const float (&l)
         }
         const int g = lane >> a.seg_shift;
         const float r = g >= a.G ? -INFINITY : (top2 && b2 > -INFINITY ? b1 + b2 : b1);
-        // sums of softmax numerators: relative to the largest, 1
-        const float gtol = BIAS ? 4.0f * tol : (top2 ? 4.0f * UNIT * (VPL + 16) : 0.f);
-        int above = 0, near = 0;  // groups certainly before this one; groups too close to tell
-        for (int o = 0; o < a.G; ++o) {
-            const float q = __shfl_sync(FULL, r, o << a.seg_shift);
-            above += q > r + gtol;
-            near += o != g && fabsf(q - r) <= gtol;
-            if (!BIAS && !top2) {  // the logits themselves: ties go to the lower group
-                above += q == r && o < g;
-                near = 0;
+        // how close two ranks may be: with a bias by the largest magnitudes that were added; sums of scores
+        // without one by the scores' errors (softmax numerators: relative to the largest, 1)
+        float gtol = 0.f;
+        if (BIAS) {
+            const float mag = fabsf(b1) + (top2 ? fabsf(b2) : 0.f);
+            gtol = 4.0f * off(__uint_as_float(__reduce_max_sync(FULL, mag < INFINITY ? __float_as_uint(mag) : 0u)));
+        } else if (top2) {
+            gtol = 4.0f * UNIT * (VPL + 16);
+        }
+        int above = 0, near = 0;  // groups certainly before this one; groups too close to tell (and itself)
+        if (BIAS || top2) {
+#pragma unroll 4
+            for (int o = 0; o < a.G; ++o) {
+                const float d = __shfl_sync(FULL, r, o << a.seg_shift) - r;
+                above += d > gtol;
+                near += fabsf(d) <= gtol;
+            }
+            near -= r > -INFINITY;
+        } else {  // the logits themselves: ties go to the lower group
+#pragma unroll 4
+            for (int o = 0; o < a.G; ++o) {
+                const float q = __shfl_sync(FULL, r, o << a.seg_shift);
+                above += q > r || (q == r && o < g);
             }
         }
         mine = above + near < a.TG;
@@ -362,13 +379,22 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs &a, const float (&l)
         // to choose: leave the token to the exact choice
         if (__any_sync(FULL, g < a.G && ((near > 0 && above < a.TG && !mine) || (mine && r == -INFINITY)))) return false;
     }
+    // (-inf has a key too, below every other's: NONE and up are values that can be chosen)
+    constexpr uint32_t NONE = 0x00800000u;
     uint32_t key[VPL];
 #pragma unroll
-    for (int v = 0; v < VPL; ++v)
-        key[v] = mine && value(v) > -INFINITY ? (key32(value(v)) & ~static_cast<uint32_t>(VPL - 1)) | static_cast<uint32_t>(VPL - 1 - v) : 0u;
+    for (int v = 0; v < VPL; ++v) {
+        const uint32_t b = __float_as_uint(value(v) + 0.0f);  // -0 and +0 are one value
+        const uint32_t k = b ^ (static_cast<uint32_t>(static_cast<int>(b) >> 31) | 0x80000000u);
+        key[v] = (k & ~static_cast<uint32_t>(VPL - 1)) | static_cast<uint32_t>(VPL - 1 - v);
+    }
     sort_keys<VPL>(key);
+    if (!mine) {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) key[v] = 0u;
+    }
     uint32_t got = 0u;  // lane n: key of pick n
-    my_id = -1;
+    int from = 0;       // and the lane it came from
     for (int n = 0; n < a.K; ++n) {
         const uint32_t m = __reduce_max_sync(FULL, key[0]);
         // (equal logits: the lowest lane has the lowest id, whatever the place in the key says)
@@ -377,7 +403,7 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs &a, const float (&l)
         const uint32_t k = EXACT ? __shfl_sync(FULL, key[0], owner) : m;
         if (lane == n) {
             got = k;
-            my_id = owner * VPL + (VPL - 1 - static_cast<int>(k & (VPL - 1)));
+            from = owner;
         }
         if (lane == owner) {
 #pragma unroll
@@ -385,12 +411,14 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs &a, const float (&l)
             key[VPL - 1] = 0u;
         }
     }
-    if (EXACT) return !__any_sync(FULL, lane < a.K && got == 0u);
+    my_id = from * VPL + (VPL - 1 - static_cast<int>(got & (VPL - 1)));
+    if (EXACT) return !__any_sync(FULL, lane < a.K && got < NONE);
     // every pick has to be clear of the next one, and the last of the best that was left
     const uint32_t left = __reduce_max_sync(FULL, key[0]);
     uint32_t next = __shfl_down_sync(FULL, got, 1);
     if (lane == a.K - 1) next = left;
-    const bool clear = lane >= a.K || (got != 0u && (next == 0u || unkey32(got) - unkey32(next) > 2.0f * tol));
+    const float x = unkey32(got), y = unkey32(next);
+    const bool clear = lane >= a.K || (got >= NONE && (next < NONE || x - y > 2.0f * off(fmaxf(fabsf(x), fabsf(y)))));
     return __all_sync(FULL, clear);
 }
 
@@ -406,12 +434,12 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_scores_kernel(const Ro
     if (VPL * sizeof(In) >= 16 && a.vec) {  // 16-byte loads: E = 32 VPL and rows are aligned
         load_run<VPL>(row + e0, l);
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) l[v] = l[v] > -INFINITY ? l[v] : -INFINITY;
+        for (int v = 0; v < VPL; ++v) l[v] = fmaxf(l[v], -INFINITY);  // NaN masks as -inf does
     } else {
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
             const float x = load_one(row + min(e0 + v, a.E - 1));
-            l[v] = e0 + v < a.E && x > -INFINITY ? x : -INFINITY;  // NaN masks as -inf does
+            l[v] = e0 + v < a.E ? fmaxf(x, -INFINITY) : -INFINITY;
         }
     }
     int my_id, chosen = a.K;
