@@ -174,16 +174,15 @@ def _current_stream() -> int:
 def _device_stream(fn: str, stream, t) -> Optional[int]:
     """_stream for a call whose tensors must live on the current device: t is one of them."""
     if stream is not None:
-        return stream if isinstance(stream, int) else stream.cuda_stream
-    if t is None or isinstance(t, int):
+        return stream if stream.__class__ is int else stream.cuda_stream
+    if t is None or t.__class__ is int:
         return _current_stream()
     at = t.get_device()
-    if at < 0:  # not a CUDA tensor
+    if _torch_device is None and at >= 0:
+        _current_stream()
+    if at < 0 or (_torch_device is not None and at != _torch_device()):  # (-1: not a CUDA tensor)
         raise ColiError(fn, 1)
-    st = _current_stream()
-    if _torch_device is not None and at != _torch_device():
-        raise ColiError(fn, 1)
-    return st
+    return _torch_stream(at) if _torch_device is not None else _current_stream()
 
 
 def _check(fn: str, status: int) -> None:
@@ -328,12 +327,16 @@ def coli_moe_check_router(router: MoERouter) -> None:
     _check("coli_moe_check_router", lib.coli_moe_check_router(C.byref(router)))
 
 
+# The calls below may run every few microseconds (one decoded token through a router or a linear layer), so
+# they pass structures and pointers to ctypes without helpers in between.
+
 def coli_moe_route_scores(router: MoERouter, logits, ld, bias, T, topk_ids, topk_w, stream=None) -> None:
     """Softmax or sigmoid routing of T tokens: row t of the logits at element t * ld (0: n_experts),
     bias [E] float32 or None."""
-    _check("coli_moe_route_scores", lib.coli_moe_route_scores(
-        C.byref(router), _p(logits), ld, _p(bias), T, _p(topk_ids), _p(topk_w),
-        _device_stream("coli_moe_route_scores", stream, logits)))
+    st = _device_stream("coli_moe_route_scores", stream, logits)
+    status = lib.coli_moe_route_scores(router, _p(logits), ld, _p(bias), T, _p(topk_ids), _p(topk_w), st)
+    if status:
+        raise ColiError("coli_moe_route_scores", status)
 
 
 def coli_moe_fp4_scale_pitch(fmt: int, k: int) -> int:
@@ -352,22 +355,27 @@ def coli_moe_fp4_quantize(fmt, layout, act, x, src_rows, ldx, row_index, row_div
                           stream=None) -> None:
     """Rows of x (row i at element i * ldx) to 4-bit codes, block scales and row scales; row r of the
     result is source row r, or row_index[r] // row_div."""
-    _check("coli_moe_fp4_quantize", lib.coli_moe_fp4_quantize(
-        fmt, layout, act, _p(x), src_rows, ldx, _p(row_index), row_div, rows, k, _p(codes), _p(scales), _p(row_scale),
-        _p(ws), _device_stream("coli_moe_fp4_quantize", stream, x)))
+    st = _device_stream("coli_moe_fp4_quantize", stream, x)
+    status = lib.coli_moe_fp4_quantize(fmt, layout, act, _p(x), src_rows, ldx, _p(row_index), row_div, rows, k, _p(codes),
+                                       _p(scales), _p(row_scale), _p(ws), st)
+    if status:
+        raise ColiError("coli_moe_fp4_quantize", status)
 
 
 def coli_moe_fp4_dequantize(fmt, layout, codes, scales, row_scale, rows, k, act, out, ldo, stream=None) -> None:
-    _check("coli_moe_fp4_dequantize", lib.coli_moe_fp4_dequantize(
-        fmt, layout, _p(codes), _p(scales), _p(row_scale), rows, k, act, _p(out), ldo,
-        _device_stream("coli_moe_fp4_dequantize", stream, out)))
+    """The values that codes, block scales and row scales stand for, rounded to act; row r at out + r * ldo."""
+    st = _device_stream("coli_moe_fp4_dequantize", stream, out)
+    status = lib.coli_moe_fp4_dequantize(fmt, layout, _p(codes), _p(scales), _p(row_scale), rows, k, act, _p(out), ldo, st)
+    if status:
+        raise ColiError("coli_moe_fp4_dequantize", status)
 
 
 def coli_moe_fp4_product(fmt, a: FP4Rows, w: FP4Mats, k, offsets, out_type, out, ldo, ws, stream=None) -> None:
     """out row i = a's row i times the matrix of its group (offsets [count + 1] int32; None: one matrix)."""
-    _check("coli_moe_fp4_product", lib.coli_moe_fp4_product(
-        fmt, C.byref(a), C.byref(w), k, _p(offsets), out_type, _p(out), ldo, _p(ws),
-        _device_stream("coli_moe_fp4_product", stream, out)))
+    st = _device_stream("coli_moe_fp4_product", stream, out)
+    status = lib.coli_moe_fp4_product(fmt, a, w, k, _p(offsets), out_type, _p(out), ldo, _p(ws), st)
+    if status:
+        raise ColiError("coli_moe_fp4_product", status)
 
 
 def coli_moe_fp4_pack_record(cfg: MoEConfig, act, wg, wu, wd, record, ws, stream=None) -> None:
@@ -378,7 +386,7 @@ def coli_moe_fp4_pack_record(cfg: MoEConfig, act, wg, wu, wd, record, ws, stream
 
 def fp4_rows_for(codes, scales, row_scale=None) -> FP4Rows:
     """FP4Rows over device tensors: codes [rows, k/2] uint8, scales [rows, pitch] uint8, row_scale [rows]."""
-    return FP4Rows(_p(codes), _p(scales), _p(row_scale), codes.shape[0])
+    return FP4Rows(codes.data_ptr(), scales.data_ptr(), _p(row_scale), codes.shape[0])
 
 
 def fp4_mats_for(codes, scales, row_scale=None) -> FP4Mats:
