@@ -393,5 +393,5 @@ def fp4_mats_for(codes, scales, row_scale=None) -> FP4Mats:
     """FP4Mats over device tensors: codes [count, n, k/2] uint8, scales [count, bytes] uint8 in tiles,
     row_scale [count, n]."""
     count, n, _ = codes.shape
-    return FP4Mats(codes.data_ptr(), scales.data_ptr(), _p(row_scale), count, n, codes.stride(0), scales.stride(0),
-                   0 if row_scale is None else row_scale.stride(0))
+    return FP4Mats(codes.data_ptr(), scales.data_ptr(), _p(row_scale), count, n, codes.stride()[0], scales.stride()[0],
+                   0 if row_scale is None else row_scale.stride()[0])
