@@ -142,17 +142,17 @@ def test_expert_half(wfmt, T, H, I, E, K, shared, act):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("wfmt", [20, 36])
-@pytest.mark.parametrize("T", [1, 6, 130])
-def test_whole_layer(wfmt, T):
+@pytest.mark.parametrize("T,act", [(1, 1), (6, 0), (64, 1), (65, 0), (130, 1)])
+def test_whole_layer(wfmt, T, act):
     """The layer is its parts: routing as coli_moe_route_scores gives it (and coli_moe_route, but for the last
     bits of its weights), the expert half on that routing, bit for bit; replayed from a graph with new
     activations too; and without allocation."""
-    cfg = config(wfmt)
+    cfg = config(wfmt, act=act)
     assert q.coli_moe_layer_kernels(cfg, T) == 8
     ex = Experts(cfg)
     H, K = cfg.hidden, cfg.top_k
     g = torch.Generator().manual_seed(T)
-    xs = [torch.randn(T, H, generator=g).to(torch.bfloat16).cuda() for _ in range(2)]
+    xs = [torch.randn(T, H, generator=g).to(torch.bfloat16 if act else torch.float32).cuda() for _ in range(2)]
     ws = torch.zeros(q.coli_moe_workspace_size(cfg, T), dtype=torch.uint8, device="cuda")
     ids, w = torch.empty(T, K, dtype=torch.int32, device="cuda"), torch.empty(T, K, device="cuda")
 
