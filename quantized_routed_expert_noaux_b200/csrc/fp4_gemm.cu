@@ -443,12 +443,12 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
     unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char *sa = sm, *sb = sa + P::S * A_BYTES, *ssa = sb + P::S * P::B_BYTES, *ssb = ssa + P::S * P::SFA_BYTES;
     constexpr bool SPLIT = NT <= 32;
-    __shared__ __align__(8) uint64_t bars[3 * P::S + 7];
+    __shared__ __align__(8) uint64_t bars[2 * P::S + 7];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_tiles;
     __shared__ TileList list;
     __shared__ int s_scan[THREADS / 32];
-    uint64_t *full = bars, *sfull = full + P::S, *empty = sfull + P::S;
+    uint64_t *full = bars, *empty = full + P::S;
     uint64_t *dfull = empty + P::S, *dempty = dfull + 2, *drain = dempty + 2;
     uint64_t *pfull = drain + 1, *pfree = pfull + 1;  // split k: partial sums there; their place free again
     float *part = reinterpret_cast<float *>(ssb + P::S * P::SFB_BYTES);
@@ -463,8 +463,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
 
     if (threadIdx.x == 32) {
         for (int i = 0; i < P::S; ++i) {
-            mbar_init(smem_u32(&full[i]), 1);
-            mbar_init(smem_u32(&sfull[i]), 1);
+            mbar_init(smem_u32(&full[i]), 2);  // the producer and a row-scale warp
             mbar_init(smem_u32(&empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -498,7 +497,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
         // 16 << i rows for every bit i of the row count (from lanes that differ, or behind a test of the
         // lane, a copy took the compiler's loop over lanes and 200 cycles)
         const size_t mtile = 128 * fp4_pitch(FMT, p.k);  // scale bytes of 128 weight rows
-        uint32_t it = 0;
+        uint32_t it = 0, s = 0, phase = 1;
         for (int t = first; t < ntiles; t += stride) {
             const Tile x = tile_at<NT>(t, list, p, W);
             const bool shared = x.e >= p.E;
@@ -507,8 +506,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
             const uint8_t *wsf = (shared ? p.wsf_shared : p.wsf + static_cast<size_t>(x.e) * p.wsf_stride) + static_cast<size_t>(x.m) * mtile;
             const int n16 = (x.nr + 15) / 16;
             for (int kb = 0; kb < KT; ++kb, ++it) {
-                const int s = it % P::S;
-                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[s]), ((it / P::S) & 1) ^ 1, abort, p.err))) goto prod_done;
+                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[s]), phase, abort, p.err))) goto prod_done;
                 const uint32_t fb = smem_u32(&full[s]);
                 if (elect_one()) {
                     mbar_expect_tx(fb, A_BYTES + P::SFA_BYTES + n16 * 16 * 128);
@@ -521,6 +519,10 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
                     }
                 }
                 __syncwarp();
+                if (++s == P::S) {
+                    s = 0;
+                    phase ^= 1;
+                }
             }
         }
     prod_done:
@@ -531,7 +533,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
         }
     } else if (warp == W_MMA) {
         // ------------------------------------------------------------------ MMA issuer
-        uint32_t it = 0, tl = 0;
+        uint32_t s = 0, phase = 0, tl = 0;
         const uint64_t adesc0 = smem_desc_sw128(smem_u32(sa)), bdesc0 = smem_desc_sw128(smem_u32(sb));
         const uint64_t sadesc0 = smem_desc_sf(smem_u32(ssa)), sbdesc0 = smem_desc_sf(smem_u32(ssb));
         for (int t = first; t < ntiles; t += stride, ++tl) {
@@ -542,10 +544,8 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
             if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&dempty[acc]), ((tl >> 1) & 1) ^ 1, abort, p.err))) goto mma_done;
             tc_fence_after();
             const uint32_t dt = tbase + acc * 128;
-            for (int kb = 0; kb < KT; ++kb, ++it) {
-                const int s = it % P::S;
-                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[s]), (it / P::S) & 1, abort, p.err))) goto mma_done;
-                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sfull[s]), (it / P::S) & 1, abort, p.err))) goto mma_done;
+            for (int kb = 0; kb < KT; ++kb) {
+                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[s]), phase, abort, p.err))) goto mma_done;
                 tc_fence_after();
                 const int steps = min(4, (p.k - (kb0 + kb) * FP4_KB + 63) / 64);  // K = 64 steps that hold elements
                 if (elect_one()) {
@@ -570,6 +570,10 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
                     mma_commit(smem_u32(&empty[s]));
                 }
                 __syncwarp();
+                if (++s == P::S) {
+                    s = 0;
+                    phase ^= 1;
+                }
             }
             if (elect_one()) mma_commit(smem_u32(&dfull[acc]));
             __syncwarp();
@@ -582,7 +586,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
     } else if (warp < W_EPI0) {
         // ------------------------------------------------------------------ scales of the rows
         row_scales<FMT, NT>(p, warp - W_SF, first, stride, ntiles, KT, list, W, ssb, empty, P::S, kb0, abort,
-                            [&](int st) { mbar_arrive(smem_u32(&sfull[st])); });
+                            [&](int st) { mbar_arrive(smem_u32(&full[st])); });
     } else {
         // ------------------------------------------------------------------ epilogue
         const int q = warp - W_EPI0;  // TMEM lane quarter (warp % 4)
