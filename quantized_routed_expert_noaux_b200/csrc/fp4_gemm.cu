@@ -796,7 +796,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) fp4_pair_kernel(const __grid_con
     if (warp == W_PROD) {
         // ------------------------------------------------------------------ TMA producer
         const int atoms = static_cast<int>(fp4_pitch(FMT, p.k) / 4);  // scale tiles of 128 weight rows
-        uint32_t it = 0;
+        uint32_t s = 0, phase = 1;
         for (int t = pair; t < ntiles; t += pairs) {
             const Tile x = tile_at<P_NT>(t, list, p, W);
             const bool shared = x.e >= p.E;
@@ -804,9 +804,8 @@ __global__ void __launch_bounds__(P_THREADS, 1) fp4_pair_kernel(const __grid_con
             const int ez = shared ? 0 : x.e;
             const int n32 = (x.nr + 31) / 32;                        // N / 32; this CTA's share is 16 * n32 rows
             const int row_lo = x.n0 + static_cast<int>(rank) * 16 * n32;
-            for (int kb = 0; kb < KT; ++kb, ++it) {
-                const int s = it % P::S;
-                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[s]), ((it / P::S) & 1) ^ 1, abort, p.err))) goto prod_done;
+            for (int kb = 0; kb < KT; ++kb) {
+                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[s]), phase, abort, p.err))) goto prod_done;
                 const uint32_t fb = map_rank(smem_u32(&full[s]), 0);
                 if (elect_one()) {
                     remote_expect_tx(fb, A_BYTES + P::SFA_BYTES + n32 * 16 * 128);
@@ -819,6 +818,10 @@ __global__ void __launch_bounds__(P_THREADS, 1) fp4_pair_kernel(const __grid_con
                     }
                 }
                 __syncwarp();
+                if (++s == P::S) {
+                    s = 0;
+                    phase ^= 1;
+                }
             }
         }
     prod_done:
@@ -827,7 +830,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) fp4_pair_kernel(const __grid_con
         ;
     } else if (warp == W_MMA && rank == 0) {
         // ------------------------------------------------------------------ MMA issuer (the pair's)
-        uint32_t it = 0, tl = 0;
+        uint32_t s = 0, phase = 0, tl = 0;
         const uint64_t adesc0 = smem_desc_sw128(smem_u32(sa)), bdesc0 = smem_desc_sw128(smem_u32(sb));
         const uint64_t sadesc0 = smem_desc_sf(smem_u32(ssa)), sbdesc0 = smem_desc_sf(smem_u32(ssb));
         for (int t = pair; t < ntiles; t += pairs, ++tl) {
@@ -836,9 +839,8 @@ __global__ void __launch_bounds__(P_THREADS, 1) fp4_pair_kernel(const __grid_con
             const uint32_t idesc = (idesc_fp4<FMT>() & ~(3u << 27)) | (2u << 27) | (static_cast<uint32_t>(4 * n32) << 17);
             if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(dempty), (tl & 1) ^ 1, abort, p.err))) goto mma_done;
             tc_fence_after();
-            for (int kb = 0; kb < KT; ++kb, ++it) {
-                const int s = it % P::S;
-                if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&full[s]), (it / P::S) & 1, abort, p.err))) goto mma_done;
+            for (int kb = 0; kb < KT; ++kb) {
+                if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&full[s]), phase, abort, p.err))) goto mma_done;
                 tc_fence_after();
                 const int steps = min(4, (p.k - kb * FP4_KB + 63) / 64);
                 if (elect_one()) {
@@ -862,6 +864,10 @@ __global__ void __launch_bounds__(P_THREADS, 1) fp4_pair_kernel(const __grid_con
                     pair_commit(smem_u32(&empty[s]));
                 }
                 __syncwarp();
+                if (++s == P::S) {
+                    s = 0;
+                    phase ^= 1;
+                }
             }
             if (elect_one()) pair_commit(smem_u32(dfull));
             __syncwarp();
@@ -871,8 +877,15 @@ __global__ void __launch_bounds__(P_THREADS, 1) fp4_pair_kernel(const __grid_con
             asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(drain)) : "memory");
         __syncwarp();
         mbar_drain(smem_u32(drain), 0);
-        if (*abort)  // copies that are still in flight land before shared memory is released
-            for (uint32_t i = it; i < it + P::S; ++i) mbar_drain(smem_u32(&full[i % P::S]), (i / P::S) & 1);
+        if (*abort) {  // copies that are still in flight land before shared memory is released
+            for (int i = 0; i < P::S; ++i) {
+                mbar_drain(smem_u32(&full[s]), phase);
+                if (++s == P::S) {
+                    s = 0;
+                    phase ^= 1;
+                }
+            }
+        }
     } else if (warp == W_SF || warp == W_SF + 1) {
         // ------------------------------------------------------------------ scales of the rows
         row_scales<FMT, P_NT>(p, warp - W_SF, pair, pairs, ntiles, KT, list, W, ssb, empty, P::S, 0, abort,
