@@ -614,6 +614,7 @@ coli_status coli_moe_fp4_product(int fmt, const coli_fp4_rows *a, const coli_fp4
     p.a = *a;
     p.w = *w;
     p.shared = nullptr;
+    p.shared_rows = 0;
     p.k = k;
     p.offsets = offsets;
     p.out_kind = out_type == COLI_ACT_F32 ? FP4_OUT_F32 : FP4_OUT_BF16;

@@ -46,6 +46,7 @@ struct Fp4ProductArgs {
     coli_fp4_rows a;
     coli_fp4_mats w;
     const coli_fp4_mats *shared;  // one more matrix for the rows offsets[count] .. a.rows - 1, or nullptr
+    int shared_rows;              // how many those are when every row has its group
     int k;
     const int32_t *offsets;
     int out_kind;

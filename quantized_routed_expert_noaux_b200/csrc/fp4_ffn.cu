@@ -93,6 +93,7 @@ cudaError_t launch_ffn_fp4(const FfnParams &f, int wfmt, const Fp4Buffers &b, cu
     p.w = mats(f.experts, f.E, false);
     coli_fp4_mats shared = f.S ? mats(f.shared, 1, false) : p.w;
     p.shared = f.S ? &shared : nullptr;
+    p.shared_rows = f.T * f.S;
     p.k = f.H;
     p.out_kind = FP4_OUT_SWIGLU;
     p.out = b.h;

@@ -10,9 +10,9 @@
 // spread over many experts): the kernel is then a stream of weights from HBM, and the ring of k-blocks
 // (128 x 128 bytes of codes and their scales) is what keeps it full.  Three tiles, chosen on the host:
 //   at most 32 rows in all      128 weight rows x 32, k split over a cluster where tiles are few
-//   fewer than PAIR_ROWS each   128 weight rows x 128
+//   few each (use_pairs)        128 weight rows x 128
 //   more                        256 weight rows x 256 on a pair of CTAs
-// 64 matrices of 4096 x 6144 (NV) with 4 to 32 rows each stream at 6.4 to 6.6 TB/s, the copy peak; 8192
+// 64 matrices of 4096 x 6144 (NV) with 4 to 32 rows each stream at 6.5 to 6.9 TB/s (copy peak 6.5); 8192
 // rows of one run at 4.3 to 4.9 PFLOP/s, where L2 gives a pair its operands at about 58 bytes per cycle and SM.
 //
 // One persistent CTA per SM, warp-specialised; tiles are taken round-robin:
@@ -1051,15 +1051,23 @@ cudaError_t launch_fmt(const GemmMaps &maps, const GemmArgs &g, int out_kind, bo
 
 }  // namespace
 
-// Tiles of 256 x 256 on CTA pairs, or of 128 x 128 on single CTAs: pairs from PAIR_ROWS rows per matrix
-// on average.  Measured (4096 x 6144 matrices, NV, bf16 out; pairs against single CTAs, us): 64
-// matrices with 32 / 64 / 128 rows each 147 / 152 / 167 against 145 / 152 / 211; one matrix with 16 / 64 /
-// 256 / 2048 / 8192 rows 11.7 / 12.4 / 16.5 / 31.5 / 94 against 11.7 / 14.5 / 19.2 / 49 / 146.
-constexpr int PAIR_ROWS = 48;
+// Tiles of 256 x 256 on CTA pairs, or of 128 x 128 on single CTAs: pairs from PAIR_ROWS rows per matrix on
+// average, and from 33 where tiles of 128 x 128 do not fill the GPU (the pair kernel's epilogue is the
+// faster one).  Measured (4096 x 6144 matrices, NV, bf16 out; pairs against single CTAs, us): 64 matrices
+// with 32 / 64 / 96 rows each 142 / 150 / 158 against 142 / 148 / 156, with 128 rows 167 against 211; one
+// matrix with 64 / 256 / 2048 / 8192 rows 12 / 16 / 31 / 95 against 14 / 19 / 49 / 146.  A shared expert's many
+// rows ask for pairs too: expert half of a layer with 512 / 1024 / 2048 tokens (256 experts, Zipf, 8 and the
+// shared one per token) 639 / 819 / 1141 us against 637 / 831 / 1272.
+constexpr int PAIR_ROWS = 112, PAIR_SHARED = 768;
+
+static bool use_pairs(const Fp4ProductArgs &p) {
+    const int mats = p.w.count + (p.shared ? 1 : 0), avg = p.a.rows / mats;
+    return avg >= PAIR_ROWS || p.shared_rows >= PAIR_SHARED || (avg > 32 && static_cast<long>(mats) * ((avg + 127) / 128) * ((p.w.n + 127) / 128) < device_sm_count());
+}
 
 cudaError_t launch_fp4_product(int fmt, const Fp4ProductArgs &p, cudaStream_t st) {
     GemmMaps maps;
-    const bool pairs = p.a.rows / (p.w.count + (p.shared ? 1 : 0)) >= PAIR_ROWS;
+    const bool pairs = use_pairs(p);
     bool ok = mats_map(&maps.a, p.w, p.k) && (!p.shared || mats_map(&maps.as, *p.shared, p.k));
     ok = ok && rows_maps(maps.b, p.a, p.k);
     if (pairs) ok = ok && tiles_map(&maps.sf, p.w, fmt, p.k) && (!p.shared || tiles_map(&maps.sfs, *p.shared, fmt, p.k));

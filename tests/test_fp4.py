@@ -250,6 +250,7 @@ SHAPES = [  # rows of every group, n, k
     ([300], 384, 320), ([0, 1, 0, 5, 33, 0], 192, 224), ([7, 0, 140, 1], 136, 544), ([1] * 9, 256, 1024), ([0, 0, 2], 16, 2048),
     ([40, 260], 640, 128), ([1], 384, 6144), ([600], 100, 6144), ([32], 2048, 2048), ([2, 0, 9, 20], 4096, 1024),
     ([int(e % 97 == 3) for e in range(1023)] + [2], 48, 64), ([e % 5 for e in range(1000)], 24, 32), ([0] * 31 + [40] + [0] * 32 + [1], 160, 96),
+    ([0] * 9 + [300], 200, 320), ([1] * 20 + [260], 130, 1056),
 ]
 
 
