@@ -10,6 +10,7 @@
 #include "fp4.h"
 #include "internal.h"
 #include "residual.h"
+#include "route_scores.h"
 
 namespace coli {
 
@@ -83,6 +84,33 @@ void record_cuda_error(cudaError_t e) {
     snprintf(g_last_cuda_error, sizeof g_last_cuda_error, "%s: %s", cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
+namespace {
+
+// The part of the workspace that layers over records in 4-bit containers use beside the rest (their h, in
+// bf16, lies where the others' is); behind the last of the other parts.
+struct Fp4Layout {
+    size_t xc, xs, xr, hc, hs, hr, y, inv, end;
+};
+
+Fp4Layout fp4_layout(const coli_moe_config &c, int T, size_t o) {
+    const int f = fp4_of(c.wfmt);
+    const size_t n = static_cast<size_t>(T) * c.top_k, slots = n + static_cast<size_t>(T) * c.n_shared;
+    const size_t H = static_cast<size_t>(c.hidden), I = static_cast<size_t>(c.inter);
+    Fp4Layout L;
+    L.xc = o;  o = align256(o + slots * H / 2);
+    L.xs = o;  o = align256(o + slots * fp4_pitch(f, c.hidden));
+    L.xr = o;  o = align256(o + slots * 4);
+    L.hc = o;  o = align256(o + slots * I / 2);
+    L.hs = o;  o = align256(o + slots * fp4_pitch(f, c.inter));
+    L.hr = o;  o = align256(o + slots * 4);
+    L.y = o;   o = align256(o + slots * H * 2);
+    L.inv = o; o = align256(o + n * 4);
+    L.end = o;
+    return L;
+}
+
+}  // namespace
+
 WsLayout ws_layout(const coli_moe_config &c, int T) {
     WsLayout L;
     const size_t n = static_cast<size_t>(T) * c.top_k;
@@ -110,16 +138,7 @@ WsLayout ws_layout(const coli_moe_config &c, int T) {
     L.w_of = o;     o = align256(o + (tc ? slots * 4 : 0));
     L.chunks = o;   o = align256(o + (tc ? static_cast<size_t>(tc_max_chunks(c, T)) * 16 : 0));
     L.n_chunks = o; o = align256(o + (tc ? 4 : 0));
-    const bool f4 = fp4_wfmt(c.wfmt);
-    const int f = fp4_of(c.wfmt);
-    L.f_xc = o;     o = align256(o + (f4 ? slots * H / 2 : 0));
-    L.f_xs = o;     o = align256(o + (f4 ? slots * fp4_pitch(f, c.hidden) : 0));
-    L.f_xr = o;     o = align256(o + (f4 ? slots * 4 : 0));
-    L.f_hc = o;     o = align256(o + (f4 ? slots * I / 2 : 0));
-    L.f_hs = o;     o = align256(o + (f4 ? slots * fp4_pitch(f, c.inter) : 0));
-    L.f_hr = o;     o = align256(o + (f4 ? slots * 4 : 0));
-    L.f_y = o;      o = align256(o + (f4 ? slots * H * 2 : 0));
-    L.f_inv = o;    o = align256(o + (f4 ? n * 4 : 0));
+    if (fp4_wfmt(c.wfmt)) o = fp4_layout(c, T, o).end;
     L.total = o;
     return L;
 }
@@ -352,17 +371,18 @@ static DecodeParams make_decode(const coli_moe_config *c, const FfnParams &f, ch
 // the general GEMV kernels.
 static coli_status run_ffn(const coli_moe_config *c, const FfnParams &p, char *base, cudaStream_t st) {
     if (fp4_wfmt(c->wfmt)) {
-        const WsLayout L = ws_layout(*c, p.T);
+        const WsLayout W = ws_layout(*c, p.T);
+        const Fp4Layout L = fp4_layout(*c, p.T, W.n_chunks);  // (nothing of the integer GEMM's lies there)
         Fp4Buffers b;
-        b.xc = reinterpret_cast<uint8_t *>(base + L.f_xc);
-        b.xs = reinterpret_cast<uint8_t *>(base + L.f_xs);
-        b.xr = reinterpret_cast<float *>(base + L.f_xr);
-        b.h = base + L.h;
-        b.hc = reinterpret_cast<uint8_t *>(base + L.f_hc);
-        b.hs = reinterpret_cast<uint8_t *>(base + L.f_hs);
-        b.hr = reinterpret_cast<float *>(base + L.f_hr);
-        b.y = base + L.f_y;
-        b.inverse = reinterpret_cast<int32_t *>(base + L.f_inv);
+        b.xc = reinterpret_cast<uint8_t *>(base + L.xc);
+        b.xs = reinterpret_cast<uint8_t *>(base + L.xs);
+        b.xr = reinterpret_cast<float *>(base + L.xr);
+        b.h = base + W.h;
+        b.hc = reinterpret_cast<uint8_t *>(base + L.hc);
+        b.hs = reinterpret_cast<uint8_t *>(base + L.hs);
+        b.hr = reinterpret_cast<float *>(base + L.hr);
+        b.y = base + L.y;
+        b.inverse = reinterpret_cast<int32_t *>(base + L.inv);
         return from_cuda(launch_ffn_fp4(p, c->wfmt, b, st));
     }
     if (use_tc(c, p.T)) {

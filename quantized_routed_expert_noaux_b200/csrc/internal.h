@@ -132,8 +132,6 @@ struct WsLayout {
     size_t h;        // [(T*K+T*S)][I] f32 intermediate
     // tensor-core path only (zero size otherwise)
     size_t xq, hq, sx, sh, tok_of, w_of, chunks, n_chunks;
-    // records in 4-bit containers only (zero size otherwise); h is theirs too, in bf16
-    size_t f_xc, f_xs, f_xr, f_hc, f_hs, f_hr, f_y, f_inv;
     size_t total;
 };
 
@@ -144,8 +142,6 @@ cudaError_t launch_gate(const coli_moe_config &c, const float *Wr, const void *x
                         float *logits, cudaStream_t st);
 cudaError_t launch_route(const coli_moe_config &c, const float *logits, const float *bias,
                          int T, int32_t *ids, float *w, cudaStream_t st);
-cudaError_t launch_route_scores(const coli_moe_router &r, const void *logits, size_t ld, const float *bias, int T,
-                                int32_t *ids, float *w, cudaStream_t st);
 cudaError_t launch_group(const coli_moe_config &c, const int32_t *ids, int T, int32_t *counts,
                          int32_t *offsets, int32_t *perm, int32_t *unique, int32_t *n_unique,
                          int *err, cudaStream_t st);

@@ -16,6 +16,7 @@
 
 #include "internal.h"
 #include "pdl.h"
+#include "route_scores.h"
 
 namespace coli {
 
