@@ -286,7 +286,8 @@ __device__ __forceinline__ void sort_keys(uint32_t (&k)[VPL]) {
 // Errors in units of 2^-24.  With a bias: sigmoid, (4 + 1.5 |l|) of exp(-l), of which s takes s (1 - s), the
 // sum's 1 and the reciprocal's 2 make 5; softmax, expf's 4, its argument's rounding 1, a sum of VPL
 // terms per lane and 5 rounds VPL + 5 of s; the sum with the bias 1 of c.  The place costs 2 VPL units of |c|, or
-// of |l| without a bias; of bf16 logits it takes bits that are zero, and equal logits come in the order of
+// of |l| without a bias, and VPL 2^-149 where float32's last place is no smaller (equal logits of 0 differ by
+// their places alone); of bf16 logits it takes bits that are zero, and equal logits come in the order of
 // their ids.  Groups by two scores without a bias: the scores' errors alone.
 template <int VPL, bool BIAS, typename In>
 __device__ __forceinline__ bool choose_fast(const RouteArgs &a, const float (&l)[VPL], int e0, int lane, int &my_id, float &top, double &sum) {
@@ -331,8 +332,9 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs &a, const float (&l)
         }
     }
     auto value = [&](int v) { return BIAS ? c[v] : l[v]; };
-    // how far a float32 value of magnitude m may be off
-    auto off = [&](float m) { return UNIT * ((BIAS ? (VPL + 16) * (smax + m) : 0.f) + 2 * VPL * m); };
+    // how far a float32 value of magnitude m may be off; the place alone, VPL units of the last place, which are
+    // 2^-149 each for logits below 2^-125 (scores with a bias are off by more than that already)
+    auto off = [&](float m) { return BIAS ? UNIT * ((VPL + 16) * (smax + m) + 2 * VPL * m) : fmaxf(UNIT * (2 * VPL * m), VPL * 1.40129846e-45f); };
     bool mine = true;  // this lane's experts are of a group that is kept
     if (groups) {
         // a group's lanes: 1 << seg_shift of them (the launcher's rule)
