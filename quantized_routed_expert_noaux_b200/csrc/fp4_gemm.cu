@@ -270,6 +270,45 @@ __device__ __forceinline__ int tile_list(const GemmArgs &p, int W, int MB, TileL
     return carry;
 }
 
+// The row scales.  A sum is multiplied with rw * rx, which can leave float32's range before the result does: the
+// quantiser itself hands out scales of 2^-126 to 2^117.  Of scales within [2^-63, 2^64) every product is a
+// normal float32 and nothing more is done.  Otherwise half of each scale's exponent, a power of two, goes out of
+// rw and rx and into the sums: rw rx is then in range for all pairs; it and the power have exponents of the same
+// sign, so neither overflows or underflows a result that does not; and a normal result whose rw rx was in range
+// has the same bits as without.
+__device__ __forceinline__ bool ordinary(float s) { return (__float_as_uint(s) >> 23 & 0xffu) - 64u <= 126u; }
+// s = the returned power of two * s afterwards.
+__device__ __forceinline__ float halve_exponent(float &s) {
+    const int e = static_cast<int>(__float_as_uint(s) >> 23 & 0xffu), k = e ? (e - 126) >> 1 : -74;
+    s *= __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+    return __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+}
+// A sum times the parts of the exponent (2^64 twice would be infinite).
+__device__ __forceinline__ int scaled_sum(int v, float pw, float px) {
+    const float s = __int_as_float(v);
+    return __float_as_int((px < 1.f) == (pw < 1.f) ? s * px * pw : s * (px * pw));
+}
+// A run of 32 rows (rx: row `lane`'s) x a weight row per lane, whose part of the exponent is `pw`.
+__device__ __forceinline__ void split_scales(int (&v)[32], float pw, float &rx) {
+    const float px = halve_exponent(rx);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = scaled_sum(v[j], pw, __shfl_sync(0xffffffffu, px, j));
+}
+// The same in tensor memory, 8 columns at a time.
+__device__ __forceinline__ void split_scales(uint32_t taddr, float pw, float &rx) {
+    const float px = halve_exponent(rx);
+#pragma unroll 1
+    for (int c = 0; c < 32; c += 8) {
+        uint32_t v[8];
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]) : "r"(taddr + c) : "memory");
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = static_cast<uint32_t>(scaled_sum(static_cast<int>(v[j]), pw, __shfl_sync(0xffffffffu, px, c + j)));
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n\ttcgen05.wait::st.sync.aligned;"
+                     ::"r"(taddr + c), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
+    }
+}
+
 // SiLU(gate) * up for rows i (gate lanes, 0-15) and 16 + i (up lanes) of a run of 32 rows: the lane
 // exchanges the sum it does not use with its partner's.  Rounded to bf16: h is quantised to 4 bits next,
 // whose steps are 32 times as wide at least.
@@ -608,8 +647,12 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
                     if (!split_sum(v, x.nr, C, rank, q, lane, tl, t + stride >= ntiles, part, pfull, pfree, abort, p.err)) break;
                     if (rank != 0) break;
                 }
-                const float rx = p.xrow && g + lane < x.nr ? __ldg(p.xrow + x.n0 + g + lane) : 1.f;
-                store_run<OUT>(p, x, v, g, r, rw, rx, lane);
+                float rx = p.xrow && g + lane < x.nr ? __ldg(p.xrow + x.n0 + g + lane) : 1.f, rwg = rw;
+                if (!__all_sync(0xffffffffu, ordinary(rw) && ordinary(rx))) {
+                    const float pw = halve_exponent(rwg);
+                    split_scales(v, pw, rx);
+                }
+                store_run<OUT>(p, x, v, g, r, rwg, rx, lane);
             }
             tc_fence_before();
             mbar_arrive(smem_u32(&dempty[acc]));
@@ -901,16 +944,26 @@ __global__ void __launch_bounds__(P_THREADS, 1) fp4_pair_kernel(const __grid_con
             const Tile x = tile_at<P_NT>(t, list, p, W);
             const int r = x.m * 256 + static_cast<int>(rank) * 128 + 32 * q + lane;
             const float *wrow = x.e >= p.E ? p.wrow_shared : (p.wrow ? p.wrow + static_cast<size_t>(x.e) * p.wrow_stride : nullptr);
-            const float rw = wrow && r < p.n ? __ldg(wrow + r) : 1.f;
+            float rw = wrow && r < p.n ? __ldg(wrow + r) : 1.f;
             float rx[4];
+            bool usual = ordinary(rw);
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const int j = 128 * half + 32 * g + lane;
                 rx[g] = p.xrow && j < x.nr ? __ldg(p.xrow + x.n0 + j) : 1.f;
+                usual = usual && ordinary(rx[g]);
             }
             // (all eight warps meet in the staging barriers: they give up together, or not at all)
             if (epi_or(!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(dfull), tl & 1, abort, p.err)))) break;
             tc_fence_after();
+            if (!__all_sync(0xffffffffu, usual)) {
+                // in tensor memory, before the sums fill the registers (8 at a time: more took registers from the
+                // ordinary tiles, 8192 rows, k 512, 57 us against 49)
+                const float pw = halve_exponent(rw);
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    if (128 * half + 32 * g < x.nr) split_scales(tbase + (static_cast<uint32_t>(32 * q) << 16) + 128 * half + 32 * g, pw, rx[g]);
+            }
             int v[4][32];
 #pragma unroll
             for (int g = 0; g < 4; ++g)
