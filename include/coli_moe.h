@@ -327,8 +327,10 @@ coli_status coli_moe_fp4_quantize(int fmt, int layout, int act, const void *x, i
                                   int k, uint8_t *codes, uint8_t *scales, float *row_scale,
                                   void *ws, void *stream);
 
-/* The values that codes and scales stand for, rounded once to `act`: out row r at out + r * ldo
- * elements (16-byte aligned, ldo a multiple of 16 bytes).  row_scale NULL: 1.  One kernel. */
+/* The values that codes and scales stand for, code * block scale * row scale rounded to float32 and
+ * that to `act` (a row scale that is a power of two takes part in no rounding but that of results
+ * below 2^-126): out row r at out + r * ldo elements (16-byte aligned, ldo a multiple of 16 bytes).
+ * row_scale NULL: 1.  One kernel. */
 coli_status coli_moe_fp4_dequantize(int fmt, int layout, const uint8_t *codes,
                                     const uint8_t *scales, const float *row_scale, int rows,
                                     int k, int act, void *out, size_t ldo, void *stream);

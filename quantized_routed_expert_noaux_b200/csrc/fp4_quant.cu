@@ -432,20 +432,24 @@ __global__ void __launch_bounds__(QT) fp4_dequant_kernel(const uint8_t *__restri
     const size_t pitch = fp4_pitch(FMT, k);
     const bool wide = ((reinterpret_cast<uintptr_t>(out) | ldo * sizeof(Out)) & 31) == 0;
     for (int r = blockIdx.x * (QT / TPR) + threadIdx.x / TPR; r < rows; r += gridDim.x * (QT / TPR)) {
-        const float rs = row_scale ? __ldg(row_scale + r) : 1.f;
+        float rs = row_scale ? __ldg(row_scale + r) : 1.f, unit = 1.f;
+        if (FMT == COLI_FP4_MX && fabsf(rs) < 1.f) {  // code * block scale may overflow (6 * 2^127) where the value does not
+            unit = 0.25f;
+            rs *= 4.f;
+        }
         const uint2 *row = reinterpret_cast<const uint2 *>(codes) + static_cast<size_t>(r) * n;
         Out *o = out + static_cast<size_t>(r) * ldo;
         for (int i = threadIdx.x % TPR; i < n; i += TPR) {
             const uint2 c = __ldg(row + i);
             const uint32_t b = __ldg(scales + scale_at(layout, pitch, r, FMT == COLI_FP4_NV ? i : i >> 1));
             float s;
-            if (FMT == COLI_FP4_MX) s = __uint_as_float(b == 0xffu ? 0x7fc00000u : (b ? b << 23 : 0x00400000u));
+            if (FMT == COLI_FP4_MX) s = __uint_as_float(b == 0xffu ? 0x7fc00000u : (b ? b << 23 : 0x00400000u)) * unit;
             else s = e4m3_value(b & 0x7fu);
             float v[16];
             auto four = [&](uint32_t w, float *d) {
                 const float2 e[4] = {e2m1x2_values<0>(w), e2m1x2_values<1>(w), e2m1x2_values<2>(w), e2m1x2_values<3>(w)};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {  // code * block scale is exact: one rounding, by the row scale
+                for (int j = 0; j < 4; ++j) {  // code * block scale is exact: one rounding to float32, by the row scale
                     d[2 * j] = e[j].x * s * rs;
                     d[2 * j + 1] = e[j].y * s * rs;
                 }
