@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(QT) fp4_quant_kernel(const Fp4QuantArgs a, int
 constexpr int ST = 256, SEG = 4096;
 constexpr int SPREAD_SMEM = 88 * 1024;  // two CTAs per SM at least
 constexpr int SPREAD_MIN = 1024;        // rows
-constexpr int SPREAD_CTAS = 512;        // at most, about: what the passes over the index cost
+constexpr int SPREAD_CTAS = 512;        // about, where shared memory allows it
 
 template <int FMT, int TPR, typename In>
 __global__ void __launch_bounds__(ST, sizeof(In) == 2 ? 4 : 2) fp4_spread_kernel(const Fp4QuantArgs a, int per) {
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(ST, sizeof(In) == 2 ? 4 : 2) fp4_spread_kernel
     wait_for_previous();
     const int tid = threadIdx.x;
     const int pitch = static_cast<int>(fp4_pitch(FMT, a.k)), half = a.k / 2;
-    const int each = half + ((pitch + 15) & ~15);      // bytes of a row in shared memory
+    const int each = half + pitch;                      // bytes of a row in shared memory, a multiple of 16
     float *s_rs = reinterpret_cast<float *>(sm + static_cast<size_t>(per + 1) * each);  // (row `per`: zeros)
     const int t0 = blockIdx.x * per, nt = min(per, a.src_rows - t0);
     const bool wide = ((reinterpret_cast<uintptr_t>(a.x) | a.ldx * sizeof(In)) & 31) == 0;
@@ -364,11 +364,7 @@ __global__ void __launch_bounds__(ST, sizeof(In) == 2 ? 4 : 2) fp4_spread_kernel
         uint8_t *c = a.codes + static_cast<size_t>(r) * half, *d = a.scales + static_cast<size_t>(r) * pitch;
         const uint32_t src = static_cast<uint32_t>(__cvta_generic_to_shared(from));
         asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(c), "r"(src), "r"(half) : "memory");
-        if (pitch % 16 == 0) {
-            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(d), "r"(src + half), "r"(pitch) : "memory");
-        } else {
-            for (int j = 0; j < pitch / 8; ++j) reinterpret_cast<uint2 *>(d)[j] = reinterpret_cast<const uint2 *>(from + half)[j];
-        }
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(d), "r"(src + half), "r"(pitch) : "memory");
         if (a.row_scale) a.row_scale[r] = s_rs[i];
     };
     for (int i = tid; i < nt && a.n_index + t0 + i < a.rows; i += ST) copy(i, a.n_index + t0 + i);
@@ -461,21 +457,31 @@ __global__ void __launch_bounds__(QT) fp4_dequant_kernel(const uint8_t *__restri
     }
 }
 
-// Source rows per CTA of the spreading kernel; 0: every row by itself.  Worth its passes over the index
-// when a source row is taken twice at least and the rows fill the GPU.
-template <int FMT>
+// Source rows per CTA of the spreading kernel; 0: every row by itself.  What each costs, in picoseconds: a row
+// quantised once more, AGAIN per element; a row copied, 440 with every SM at work, 0.3 per element, and 1.17 for
+// each CTA that reads its entry of the index.  The last is what limits the batch: shared memory holds a few rows,
+// so the CTAs grow with the source rows, and their passes over the index with the square (262,144 rows of 6144
+// bf16 elements, 8 times each: 30.4 ms, row by row 6.3; 2048 rows: 21 us against 47).  Both kernels were timed on
+// 1522 sizes (both formats and types, 1024 to 2 million rows of 512 to 16,384 elements, 2 to 32 copies): the rule
+// takes the slower one by more than 10% in 24 of them, by 23% at most; spreading always would in 460, by up to 2.5
+// times.  Scales are copied in pieces of 16 bytes: MX rows with an odd number of k-blocks go row by row (by 8-byte
+// stores the spreading kernel was never the faster one for them).
+template <int FMT, typename In>
 int spread_rows(int layout, const Fp4QuantArgs &a) {
+    constexpr double AGAIN = FMT == COLI_FP4_MX ? (sizeof(In) == 4 ? 1.12 : 0.74) : (sizeof(In) == 4 ? 1.42 : 0.89);
     if (layout != COLI_FP4_ROWS || !a.row_index || a.src_rows == 0 || a.rows < SPREAD_MIN || a.rows / 2 < a.src_rows) return 0;
-    if ((reinterpret_cast<uintptr_t>(a.codes) | reinterpret_cast<uintptr_t>(a.scales)) & 15) return 0;
-    const size_t each = a.k / 2 + fp4_pitch(FMT, a.k) + 16;
+    const size_t pitch = fp4_pitch(FMT, a.k), each = a.k / 2 + pitch;
+    if (pitch % 16 || (reinterpret_cast<uintptr_t>(a.codes) | reinterpret_cast<uintptr_t>(a.scales)) & 15) return 0;
     const int at_once = ST / (a.k <= 2048 ? 32 : QT), turns = (a.src_rows + at_once * SPREAD_CTAS - 1) / (at_once * SPREAD_CTAS);
-    const int fit = static_cast<int>(SPREAD_SMEM / each) - 1, want = at_once * turns;
-    return fit < want ? (fit > 0 ? fit : 0) : want;
+    const int fit = static_cast<int>(SPREAD_SMEM / (each + sizeof(float))) - 1, per = fit < at_once * turns ? fit : at_once * turns;
+    if (per < 1) return 0;
+    const double rows = a.rows, k = a.k, ctas = (a.src_rows + per - 1) / per, sms = device_sm_count();
+    return (rows - a.src_rows) * k * AGAIN > rows * (440.0 * (ctas < sms ? sms / ctas : 1.0) + 0.3 * k + 1.17 * ctas) ? per : 0;
 }
 
 template <int FMT, int TPR, typename In>
 cudaError_t launch_spread(const Fp4QuantArgs &a, int per, cudaStream_t st) {
-    const size_t smem = (per + 1) * (a.k / 2 + ((fp4_pitch(FMT, a.k) + 15) & ~static_cast<size_t>(15)) + sizeof(float));
+    const size_t smem = (per + 1) * (a.k / 2 + fp4_pitch(FMT, a.k) + sizeof(float));
     const cudaError_t e = cudaFuncSetAttribute(fp4_spread_kernel<FMT, TPR, In>, cudaFuncAttributeMaxDynamicSharedMemorySize, SPREAD_SMEM);
     if (e != cudaSuccess) return e;
     return launch_early(fp4_spread_kernel<FMT, TPR, In>, dim3((a.src_rows + per - 1) / per), ST, smem, st, 1, a, per);
@@ -483,7 +489,7 @@ cudaError_t launch_spread(const Fp4QuantArgs &a, int per, cudaStream_t st) {
 
 template <int FMT, typename In>
 cudaError_t launch_quant(int layout, const Fp4QuantArgs &a, cudaStream_t st) {
-    if (const int per = spread_rows<FMT>(layout, a)) return a.k <= 2048 ? launch_spread<FMT, 32, In>(a, per, st) : launch_spread<FMT, QT, In>(a, per, st);
+    if (const int per = spread_rows<FMT, In>(layout, a)) return a.k <= 2048 ? launch_spread<FMT, 32, In>(a, per, st) : launch_spread<FMT, QT, In>(a, per, st);
     const int out_rows = layout == COLI_FP4_TILES ? (a.rows + 127) / 128 * 128 : a.rows;
     if (a.k <= 2048) return launch_early(fp4_quant_kernel<FMT, 32, In>, dim3((out_rows + QT / 32 - 1) / (QT / 32)), QT, 0, st, 1, a, layout, out_rows);
     return launch_early(fp4_quant_kernel<FMT, QT, In>, dim3(out_rows), QT, 0, st, 1, a, layout, out_rows);
