@@ -138,7 +138,8 @@ coli_status coli_moe_error_word(void *ws, void *stream, int *code);
 
 /* a1, router gate projection (colibri-strix README, "What's implemented": sigmoid router).
  * logits[t][e] = float32( sum_h x[t][h] * router_w[e][h] ), the products and the sum taken in
- * double precision, rounded once to float32.  T = 0 is a no-op. */
+ * double precision, rounded once to float32.  T = 0 is a no-op; more than 65535 * 64 tokens are
+ * COLI_ERR_UNSUPPORTED, here and in the layer. */
 coli_status coli_moe_gate(const coli_moe_config *cfg, const float *router_w, const void *x,
                           int T, float *logits, void *stream);
 

@@ -8,6 +8,7 @@
 
 #include "coli_moe.h"
 #include "fp4.h"
+#include "gate.h"
 #include "internal.h"
 #include "residual.h"
 #include "route_scores.h"
@@ -269,6 +270,7 @@ coli_status coli_moe_gate(const coli_moe_config *c, const float *router_w, const
     coli_status s = coli_moe_check_config(c);
     if (s != COLI_OK) return s;
     if (T < 0) return COLI_ERR_SHAPE;
+    if (T > GATE_MAX_TOKENS) return COLI_ERR_UNSUPPORTED;
     if (T == 0) return COLI_OK;
     if (!router_w || !x || !logits) return COLI_ERR_INVALID_ARG;
     if (!aligned(router_w, 16) || !aligned(x, 16) || !aligned(logits, 4)) return COLI_ERR_ALIGN;
@@ -443,7 +445,7 @@ coli_status coli::layer_args_status(const coli_moe_config *c, const coli_moe_wei
     if (!aligned(x, 16) || !aligned(out, 16)) return COLI_ERR_ALIGN;
     if ((topk_ids_out && !aligned(topk_ids_out, 4)) || (topk_w_out && !aligned(topk_w_out, 4)))
         return COLI_ERR_ALIGN;
-    if (T > max_tokens(c) && !use_tc(c, T)) return COLI_ERR_UNSUPPORTED;
+    if (T > GATE_MAX_TOKENS || (T > max_tokens(c) && !use_tc(c, T))) return COLI_ERR_UNSUPPORTED;
     return COLI_OK;
 }
 

@@ -11,6 +11,7 @@
 #include <stdint.h>
 
 #include "fp4.h"
+#include "gate.h"
 #include "internal.h"
 #include "pdl.h"
 
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(128) gate_few_kernel(const float *__restrict__
 // distributed shared memory and are added pairwise in a fixed order: p0 + p1 (and p2 + p3,
 // then (p0 + p1) + (p2 + p3)).  Measured on B200 (2048 tokens, 256 experts, H 6144): 32 x 32
 // warp tiles 260 us against 271 us for 32 x 16; the m16n8k8 double shape, 303 us.
-constexpr int GM = 64, GN = 64, GK = 32;
+constexpr int GM = GATE_TILE, GN = 64, GK = 32;
 constexpr int GKP = GK + 4;  // row pitch (doubles): the 8 x 4 fragment reads hit each bank twice
 
 __device__ __forceinline__ void dmma(double &d0, double &d1, double a, double b) {
