@@ -356,11 +356,15 @@ typedef struct {
 /* out[i][j] = sum_k a[i][k] * w[j][k] for every row i of `a`, w the matrix of the row's group:
  * rows offsets[e] .. offsets[e+1] - 1 belong to matrix e (device int32 [count + 1], ascending, as
  * coli_moe_group writes them); offsets NULL: one matrix (count == 1) for all rows.  Rows outside
- * every group keep what `out` held.  Groups that are not ascending within [0, rows] are left out
- * and set COLI_DEVERR_GROUPING in the error word of `ws`.
- * Products on the tensor cores, block scales applied there, float32 sums; the row scales are
- * applied to the sum, which is rounded once to out_type (coli_act).  No atomics: the same call
- * gives the same bits.
+ * every group keep what `out` held.  A group whose own two offsets are not ascending within
+ * [0, rows] is left out and sets COLI_DEVERR_GROUPING in the error word of `ws`; where such offsets
+ * make two groups overlap, the rows they share hold one's results or the other's.
+ * Products on the tensor cores, block scales applied there, float32 sums.  A sum is multiplied with
+ * the product of its two row scales, both rounded to float32 (exact for powers of two), and the
+ * result rounded to out_type (coli_act); any finite scales will do, their product may leave
+ * float32's range where the result does not.  No atomics: the same call gives the same bits.
+ * Tiles are counted in 32 bits: COLI_ERR_UNSUPPORTED where (rows / 16 + 1) * ceil(n / 128) *
+ * (count + 1) does not fit.
  * out: row i at out + i * ldo elements, ldo >= n, aligned to its elements.  rows = 0 is a no-op.
  * One kernel; allocates nothing; may be captured. */
 coli_status coli_moe_fp4_product(int fmt, const coli_fp4_rows *a, const coli_fp4_mats *w, int k,
