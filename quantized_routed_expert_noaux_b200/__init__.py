@@ -171,18 +171,24 @@ def _current_stream() -> int:
     return _torch_stream(_torch_device())
 
 
-def _device_stream(fn: str, stream, t) -> Optional[int]:
-    """_stream for a call whose tensors must live on the current device: t is one of them."""
+def _stream_at(fn: str, stream, at: int, together: bool) -> Optional[int]:
+    """_stream for a call whose tensors lie on CUDA device `at`, all of them if `together`: the current one it must be."""
+    if not together or at < 0:  # (-1: not a CUDA tensor)
+        raise ColiError(fn, 1)
+    if _torch_device is None:
+        _current_stream()
+    if _torch_device is not None and at != _torch_device():
+        raise ColiError(fn, 1)
     if stream is not None:
         return stream if stream.__class__ is int else stream.cuda_stream
-    if t is None or t.__class__ is int:
-        return _current_stream()
-    at = t.get_device()
-    if _torch_device is None and at >= 0:
-        _current_stream()
-    if at < 0 or (_torch_device is not None and at != _torch_device()):  # (-1: not a CUDA tensor)
-        raise ColiError(fn, 1)
     return _torch_stream(at) if _torch_device is not None else _current_stream()
+
+
+def _pointers(fn: str, stream, *tensors):
+    """The same for tensors, device pointers and None in any mixture: their pointers and the stream."""
+    devices = [t.get_device() for t in tensors if t is not None and t.__class__ is not int]
+    st = _stream_at(fn, stream, devices[0], devices.count(devices[0]) == len(devices)) if devices else _stream(stream)
+    return *map(_p, tensors), st
 
 
 def _check(fn: str, status: int) -> None:
@@ -328,13 +334,21 @@ def coli_moe_check_router(router: MoERouter) -> None:
 
 
 # The calls below may run every few microseconds (one decoded token through a router or a linear layer), so
-# they pass structures and pointers to ctypes without helpers in between.
+# they pass structures and pointers to ctypes without helpers in between.  All tensors of a call must live on the
+# current device: one that does not would be a bad address to the kernel.
 
 def coli_moe_route_scores(router: MoERouter, logits, ld, bias, T, topk_ids, topk_w, stream=None) -> None:
     """Softmax or sigmoid routing of T tokens: row t of the logits at element t * ld (0: n_experts),
     bias [E] float32 or None."""
-    st = _device_stream("coli_moe_route_scores", stream, logits)
-    status = lib.coli_moe_route_scores(router, _p(logits), ld, _p(bias), T, _p(topk_ids), _p(topk_w), st)
+    try:
+        at = logits.get_device()
+        st = _stream_at("coli_moe_route_scores", stream, at,
+                        at == topk_ids.get_device() == topk_w.get_device() and (bias is None or at == bias.get_device()))
+        status = lib.coli_moe_route_scores(router, logits.data_ptr(), ld, None if bias is None else bias.data_ptr(), T, topk_ids.data_ptr(),
+                                           topk_w.data_ptr(), st)
+    except AttributeError:  # device pointers among them
+        logits, bias, topk_ids, topk_w, st = _pointers("coli_moe_route_scores", stream, logits, bias, topk_ids, topk_w)
+        status = lib.coli_moe_route_scores(router, logits, ld, bias, T, topk_ids, topk_w, st)
     if status:
         raise ColiError("coli_moe_route_scores", status)
 
@@ -355,33 +369,52 @@ def coli_moe_fp4_quantize(fmt, layout, act, x, src_rows, ldx, row_index, row_div
                           stream=None) -> None:
     """Rows of x (row i at element i * ldx) to 4-bit codes, block scales and row scales; row r of the
     result is source row r, or row_index[r] // row_div."""
-    st = _device_stream("coli_moe_fp4_quantize", stream, x)
-    status = lib.coli_moe_fp4_quantize(fmt, layout, act, _p(x), src_rows, ldx, _p(row_index), row_div, rows, k, _p(codes),
-                                       _p(scales), _p(row_scale), _p(ws), st)
+    try:
+        at = x.get_device()
+        st = _stream_at("coli_moe_fp4_quantize", stream, at,
+                        at == codes.get_device() == scales.get_device() == row_scale.get_device() == ws.get_device() and
+                        (row_index is None or at == row_index.get_device()))
+        status = lib.coli_moe_fp4_quantize(fmt, layout, act, x.data_ptr(), src_rows, ldx, None if row_index is None else row_index.data_ptr(), row_div,
+                                           rows, k, codes.data_ptr(), scales.data_ptr(), row_scale.data_ptr(), ws.data_ptr(), st)
+    except AttributeError:
+        x, row_index, codes, scales, row_scale, ws, st = _pointers("coli_moe_fp4_quantize", stream, x, row_index, codes, scales, row_scale, ws)
+        status = lib.coli_moe_fp4_quantize(fmt, layout, act, x, src_rows, ldx, row_index, row_div, rows, k, codes, scales, row_scale, ws, st)
     if status:
         raise ColiError("coli_moe_fp4_quantize", status)
 
 
 def coli_moe_fp4_dequantize(fmt, layout, codes, scales, row_scale, rows, k, act, out, ldo, stream=None) -> None:
     """The values that codes, block scales and row scales stand for, rounded to act; row r at out + r * ldo."""
-    st = _device_stream("coli_moe_fp4_dequantize", stream, out)
-    status = lib.coli_moe_fp4_dequantize(fmt, layout, _p(codes), _p(scales), _p(row_scale), rows, k, act, _p(out), ldo, st)
+    try:
+        at = out.get_device()
+        st = _stream_at("coli_moe_fp4_dequantize", stream, at,
+                        at == codes.get_device() == scales.get_device() and (row_scale is None or at == row_scale.get_device()))
+        status = lib.coli_moe_fp4_dequantize(fmt, layout, codes.data_ptr(), scales.data_ptr(), None if row_scale is None else row_scale.data_ptr(), rows, k,
+                                             act, out.data_ptr(), ldo, st)
+    except AttributeError:
+        codes, scales, row_scale, out, st = _pointers("coli_moe_fp4_dequantize", stream, codes, scales, row_scale, out)
+        status = lib.coli_moe_fp4_dequantize(fmt, layout, codes, scales, row_scale, rows, k, act, out, ldo, st)
     if status:
         raise ColiError("coli_moe_fp4_dequantize", status)
 
 
 def coli_moe_fp4_product(fmt, a: FP4Rows, w: FP4Mats, k, offsets, out_type, out, ldo, ws, stream=None) -> None:
     """out row i = a's row i times the matrix of its group (offsets [count + 1] int32; None: one matrix)."""
-    st = _device_stream("coli_moe_fp4_product", stream, out)
-    status = lib.coli_moe_fp4_product(fmt, a, w, k, _p(offsets), out_type, _p(out), ldo, _p(ws), st)
+    try:
+        at = out.get_device()
+        st = _stream_at("coli_moe_fp4_product", stream, at, at == ws.get_device() and (offsets is None or at == offsets.get_device()))
+        status = lib.coli_moe_fp4_product(fmt, a, w, k, None if offsets is None else offsets.data_ptr(), out_type, out.data_ptr(), ldo, ws.data_ptr(), st)
+    except AttributeError:
+        offsets, out, ws, st = _pointers("coli_moe_fp4_product", stream, offsets, out, ws)
+        status = lib.coli_moe_fp4_product(fmt, a, w, k, offsets, out_type, out, ldo, ws, st)
     if status:
         raise ColiError("coli_moe_fp4_product", status)
 
 
 def coli_moe_fp4_pack_record(cfg: MoEConfig, act, wg, wu, wd, record, ws, stream=None) -> None:
     """One expert's gate, up [I, H] and down [H, I] matrices into a record of cfg's 4-bit container."""
-    _check("coli_moe_fp4_pack_record", lib.coli_moe_fp4_pack_record(
-        C.byref(cfg), act, _p(wg), _p(wu), _p(wd), _p(record), _p(ws), _device_stream("coli_moe_fp4_pack_record", stream, wg)))
+    wg, wu, wd, record, ws, st = _pointers("coli_moe_fp4_pack_record", stream, wg, wu, wd, record, ws)
+    _check("coli_moe_fp4_pack_record", lib.coli_moe_fp4_pack_record(C.byref(cfg), act, wg, wu, wd, record, ws, st))
 
 
 def fp4_rows_for(codes, scales, row_scale=None) -> FP4Rows:
