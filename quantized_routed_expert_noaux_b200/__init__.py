@@ -73,10 +73,12 @@ class MoERouter(C.Structure):
 
 
 class FP4Rows(C.Structure):
+    device = None  # of the tensors that fp4_rows_for took
     _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("row_scale", C.c_void_p), ("rows", C.c_int)]
 
 
 class FP4Mats(C.Structure):
+    device = None
     _fields_ = [
         ("codes", C.c_void_p), ("scales", C.c_void_p), ("row_scale", C.c_void_p), ("count", C.c_int), ("n", C.c_int),
         ("codes_stride", C.c_size_t), ("scales_stride", C.c_size_t), ("row_scale_stride", C.c_size_t),
@@ -333,6 +335,9 @@ def coli_moe_check_router(router: MoERouter) -> None:
     _check("coli_moe_check_router", lib.coli_moe_check_router(C.byref(router)))
 
 
+_c_route_scores, _c_fp4_quantize = lib.coli_moe_route_scores, lib.coli_moe_fp4_quantize
+_c_fp4_dequantize, _c_fp4_product = lib.coli_moe_fp4_dequantize, lib.coli_moe_fp4_product
+
 # The calls below may run every few microseconds (one decoded token through a router or a linear layer), so
 # they pass structures and pointers to ctypes without helpers in between.  All tensors of a call must live on the
 # current device: one that does not would be a bad address to the kernel.
@@ -342,13 +347,14 @@ def coli_moe_route_scores(router: MoERouter, logits, ld, bias, T, topk_ids, topk
     bias [E] float32 or None."""
     try:
         at = logits.get_device()
-        st = _stream_at("coli_moe_route_scores", stream, at,
-                        at == topk_ids.get_device() == topk_w.get_device() and (bias is None or at == bias.get_device()))
-        status = lib.coli_moe_route_scores(router, logits.data_ptr(), ld, None if bias is None else bias.data_ptr(), T, topk_ids.data_ptr(),
+        together = at == topk_ids.get_device() == topk_w.get_device() and (bias is None or at == bias.get_device())
+        st = (_torch_stream(at) if together and stream is None and _torch_device is not None and at == _torch_device()
+              else _stream_at("coli_moe_route_scores", stream, at, together))
+        status = _c_route_scores(router, logits.data_ptr(), ld, None if bias is None else bias.data_ptr(), T, topk_ids.data_ptr(),
                                            topk_w.data_ptr(), st)
     except AttributeError:  # device pointers among them
         logits, bias, topk_ids, topk_w, st = _pointers("coli_moe_route_scores", stream, logits, bias, topk_ids, topk_w)
-        status = lib.coli_moe_route_scores(router, logits, ld, bias, T, topk_ids, topk_w, st)
+        status = _c_route_scores(router, logits, ld, bias, T, topk_ids, topk_w, st)
     if status:
         raise ColiError("coli_moe_route_scores", status)
 
@@ -371,14 +377,15 @@ def coli_moe_fp4_quantize(fmt, layout, act, x, src_rows, ldx, row_index, row_div
     result is source row r, or row_index[r] // row_div."""
     try:
         at = x.get_device()
-        st = _stream_at("coli_moe_fp4_quantize", stream, at,
-                        at == codes.get_device() == scales.get_device() == row_scale.get_device() == ws.get_device() and
-                        (row_index is None or at == row_index.get_device()))
-        status = lib.coli_moe_fp4_quantize(fmt, layout, act, x.data_ptr(), src_rows, ldx, None if row_index is None else row_index.data_ptr(), row_div,
+        together = (at == codes.get_device() == scales.get_device() == row_scale.get_device() == ws.get_device() and
+                    (row_index is None or at == row_index.get_device()))
+        st = (_torch_stream(at) if together and stream is None and _torch_device is not None and at == _torch_device()
+              else _stream_at("coli_moe_fp4_quantize", stream, at, together))
+        status = _c_fp4_quantize(fmt, layout, act, x.data_ptr(), src_rows, ldx, None if row_index is None else row_index.data_ptr(), row_div,
                                            rows, k, codes.data_ptr(), scales.data_ptr(), row_scale.data_ptr(), ws.data_ptr(), st)
     except AttributeError:
         x, row_index, codes, scales, row_scale, ws, st = _pointers("coli_moe_fp4_quantize", stream, x, row_index, codes, scales, row_scale, ws)
-        status = lib.coli_moe_fp4_quantize(fmt, layout, act, x, src_rows, ldx, row_index, row_div, rows, k, codes, scales, row_scale, ws, st)
+        status = _c_fp4_quantize(fmt, layout, act, x, src_rows, ldx, row_index, row_div, rows, k, codes, scales, row_scale, ws, st)
     if status:
         raise ColiError("coli_moe_fp4_quantize", status)
 
@@ -387,13 +394,14 @@ def coli_moe_fp4_dequantize(fmt, layout, codes, scales, row_scale, rows, k, act,
     """The values that codes, block scales and row scales stand for, rounded to act; row r at out + r * ldo."""
     try:
         at = out.get_device()
-        st = _stream_at("coli_moe_fp4_dequantize", stream, at,
-                        at == codes.get_device() == scales.get_device() and (row_scale is None or at == row_scale.get_device()))
-        status = lib.coli_moe_fp4_dequantize(fmt, layout, codes.data_ptr(), scales.data_ptr(), None if row_scale is None else row_scale.data_ptr(), rows, k,
+        together = at == codes.get_device() == scales.get_device() and (row_scale is None or at == row_scale.get_device())
+        st = (_torch_stream(at) if together and stream is None and _torch_device is not None and at == _torch_device()
+              else _stream_at("coli_moe_fp4_dequantize", stream, at, together))
+        status = _c_fp4_dequantize(fmt, layout, codes.data_ptr(), scales.data_ptr(), None if row_scale is None else row_scale.data_ptr(), rows, k,
                                              act, out.data_ptr(), ldo, st)
     except AttributeError:
         codes, scales, row_scale, out, st = _pointers("coli_moe_fp4_dequantize", stream, codes, scales, row_scale, out)
-        status = lib.coli_moe_fp4_dequantize(fmt, layout, codes, scales, row_scale, rows, k, act, out, ldo, st)
+        status = _c_fp4_dequantize(fmt, layout, codes, scales, row_scale, rows, k, act, out, ldo, st)
     if status:
         raise ColiError("coli_moe_fp4_dequantize", status)
 
@@ -402,11 +410,17 @@ def coli_moe_fp4_product(fmt, a: FP4Rows, w: FP4Mats, k, offsets, out_type, out,
     """out row i = a's row i times the matrix of its group (offsets [count + 1] int32; None: one matrix)."""
     try:
         at = out.get_device()
-        st = _stream_at("coli_moe_fp4_product", stream, at, at == ws.get_device() and (offsets is None or at == offsets.get_device()))
-        status = lib.coli_moe_fp4_product(fmt, a, w, k, None if offsets is None else offsets.data_ptr(), out_type, out.data_ptr(), ldo, ws.data_ptr(), st)
+        together = (at == ws.get_device() and (offsets is None or at == offsets.get_device()) and
+                    (a.device is None or at == a.device) and (w.device is None or at == w.device))
+        st = (_torch_stream(at) if together and stream is None and _torch_device is not None and at == _torch_device()
+              else _stream_at("coli_moe_fp4_product", stream, at, together))
+        status = _c_fp4_product(fmt, a, w, k, None if offsets is None else offsets.data_ptr(), out_type, out.data_ptr(), ldo, ws.data_ptr(), st)
     except AttributeError:
+        operands = {getattr(m, "device", None) for m in (a, w)} - {None}
+        if len(operands) > 1:
+            raise ColiError("coli_moe_fp4_product", 1) from None
         offsets, out, ws, st = _pointers("coli_moe_fp4_product", stream, offsets, out, ws)
-        status = lib.coli_moe_fp4_product(fmt, a, w, k, offsets, out_type, out, ldo, ws, st)
+        status = _c_fp4_product(fmt, a, w, k, offsets, out_type, out, ldo, ws, st)
     if status:
         raise ColiError("coli_moe_fp4_product", status)
 
@@ -418,13 +432,36 @@ def coli_moe_fp4_pack_record(cfg: MoEConfig, act, wg, wu, wd, record, ws, stream
 
 
 def fp4_rows_for(codes, scales, row_scale=None) -> FP4Rows:
-    """FP4Rows over device tensors: codes [rows, k/2] uint8, scales [rows, pitch] uint8, row_scale [rows]."""
-    return FP4Rows(codes.data_ptr(), scales.data_ptr(), _p(row_scale), codes.shape[0])
+    """FP4Rows over device tensors: codes [rows, k/2] uint8, scales [rows, pitch] uint8, row_scale [rows],
+    all of them contiguous (the kernels take no strides for them)."""
+    at = codes.get_device()
+    if row_scale is None:
+        row, dense, together = None, codes.is_contiguous() and scales.is_contiguous(), at == scales.get_device()
+    else:
+        row, dense = row_scale.data_ptr(), codes.is_contiguous() and scales.is_contiguous() and row_scale.is_contiguous()
+        together = at == scales.get_device() == row_scale.get_device()
+    if not dense or not together or at < 0:
+        raise ColiError("fp4_rows_for", 1 if dense else 2)
+    a = FP4Rows(codes.data_ptr(), scales.data_ptr(), row, codes.shape[0])
+    a.device = at
+    return a
 
 
 def fp4_mats_for(codes, scales, row_scale=None) -> FP4Mats:
     """FP4Mats over device tensors: codes [count, n, k/2] uint8, scales [count, bytes] uint8 in tiles,
-    row_scale [count, n]."""
-    count, n, _ = codes.shape
-    return FP4Mats(codes.data_ptr(), scales.data_ptr(), _p(row_scale), count, n, codes.stride()[0], scales.stride()[0],
-                   0 if row_scale is None else row_scale.stride()[0])
+    row_scale [count, n].  Each matrix of a tensor is contiguous; the matrices may lie further apart."""
+    at = codes.get_device()
+    count, n, half = codes.shape
+    c, s = codes.stride(), scales.stride()
+    if row_scale is None:
+        row, r, together = None, (0, 1), at == scales.get_device()
+    else:
+        row, r, together = row_scale.data_ptr(), row_scale.stride(), at == scales.get_device() == row_scale.get_device()
+    if not (c[2] == 1 and c[1] == half and len(s) == 2 and s[1] == 1 and r[1] == 1):  # (dimensions of one element may have any stride)
+        if not all(t is None or t.is_contiguous() or t[0].is_contiguous() for t in (codes, scales, row_scale)):
+            raise ColiError("fp4_mats_for", 2)
+    if not together or at < 0:
+        raise ColiError("fp4_mats_for", 1)
+    w = FP4Mats(codes.data_ptr(), scales.data_ptr(), row, count, n, c[0], s[0], r[0])
+    w.device = at
+    return w
