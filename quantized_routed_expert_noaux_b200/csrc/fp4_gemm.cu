@@ -44,7 +44,7 @@ constexpr int A_BYTES = 128 * 128;       // weight codes of a k-block
 constexpr int P_NT = 256;                // rows of a CTA pair's tile
 constexpr int BAND = 8;                  // weight blocks side by side in the order of the tiles
 constexpr int MAX_MATS = 1025;           // 1024 and a shared one
-constexpr int NBOX = 5;                  // box heights 16 << i rows
+constexpr int NBOX = 4;                  // box heights 16 << i rows
 constexpr int W_PROD = 0, W_MMA = 1, W_SF = 2, N_SF = 2, W_EPI0 = 4, N_EPI = 4;
 constexpr int THREADS = 8 * 32;
 constexpr int MAX_SPLIT = 4;             // CTAs that share a tile's k-blocks at most
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
                     tma_load_3d(smem_u32(sa + s * A_BYTES), ta, (kb0 + kb) * 128, x.m * 128, ez, fb);
                     bulk_load(smem_u32(ssa + s * P::SFA_BYTES), wsf + static_cast<size_t>(kb0 + kb) * P::SFA_BYTES, P::SFA_BYTES, fb);
 #pragma unroll
-                    for (int bit = NT <= 32 ? 1 : NBOX - 2; bit >= 0; --bit) {
+                    for (int bit = NT <= 32 ? 1 : NBOX - 1; bit >= 0; --bit) {
                         const int row0 = 16 * ((n16 >> (bit + 1)) << (bit + 1));  // rows of the larger boxes
                         if ((n16 >> bit) & 1) tma_load_2d(smem_u32(sb + s * P::B_BYTES + row0 * 128), &maps.b[bit], (kb0 + kb) * 128, x.n0 + row0, fb);
                     }
@@ -855,7 +855,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) fp4_pair_kernel(const __grid_con
                     pair_load_3d(smem_u32(sa + s * A_BYTES), ta, kb * 128, x.m * 256 + static_cast<int>(rank) * 128, ez, fb);
                     pair_load_3d(smem_u32(ssa + s * P::SFA_BYTES), tsf, 0, (x.m * 2 + static_cast<int>(rank)) * atoms + kb * P::ATOMS, ez, fb);
 #pragma unroll
-                    for (int bit = NBOX - 2; bit >= 0; --bit) {
+                    for (int bit = NBOX - 1; bit >= 0; --bit) {
                         const int row0 = 16 * ((n32 >> (bit + 1)) << (bit + 1));
                         if ((n32 >> bit) & 1) pair_load_2d(smem_u32(sb + s * P::B_BYTES + row0 * 128), &maps.b[bit], kb * 128, row_lo + row0, fb);
                     }
