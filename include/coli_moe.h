@@ -313,8 +313,9 @@ coli_status coli_moe_fp4_scale_bytes(int fmt, int layout, int rows, int k, size_
 /* Quantises `rows` rows of k values.  Row r is read from source row r (row_index NULL; rows ==
  * src_rows) or row_index[r] / row_div (device int32; a slot's token with row_div = top_k), source
  * row i at x + i * ldx elements (act: coli_act).
- *   NV: row scale 2^(floor(log2(largest |x| of the row)) - 10) (1 for a row of zeros), block scale
- *       the e4m3 nearest to (largest |x| of the block) / (6 * row scale);
+ *   NV: row scale 2^(floor(log2(largest |x| of the row)) - 10), at least 2^-126 (1 for a row of
+ *       zeros), block scale the e4m3 nearest to (largest |x| of the block) / (6 * row scale); where
+ *       that is 0 the codes are 0;
  *   MX: block scale 2^(floor(log2(largest |x| of the block)) - 2), at least 2^-127; row scale 1;
  *   code: the e2m1 nearest to x / (block scale * row scale), ties to the even code, at most 6.
  * Both are exact: the quotients are those of the real numbers.  A block that holds a NaN or an

@@ -12,8 +12,10 @@
 //   at most 32 rows in all      128 weight rows x 32, k split over a cluster where tiles are few
 //   few each (use_pairs)        128 weight rows x 128
 //   more                        256 weight rows x 256 on a pair of CTAs
-// 64 matrices of 4096 x 6144 (NV) with 4 to 32 rows each stream at 6.5 to 6.9 TB/s (copy peak 6.5); 8192
-// rows of one run at 4.3 to 4.9 PFLOP/s, where L2 gives a pair its operands at about 58 bytes per cycle and SM.
+// 64 matrices of 4096 x 6144 (NV) with 1 to 32 rows each stream at 6.4 to 6.9 TB/s (copy peak 6.5); 8192
+// rows of one run at 4.4 PFLOP/s (94 us at 1965 MHz; 109 us at 1580 MHz, under the power cap, in long runs).  That is
+// 1030 to 1100 cycles per k-block, of which the products need 512; a CTA takes 41 KB from L2 in that time, 37 to
+// 40 bytes per cycle.  Which of the operands, the row scales and the single accumulator it waits for is not measured.
 //
 // One persistent CTA per SM, warp-specialised; tiles are taken round-robin:
 //   warp 0      TMA producer: weight codes (128-byte swizzle), their scale tiles (one bulk copy: the
@@ -350,8 +352,8 @@ __device__ __forceinline__ void store_run(const GemmArgs &p, const Tile &x, cons
 // Row-scale warp `w` of N_SF: its k-blocks' scales of up to NT rows, from their rows (4 * ATOMS bytes
 // each) to the tile order of tcgen05.cp.  A lane takes rows lane + 32 c of each 128: word j of its four rows is
 // one 16-byte piece of tile j, so a k-block of 128 rows is ATOMS stores of 16 bytes per lane (shared memory is
-// nearly used up by the products' operands: 4-byte stores, four times as many, took 780 of the 730 cycles that
-// a k-block of 256 rows then needed per warp and other k-block).  Rows behind the tile's last repeat a row
+// nearly used up by the products' operands: 4-byte stores, four times as many, kept a warp busy for 780 cycles per
+// k-block of 256 rows, longer than the products then took).  Rows behind the tile's last repeat a row
 // that exists: what they give is not stored by the epilogue.  publish(stage) tells the MMA warp.
 template <int FMT, int NT, typename Publish>
 __device__ __forceinline__ void row_scales(const GemmArgs &p, int w, int first, int stride, int ntiles, int KT, const TileList &list, int W,

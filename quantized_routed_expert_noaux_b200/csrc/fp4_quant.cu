@@ -323,8 +323,9 @@ __global__ void __launch_bounds__(QT) fp4_quant_kernel(const Fp4QuantArgs a, int
 // Rows of an index that takes every source row several times (the slots of a token's experts): a CTA
 // quantises `per` source rows once, ST / TPR at a time, into shared memory, then goes through the whole index;
 // a thread that meets one of them starts its bulk copies to the row that asks for it.  The index is read
-// gridDim.x times, from L2.  Rows whose index is bad are the first CTA's, copies of a row of zeros.  16,384 rows of 6144 bf16 elements from 2048 (NV): 22 us against
-// 49 with every row quantised by itself; 4096 rows from 512, 7 against 14.
+// gridDim.x times, from L2.  Rows whose index is bad are the first CTA's, copies of a row of zeros.  16,384 rows of
+// 6144 bf16 elements from 2048 (NV): 21 us against 47 with every row quantised by itself; 4096 rows from 512, 7
+// against 13.
 constexpr int ST = 256, SEG = 4096;
 constexpr int SPREAD_SMEM = 88 * 1024;  // two CTAs per SM at least
 constexpr int SPREAD_MIN = 1024;        // rows

@@ -1,8 +1,10 @@
 // pdl.h -- programmatic dependent launch: a kernel may be set up while the one before it on its stream
-// still runs.  Every kernel that is launched so calls dependents_may_launch() and then wait_for_previous()
-// before its first access to memory that an earlier kernel may touch, in every thread of every CTA; the wait
-// ends when the kernels before have completed and their writes are visible.  (A kernel that returned without
-// waiting could complete before its predecessor, and let its successor run too early.)
+// ends.  Every thread of every CTA of a kernel that is launched so calls wait_for_previous() before its first access
+// to memory that an earlier kernel may touch; the wait ends when the kernels before have completed and their
+// writes are visible.  (A kernel that returned without waiting could complete before its predecessor, and let
+// its successor run too early.)  Only the products call dependents_may_launch(), at their end; elsewhere the end
+// of the kernel is the trigger.  Earlier triggers gave the next kernel's CTAs room beside the running ones and
+// were slower (2048 tokens routed 6.5 us against 5.0, the expert half for one token 70 against 59).
 #pragma once
 
 #include <cuda_runtime.h>

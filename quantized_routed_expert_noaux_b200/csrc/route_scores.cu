@@ -6,9 +6,12 @@
 // an unsigned integer key that orders as the value does, 0 for an expert that cannot be chosen:
 // 32 bits of the logit itself without a bias (the score grows with it, no rounding takes part in
 // the choice), 64 bits of the double c = s + bias with one.  A warp's largest key is then one
-// redux.sync (three with 64 bits: high word, low word, lowest id) instead of five rounds of
-// shuffles and comparisons.
-// Bound: arithmetic, not the E * 4 bytes per token (see the launcher's figures).
+// redux.sync (two with 64 bits, high word and low word) and a ballot for the lane it is in, instead
+// of five rounds of shuffles and comparisons.  Most tokens are chosen in float32 with the expert's
+// place in the key's last bits (choose_fast); where its errors could matter, exactly.
+// Bound: instructions, not the E * 4 bytes per token.  16,384 tokens of 256 float32 logits with a
+// bias, 4 of 8 groups kept: 18.8 us, 780 instructions per token and warp, issued in 76% of the cycles
+// (11 us if they were in all); the logits alone would take 2.6 us.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -92,7 +95,6 @@ struct RouteArgs {
     float *w;
 };
 
-// What a group is ranked by: its largest key, or the sum of its two largest scores.
 // (best, second) of one lane merged with another's.
 template <typename Key>
 __device__ __forceinline__ void merge2(Key &a1, Key &a2, Key b1, Key b2) {
