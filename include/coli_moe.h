@@ -379,6 +379,95 @@ coli_status coli_moe_fp4_pack_record(const coli_moe_config *cfg, int act, const 
                                      const void *wu, const void *wd, uint8_t *record, void *ws,
                                      void *stream);
 
+/* ---------------------------------------------------------------- rows to the experts and back ----
+ * For batches whose expert products run one by one (coli_moe_fp4_product, coli_moe_i8_product, a caller's own), in
+ * training too.  hidden may be any number up to 2^20, top_k up to 32, T * top_k up to 2^30 (COLI_ERR_UNSUPPORTED
+ * above); rows may lie any number of elements apart, at any address of their type.  Rows, pointers and strides that
+ * are multiples of 16 bytes go in 16-byte pieces, others element by element.  `ws`: 256-byte aligned, its
+ * header cleared once (coli_moe_clear_error), as for the layer. */
+
+/* a3 with positions and rows: a stable counting sort of the slots s = t * top_k + k by expert id.
+ *   offsets [n_experts + 1]  rows offsets[e] .. offsets[e+1] - 1 belong to expert e (n_experts <= 1024)
+ *   perm    [T * top_k]      slot of each row in that order; -1 from offsets[n_experts] on
+ *   place   [T * top_k]      row of each slot, or -1
+ *   rows                     row place[s] (at rows + place[s] * ldr elements) = row s / top_k of x (at x + t * ldx); rows from
+ *                            offsets[n_experts] on are left as they are.  x and rows both NULL: the sort alone.
+ * An id of -1 leaves its slot out (an expert of another device, a padded token); other ids outside [0,
+ * n_experts) do too and set COLI_DEVERR_EXPERT_ID in the error word of `ws`.  A token may name an expert twice.
+ * The gradient in x is coli_moe_combine of the rows' gradients without weights.  T = 0 writes offsets alone.
+ * One kernel, or two above 2048 slots; may be captured. */
+coli_status coli_moe_sort_rows(int n_experts, int top_k, int act, const void *x, int T, int hidden,
+                               size_t ldx, const int32_t *topk_ids, int32_t *offsets, int32_t *perm,
+                               int32_t *place, void *rows, size_t ldr, void *ws, void *stream);
+
+/* a7 for any rows: out[t] = add[t] + sum_k topk_w[t][k] * y[place[t][k]], float32 sums in the order add, k = 0, 1, ..,
+ * rounded once to out_type (coli_act; y has type act).  topk_w NULL: weights of 1 (the gradient of
+ * coli_moe_sort_rows); add NULL: 0; add may be out with the same stride, else out overlaps nothing.  A place of
+ * -1 adds nothing; another one outside [0, rows) neither, and sets COLI_DEVERR_GROUPING in the error word of
+ * `ws`.  A token without rows gives add[t].  T = 0 is a no-op.  One kernel, no atomics; may be captured. */
+coli_status coli_moe_combine(int act, const void *y, int rows, size_t ldy, const int32_t *place,
+                             const float *topk_w, int T, int top_k, int hidden, int out_type,
+                             const void *add, size_t ld_add, void *out, size_t ldo, void *ws,
+                             void *stream);
+
+/* The gradient of coli_moe_combine (that in add is dout itself):
+ *   dy[place[t][k]] = topk_w[t][k] * dout[t], rounded to act; rows that no place names are left as they are
+ *   dw[t][k] = sum_h dout[t][h] * y[place[t][k]][h], a float32 sum; 0 where the slot has no row
+ * dout has type out_type.  dy or dw may be NULL (not both); y is read for dw alone.  dy overlaps nothing.  Places as
+ * in coli_moe_combine, but different ones for all slots that have a row.  T = 0 is a no-op.  One kernel, no
+ * atomics; may be captured. */
+coli_status coli_moe_combine_grad(int act, const void *y, int rows, size_t ldy, const int32_t *place,
+                                  const float *topk_w, int T, int top_k, int hidden, int out_type,
+                                  const void *dout, size_t ld_dout, void *dy, size_t ld_dy, float *dw,
+                                  void *ws, void *stream);
+
+/* ---------------------------------------------------------------- 8-bit rows and products ----
+ * Rows of signed 8-bit codes with one float32 scale each: activations with a scale per token, weight matrices [n][k]
+ * with one per output channel.  k is any number up to 131071; rows lie `ld` bytes apart, a multiple of 16.
+ * An int8 record is such a pair of matrices: gate and up rows together n = 2 * inter, k = hidden, scales sg and su
+ * one after the other; down n = hidden, k = inter (codes_stride the record stride, scale_stride a quarter of it). */
+
+/* Quantises src_rows rows of k values: scale = m / 127 with m the row's largest |x|, at least 127 * 2^-126, rounded to
+ * float32; code = the whole number nearest to x * 127 / m of the real numbers, ties to even, so within [-127, 127].
+ * A row that holds a NaN or an infinity gets the scale NaN and codes 0.
+ *   swiglu = 0: row i is x + i * ldx (act: coli_act), k values.
+ *   swiglu = 1: row i holds k gate and then k up values; what is quantised is gate / (1 + exp(-gate)) * up in float32
+ *               (a few units of its last place; a gate of -infinity gives NaN).
+ * Row i goes to the rows place[i * copies + c], c < copies, of the result (device int32; a place of -1 is left out, another
+ * one outside [0, rows) too and sets COLI_DEVERR_GROUPING in the error word of `ws`; the places differ), as
+ * coli_moe_sort_rows gives them with copies = top_k.  place NULL: row i to row i, copies == 1, rows == src_rows.
+ * Rows of the result that nothing names are left as they are.  codes 16-byte aligned, ldc bytes from row to row, a
+ * multiple of 16; bytes from k to the next multiple of 16 become 0.  src_rows = 0 is a no-op.  One kernel. */
+coli_status coli_moe_i8_quantize(int act, int swiglu, const void *x, int src_rows, size_t ldx, int k,
+                                 const int32_t *place, int copies, int rows, int8_t *codes, size_t ldc,
+                                 float *scale, void *ws, void *stream);
+
+typedef struct {
+    const int8_t *codes;   /* [rows], ld bytes apart, 16-byte aligned */
+    const float *scale;    /* [rows], or NULL: 1 */
+    int rows;
+    size_t ld;             /* bytes; a multiple of 16 */
+} coli_i8_rows;
+
+typedef struct {
+    const int8_t *codes;   /* `count` matrices of n rows, ld bytes apart, 16-byte aligned */
+    const float *scale;    /* `count` arrays [n], or NULL: 1 */
+    int count, n;          /* count <= 1024 */
+    size_t ld;             /* bytes; a multiple of 16 */
+    size_t codes_stride;   /* bytes between matrices; a multiple of 16 */
+    size_t scale_stride;   /* elements */
+} coli_i8_mats;
+
+/* out[i][j] = a.scale[i] * w.scale[j] * sum_k a[i][k] * w[j][k] for every row i of `a`, w the matrix of the row's
+ * group; offsets, groups, rows outside every group, bad offsets, out_type, out and ldo as in coli_moe_fp4_product.
+ * Sums are exact (32-bit integers; any codes, -128 too), rounded to float32 and multiplied with the product of the two
+ * scales, itself rounded to float32; any finite scales will do, their product may leave float32's range where the
+ * result does not.  The same call gives the same bits.  rows = 0 is a no-op.  One kernel; allocates nothing;
+ * may be captured. */
+coli_status coli_moe_i8_product(const coli_i8_rows *a, const coli_i8_mats *w, int k,
+                                const int32_t *offsets, int out_type, void *out, size_t ldo, void *ws,
+                                void *stream);
+
 #ifdef __cplusplus
 }
 #endif

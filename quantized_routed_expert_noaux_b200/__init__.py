@@ -25,6 +25,8 @@ __all__ = [
     "MoERouter", "coli_moe_check_router", "coli_moe_route_scores",
     "FP4Rows", "FP4Mats", "coli_moe_fp4_scale_pitch", "coli_moe_fp4_scale_bytes", "coli_moe_fp4_quantize",
     "coli_moe_fp4_dequantize", "coli_moe_fp4_product", "coli_moe_fp4_pack_record", "fp4_rows_for", "fp4_mats_for",
+    "coli_moe_sort_rows", "coli_moe_combine", "coli_moe_combine_grad",
+    "I8Rows", "I8Mats", "coli_moe_i8_quantize", "coli_moe_i8_product", "i8_rows_for", "i8_mats_for",
     "COLI_W_NVFP4", "COLI_W_MXFP4", "COLI_SCORE_SIGMOID", "COLI_SCORE_SOFTMAX", "COLI_GROUP_TOP2", "COLI_GROUP_MAX",
     "COLI_FP4_MX", "COLI_FP4_NV", "COLI_FP4_ROWS", "COLI_FP4_TILES",
     "COLI_W_INT2", "COLI_W_INT4", "COLI_W_INT8", "COLI_ACT_F32", "COLI_ACT_BF16",
@@ -85,6 +87,19 @@ class FP4Mats(C.Structure):
     ]
 
 
+class I8Rows(C.Structure):
+    device = None  # of the tensors that i8_rows_for took
+    _fields_ = [("codes", C.c_void_p), ("scale", C.c_void_p), ("rows", C.c_int), ("ld", C.c_size_t)]
+
+
+class I8Mats(C.Structure):
+    device = None
+    _fields_ = [
+        ("codes", C.c_void_p), ("scale", C.c_void_p), ("count", C.c_int), ("n", C.c_int),
+        ("ld", C.c_size_t), ("codes_stride", C.c_size_t), ("scale_stride", C.c_size_t),
+    ]
+
+
 class ColiError(RuntimeError):
     def __init__(self, fn: str, status: int):
         self.status = status
@@ -128,6 +143,11 @@ def _load():
     L.coli_moe_fp4_dequantize.argtypes = [I, I, P, P, P, I, I, I, P, S, P]
     L.coli_moe_fp4_pack_record.argtypes = [cfgp, I, P, P, P, P, P, P]
     L.coli_moe_fp4_product.argtypes = [I, C.POINTER(FP4Rows), C.POINTER(FP4Mats), I, P, I, P, S, P, P]
+    L.coli_moe_sort_rows.argtypes = [I, I, I, P, I, I, S, P, P, P, P, P, S, P, P]
+    L.coli_moe_combine.argtypes = [I, P, I, S, P, P, I, I, I, I, P, S, P, S, P, P]
+    L.coli_moe_combine_grad.argtypes = [I, P, I, S, P, P, I, I, I, I, P, S, P, S, P, P, P]
+    L.coli_moe_i8_quantize.argtypes = [I, I, P, I, S, I, P, I, I, P, S, P, P, P]
+    L.coli_moe_i8_product.argtypes = [C.POINTER(I8Rows), C.POINTER(I8Mats), I, P, I, P, S, P, P]
     L.coli_moe_layer_kernels.restype = I
     L.coli_moe_layer_noalloc.restype = I
     for name in ("coli_moe_record_bytes", "coli_moe_check_config", "coli_moe_workspace_size",
@@ -136,7 +156,9 @@ def _load():
                  "coli_moe_residual", "coli_moe_debug_set_wait", "coli_moe_set_dispatch_threshold",
                  "coli_moe_noalloc_error_word", "coli_moe_check_router", "coli_moe_route_scores",
                  "coli_moe_fp4_scale_pitch", "coli_moe_fp4_scale_bytes", "coli_moe_fp4_quantize",
-                 "coli_moe_fp4_dequantize", "coli_moe_fp4_product", "coli_moe_fp4_pack_record"):
+                 "coli_moe_fp4_dequantize", "coli_moe_fp4_product", "coli_moe_fp4_pack_record",
+                 "coli_moe_sort_rows", "coli_moe_combine", "coli_moe_combine_grad", "coli_moe_i8_quantize",
+                 "coli_moe_i8_product"):
         getattr(L, name).restype = I
     return L
 
@@ -463,5 +485,86 @@ def fp4_mats_for(codes, scales, row_scale=None) -> FP4Mats:
     if not together or at < 0:
         raise ColiError("fp4_mats_for", 1)
     w = FP4Mats(codes.data_ptr(), scales.data_ptr(), row, count, n, c[0], s[0], r[0])
+    w.device = at
+    return w
+
+
+# ------------------------------------------------------------------ rows to the experts and back, 8-bit products
+
+_c_sort_rows, _c_combine, _c_combine_grad = lib.coli_moe_sort_rows, lib.coli_moe_combine, lib.coli_moe_combine_grad
+_c_i8_quantize, _c_i8_product = lib.coli_moe_i8_quantize, lib.coli_moe_i8_product
+
+
+def coli_moe_sort_rows(n_experts, top_k, act, x, T, hidden, ldx, topk_ids, offsets, perm, place, rows, ldr, ws, stream=None) -> None:
+    """Slots sorted by expert: offsets [n_experts + 1], perm and place [T * top_k], and the slots' rows of x
+    (x and rows None: the sort alone).  An id of -1 leaves its slot out."""
+    x, topk_ids, offsets, perm, place, rows, ws, st = _pointers("coli_moe_sort_rows", stream, x, topk_ids, offsets, perm, place, rows, ws)
+    status = _c_sort_rows(n_experts, top_k, act, x, T, hidden, ldx, topk_ids, offsets, perm, place, rows, ldr, ws, st)
+    if status:
+        raise ColiError("coli_moe_sort_rows", status)
+
+
+def coli_moe_combine(act, y, rows, ldy, place, topk_w, T, top_k, hidden, out_type, add, ld_add, out, ldo, ws, stream=None) -> None:
+    """out[t] = add[t] + sum_k topk_w[t, k] * y[place[t, k]] (topk_w None: 1; add None: 0)."""
+    y, place, topk_w, add, out, ws, st = _pointers("coli_moe_combine", stream, y, place, topk_w, add, out, ws)
+    status = _c_combine(act, y, rows, ldy, place, topk_w, T, top_k, hidden, out_type, add, ld_add, out, ldo, ws, st)
+    if status:
+        raise ColiError("coli_moe_combine", status)
+
+
+def coli_moe_combine_grad(act, y, rows, ldy, place, topk_w, T, top_k, hidden, out_type, dout, ld_dout, dy, ld_dy, dw, ws,
+                          stream=None) -> None:
+    """The gradient of coli_moe_combine: dy rows [place] and dw [T, top_k], either may be None."""
+    y, place, topk_w, dout, dy, dw, ws, st = _pointers("coli_moe_combine_grad", stream, y, place, topk_w, dout, dy, dw, ws)
+    status = _c_combine_grad(act, y, rows, ldy, place, topk_w, T, top_k, hidden, out_type, dout, ld_dout, dy, ld_dy, dw, ws, st)
+    if status:
+        raise ColiError("coli_moe_combine_grad", status)
+
+
+def coli_moe_i8_quantize(act, swiglu, x, src_rows, ldx, k, place, copies, rows, codes, ldc, scale, ws, stream=None) -> None:
+    """Rows of x (row i at element i * ldx), or SiLU(gate) * up of rows of k gate and k up values, to 8-bit codes with a
+    scale each; row i to the rows place[i * copies + c] of the result, or to row i."""
+    x, place, codes, scale, ws, st = _pointers("coli_moe_i8_quantize", stream, x, place, codes, scale, ws)
+    status = _c_i8_quantize(act, swiglu, x, src_rows, ldx, k, place, copies, rows, codes, ldc, scale, ws, st)
+    if status:
+        raise ColiError("coli_moe_i8_quantize", status)
+
+
+def coli_moe_i8_product(a: I8Rows, w: I8Mats, k, offsets, out_type, out, ldo, ws, stream=None) -> None:
+    """out row i = a's row i times the matrix of its group (offsets [count + 1] int32; None: one matrix)."""
+    operands = {getattr(m, "device", None) for m in (a, w)} - {None}
+    operands |= {t.get_device() for t in (out, ws, offsets) if hasattr(t, "get_device")}
+    if len(operands) > 1:
+        raise ColiError("coli_moe_i8_product", 1)
+    offsets, out, ws, st = _pointers("coli_moe_i8_product", stream, offsets, out, ws)
+    status = _c_i8_product(a, w, k, offsets, out_type, out, ldo, ws, st)
+    if status:
+        raise ColiError("coli_moe_i8_product", status)
+
+
+def i8_rows_for(codes, scale=None) -> I8Rows:
+    """I8Rows over device tensors: codes [rows, >= k] int8, the values of a row side by side, scale [rows] contiguous."""
+    at = codes.get_device()
+    r, ld = codes.shape[0], codes.stride(0)
+    if codes.dim() != 2 or codes.stride(1) != 1 or not (scale is None or scale.is_contiguous()):
+        raise ColiError("i8_rows_for", 2)
+    if at < 0 or not (scale is None or scale.get_device() == at):
+        raise ColiError("i8_rows_for", 1)
+    a = I8Rows(codes.data_ptr(), _p(scale), r, ld)
+    a.device = at
+    return a
+
+
+def i8_mats_for(codes, scale=None) -> I8Mats:
+    """I8Mats over device tensors: codes [count, n, >= k] int8, the values of a row side by side, scale [count, n] with a
+    matrix's scales side by side."""
+    at = codes.get_device()
+    count, n, _ = codes.shape
+    c = codes.stride()
+    if c[2] != 1 or not (scale is None or scale.stride(1) == 1):
+        raise ColiError("i8_mats_for", 2)
+    if at < 0 or not (scale is None or scale.get_device() == at):
+        raise ColiError("i8_mats_for", 1)
+    w = I8Mats(codes.data_ptr(), _p(scale), count, n, c[1], c[0], 0 if scale is None else scale.stride(0))
     w.device = at
     return w

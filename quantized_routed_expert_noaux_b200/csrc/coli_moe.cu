@@ -8,10 +8,12 @@
 
 #include "coli_moe.h"
 #include "fp4.h"
+#include "i8.h"
 #include "gate.h"
 #include "internal.h"
 #include "residual.h"
 #include "route_scores.h"
+#include "sorted_rows.h"
 
 namespace coli {
 
@@ -682,6 +684,178 @@ coli_status coli_moe_fp4_pack_record(const coli_moe_config *c, int act, const vo
     a.scales = record + r.sd;
     a.row_scale = fmt == COLI_FP4_NV ? reinterpret_cast<float *>(record + r.rd) : nullptr;
     return from_cuda(launch_fp4_quantize(fmt, COLI_FP4_TILES, act, a, static_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------- rows to the experts and back
+
+static bool bad_act(int act) { return act != COLI_ACT_F32 && act != COLI_ACT_BF16; }
+static size_t item_of(int act) { return act == COLI_ACT_F32 ? 4 : 2; }
+
+static coli_status rows_shape(int T, int top_k, int hidden) {
+    if (T < 0 || top_k < 1 || hidden < 1) return COLI_ERR_SHAPE;
+    if (top_k > 32 || hidden > (1 << 20) || static_cast<long>(T) * top_k > (1 << 30)) return COLI_ERR_UNSUPPORTED;
+    return COLI_OK;
+}
+
+coli_status coli_moe_sort_rows(int n_experts, int top_k, int act, const void *x, int T, int hidden, size_t ldx,
+                               const int32_t *topk_ids, int32_t *offsets, int32_t *perm, int32_t *place, void *rows,
+                               size_t ldr, void *ws, void *stream) {
+    if (bad_act(act) || (x == nullptr) != (rows == nullptr)) return COLI_ERR_INVALID_ARG;
+    const coli_status s = rows_shape(T, top_k, x ? hidden : 1);
+    if (s != COLI_OK) return s;
+    if (n_experts < 1 || (x && (ldx < static_cast<size_t>(hidden) || ldr < static_cast<size_t>(hidden)))) return COLI_ERR_SHAPE;
+    if (n_experts > 1024) return COLI_ERR_UNSUPPORTED;
+    if (!offsets || (T > 0 && (!topk_ids || !perm || !place))) return COLI_ERR_INVALID_ARG;
+    if (!aligned(topk_ids, 4) || !aligned(offsets, 4) || !aligned(perm, 4) || !aligned(place, 4) || !aligned(x, item_of(act)) ||
+        !aligned(rows, item_of(act)))
+        return COLI_ERR_ALIGN;
+    if (!ws || !aligned(ws, 256)) return COLI_ERR_WORKSPACE;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) return from_cuda(cudaMemsetAsync(offsets, 0, (static_cast<size_t>(n_experts) + 1) * sizeof(int32_t), st));
+    SortArgs a;
+    a.ids = topk_ids;
+    a.T = T;
+    a.K = top_k;
+    a.E = n_experts;
+    a.offsets = offsets;
+    a.perm = perm;
+    a.place = place;
+    a.x = x;
+    a.hidden = hidden;
+    a.ldx = ldx;
+    a.ldr = ldr;
+    a.rows = rows;
+    a.err = static_cast<int *>(ws);
+    return from_cuda(launch_sort_rows(act, a, st));
+}
+
+coli_status coli_moe_combine(int act, const void *y, int rows, size_t ldy, const int32_t *place, const float *topk_w, int T,
+                             int top_k, int hidden, int out_type, const void *add, size_t ld_add, void *out, size_t ldo,
+                             void *ws, void *stream) {
+    if (bad_act(act) || bad_act(out_type)) return COLI_ERR_INVALID_ARG;
+    const coli_status s = rows_shape(T, top_k, hidden);
+    if (s != COLI_OK) return s;
+    const size_t h = static_cast<size_t>(hidden);
+    if (rows < 0 || ldy < h || ldo < h || (add && ld_add < h)) return COLI_ERR_SHAPE;
+    if (T == 0) return COLI_OK;
+    if ((!y && rows > 0) || !place || !out) return COLI_ERR_INVALID_ARG;
+    if (!aligned(y, item_of(act)) || !aligned(place, 4) || !aligned(topk_w, 4) || !aligned(add, item_of(out_type)) || !aligned(out, item_of(out_type)))
+        return COLI_ERR_ALIGN;
+    if (!ws || !aligned(ws, 256)) return COLI_ERR_WORKSPACE;
+    CombineArgs a;
+    a.y = y;
+    a.rows = rows;
+    a.T = T;
+    a.K = top_k;
+    a.hidden = hidden;
+    a.ldy = ldy;
+    a.place = place;
+    a.w = topk_w;
+    a.add = add;
+    a.out = out;
+    a.ld_add = ld_add;
+    a.ldo = ldo;
+    a.err = static_cast<int *>(ws);
+    return from_cuda(launch_combine(act, out_type, a, static_cast<cudaStream_t>(stream)));
+}
+
+coli_status coli_moe_combine_grad(int act, const void *y, int rows, size_t ldy, const int32_t *place, const float *topk_w, int T,
+                                  int top_k, int hidden, int out_type, const void *dout, size_t ld_dout, void *dy, size_t ld_dy,
+                                  float *dw, void *ws, void *stream) {
+    if (bad_act(act) || bad_act(out_type)) return COLI_ERR_INVALID_ARG;
+    const coli_status s = rows_shape(T, top_k, hidden);
+    if (s != COLI_OK) return s;
+    const size_t h = static_cast<size_t>(hidden);
+    if (rows < 0 || ld_dout < h || (dw && ldy < h) || (dy && ld_dy < h)) return COLI_ERR_SHAPE;
+    if (T == 0) return COLI_OK;
+    if (!place || !dout || (!dy && !dw) || (dw && !y && rows > 0)) return COLI_ERR_INVALID_ARG;
+    if (!aligned(place, 4) || !aligned(topk_w, 4) || !aligned(dout, item_of(out_type)) || !aligned(dy, item_of(act)) || !aligned(dw, 4) ||
+        (dw && !aligned(y, item_of(act))))
+        return COLI_ERR_ALIGN;
+    if (!ws || !aligned(ws, 256)) return COLI_ERR_WORKSPACE;
+    CombineGradArgs a;
+    a.y = dw ? y : nullptr;
+    a.rows = rows;
+    a.T = T;
+    a.K = top_k;
+    a.hidden = hidden;
+    a.ldy = ldy;
+    a.place = place;
+    a.w = topk_w;
+    a.dout = dout;
+    a.dy = dy;
+    a.dw = dw;
+    a.ld_dout = ld_dout;
+    a.ld_dy = ld_dy;
+    a.err = static_cast<int *>(ws);
+    return from_cuda(launch_combine_grad(act, out_type, a, static_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------- 8-bit rows and their product
+
+static coli_status i8_shape(int rows, int k) {
+    if (rows < 0 || k < 1) return COLI_ERR_SHAPE;
+    return rows > (1 << 30) || k > I8_MAX_K ? COLI_ERR_UNSUPPORTED : COLI_OK;
+}
+
+coli_status coli_moe_i8_quantize(int act, int swiglu, const void *x, int src_rows, size_t ldx, int k, const int32_t *place,
+                                 int copies, int rows, int8_t *codes, size_t ldc, float *scale, void *ws, void *stream) {
+    if (bad_act(act) || (swiglu != 0 && swiglu != 1)) return COLI_ERR_INVALID_ARG;
+    coli_status s = i8_shape(rows, k);
+    if (s == COLI_OK) s = i8_shape(src_rows, k);
+    if (s != COLI_OK) return s;
+    if (ldx < static_cast<size_t>(k) * (swiglu ? 2 : 1) || ldc < static_cast<size_t>(k) || copies < 1) return COLI_ERR_SHAPE;
+    if (!place && (copies != 1 || rows != src_rows)) return COLI_ERR_SHAPE;
+    if (static_cast<long>(src_rows) * copies > (1L << 30)) return COLI_ERR_UNSUPPORTED;
+    if (src_rows == 0) return COLI_OK;
+    if (!x || (rows > 0 && (!codes || !scale))) return COLI_ERR_INVALID_ARG;
+    if (!aligned(x, item_of(act)) || !aligned(place, 4) || !aligned(codes, 16) || ldc % 16 || !aligned(scale, 4)) return COLI_ERR_ALIGN;
+    if (!ws || !aligned(ws, 256)) return COLI_ERR_WORKSPACE;
+    I8QuantArgs a;
+    a.x = x;
+    a.src_rows = src_rows;
+    a.k = k;
+    a.ldx = ldx;
+    a.place = place;
+    a.copies = copies;
+    a.rows = rows;
+    a.codes = codes;
+    a.ldc = ldc;
+    a.row_scale = scale;
+    a.err = static_cast<int *>(ws);
+    return from_cuda(launch_i8_quantize(act, swiglu != 0, a, static_cast<cudaStream_t>(stream)));
+}
+
+coli_status coli_moe_i8_product(const coli_i8_rows *a, const coli_i8_mats *w, int k, const int32_t *offsets, int out_type, void *out,
+                                size_t ldo, void *ws, void *stream) {
+    if (!a || !w || bad_act(out_type)) return COLI_ERR_INVALID_ARG;
+    const coli_status s = i8_shape(a->rows, k);
+    if (s != COLI_OK) return s;
+    const size_t kk = static_cast<size_t>(k);
+    if (w->count <= 0 || w->n <= 0 || ldo < static_cast<size_t>(w->n) || a->ld < kk || w->ld < kk) return COLI_ERR_SHAPE;
+    if (!offsets && w->count != 1) return COLI_ERR_SHAPE;
+    // (strides of tensor maps are below 2^40; tiles of all groups, even of groups that overlap, are counted in 32 bits)
+    if (w->count > 1024 || a->ld >> 30 || w->ld >> 30 || (w->count > 1 && w->codes_stride >> 40) || static_cast<size_t>(w->n) * w->ld >> 40 ||
+        (static_cast<long>(a->rows) / 16 + 1) * ((w->n + 127L) / 128) * (w->count + 1) > 0x7fffffffL)
+        return COLI_ERR_UNSUPPORTED;
+    if (w->count > 1 && (w->codes_stride < (static_cast<size_t>(w->n) - 1) * w->ld + kk || (w->scale && w->scale_stride < static_cast<size_t>(w->n))))
+        return COLI_ERR_SHAPE;
+    if (a->rows == 0) return COLI_OK;
+    if (!a->codes || !w->codes || !out) return COLI_ERR_INVALID_ARG;
+    if (!aligned(a->codes, 16) || a->ld % 16 || !aligned(w->codes, 16) || w->ld % 16 || (w->count > 1 && w->codes_stride % 16) ||
+        !aligned(a->scale, 4) || !aligned(w->scale, 4) || !aligned(offsets, 4) || !aligned(out, item_of(out_type)))
+        return COLI_ERR_ALIGN;
+    if (!ws || !aligned(ws, 256)) return COLI_ERR_WORKSPACE;
+    I8ProductArgs p;
+    p.a = *a;
+    p.w = *w;
+    p.k = k;
+    p.offsets = offsets;
+    p.out_type = out_type;
+    p.out = out;
+    p.ldo = ldo;
+    p.err = static_cast<int *>(ws);
+    return from_cuda(launch_i8_product(p, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

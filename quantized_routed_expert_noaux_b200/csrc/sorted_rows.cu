@@ -1,0 +1,455 @@
+// sorted_rows.cu -- the slots of a routed batch sorted by expert with their tokens' rows (coli_moe_sort_rows), the
+// weighted sum of every token's expert rows (coli_moe_combine; without weights and addend the gradient of the sorted
+// rows) and its gradient (coli_moe_combine_grad).
+//
+//   place[s] = #(slots of lower experts) + #(earlier slots of the same expert),  rows[place[t K + k]] = x[t]
+//   out[t]   = add[t] + sum_k w[t][k] y[place[t K + k]]
+//   dy[place[t K + k]] = w[t][k] dout[t],  dw[t][k] = sum_h dout[t][h] y[place[t K + k]][h]
+//
+// All three move rows and compute next to nothing: HBM bounds them.  Every row is read once, by 16-byte pieces where
+// its address allows it; a token's K rows are in flight together.  No atomics on data: the same call gives the same
+// bits.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "internal.h"
+#include "pdl.h"
+#include "sorted_rows.h"
+
+namespace coli {
+
+namespace {
+
+constexpr unsigned FULL = 0xffffffffu;
+
+// ------------------------------------------------------------------ elements
+
+// V elements of a row in float32 registers and back, rounded once.
+template <typename T, int V>
+__device__ __forceinline__ void load_row(float (&v)[V], const T *p) {
+    if constexpr (sizeof(T) == 4) {
+        if constexpr (V % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i) {
+                const float4 f = __ldg(reinterpret_cast<const float4 *>(p) + i);
+                v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = __ldg(p + i);
+        }
+    } else {
+        uint32_t w[(V + 1) / 2];
+        if constexpr (V == 8) {
+            const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p));
+            w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
+        } else if constexpr (V == 4) {
+            const uint2 q = __ldg(reinterpret_cast<const uint2 *>(p));
+            w[0] = q.x; w[1] = q.y;
+        } else {
+            static_assert(V == 1, "");
+            w[0] = __ldg(reinterpret_cast<const uint16_t *>(p));
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_row(T *p, const float (&v)[V]) {
+    if constexpr (sizeof(T) == 4) {
+        if constexpr (V % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i) reinterpret_cast<float4 *>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) p[i] = v[i];
+        }
+    } else if constexpr (V == 1) {
+        *p = __float2bfloat16_rn(v[0]);
+    } else {
+        uint32_t w[V / 2];
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        if constexpr (V == 8) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        else *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    }
+}
+
+// Threads and pieces of a row of n items: at most `most` threads, rows cut evenly.
+struct Cut {
+    int threads, pieces;
+};
+inline Cut cut(int n, int most) {
+    Cut c;
+    c.pieces = (n + most - 1) / most;
+    c.threads = ((n + c.pieces - 1) / c.pieces + 31) / 32 * 32;
+    return c;
+}
+
+// ------------------------------------------------------------------ sort
+
+constexpr int SMALL_N = 2048;   // slots that every CTA counts by itself
+constexpr int SMALL_T = 256;    // threads at most
+
+// One kernel for few slots: CTA (token, piece of its row) counts where the token's slots go and copies the piece there.
+// An id that is no expert's sorts behind all experts; its slot is not placed.
+template <typename Item>
+__global__ void __launch_bounds__(SMALL_T) sort_small_kernel(const SortArgs a, int items, size_t px, size_t pr) {
+    __shared__ int s_id[SMALL_N];
+    __shared__ int s_place[32];
+    wait_for_previous();
+    const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int n = a.T * a.K;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const int id = __ldg(a.ids + i);
+        s_id[i] = static_cast<unsigned>(id) < static_cast<unsigned>(a.E) ? id : a.E;
+        if (id != -1 && s_id[i] == a.E && t == 0 && blockIdx.y == 0) atomicOr(a.err, COLI_DEVERR_EXPERT_ID);
+    }
+    __syncthreads();
+    for (int k = warp; k < a.K; k += warps) {
+        const int s = t * a.K + k, id = s_id[s];
+        int before = 0;
+        for (int i = lane; i < n; i += 32) before += s_id[i] < id || (s_id[i] == id && i < s);
+        before = __reduce_add_sync(FULL, before);
+        if (lane == 0) {
+            const int to = id < a.E ? before : -1;
+            s_place[k] = to;
+            if (blockIdx.y == 0) {
+                a.place[s] = to;
+                a.perm[before] = id < a.E ? s : -1;
+            }
+        }
+    }
+    if (blockIdx.y == 0) {
+        if (n <= 64) {
+            for (int e = t * blockDim.x + threadIdx.x; e <= a.E; e += a.T * blockDim.x) {
+                int before = 0;
+                for (int i = 0; i < n; ++i) before += s_id[i] < e;
+                a.offsets[e] = before;
+            }
+        } else {
+            for (int e = t * warps + warp; e <= a.E; e += a.T * warps) {
+                int before = 0;
+                for (int i = lane; i < n; i += 32) before += s_id[i] < e;
+                before = __reduce_add_sync(FULL, before);
+                if (lane == 0) a.offsets[e] = before;
+            }
+        }
+    }
+    if (!a.x) return;
+    __syncthreads();
+    const int i = blockIdx.y * blockDim.x + threadIdx.x;
+    if (i >= items) return;
+    const Item v = __ldg(static_cast<const Item *>(a.x) + t * px + i);
+    for (int k = 0; k < a.K; ++k) {
+        const int to = s_place[k];
+        if (to >= 0) static_cast<Item *>(a.rows)[to * pr + i] = v;
+    }
+}
+
+// Many slots: a cluster of SORT_CTAS CTAs sorts them (a share of the slots each, a warp its part of that, in order), then
+// a second kernel copies the rows.  Pass 1 counts by warp and expert; the scans over warps, CTAs (through each
+// other's shared memory) and experts turn the counts into first positions; pass 2 places the slots.
+constexpr int SORT_CTAS = 8, SORT_WARPS = 32;
+
+__device__ __forceinline__ const int *peer(const int *p, int rank) {
+    uint64_t r;
+    asm("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+    return reinterpret_cast<const int *>(r);
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__global__ void __launch_bounds__(SORT_WARPS * 32) sort_cluster_kernel(const SortArgs a) {  // one cluster of SORT_CTAS
+    extern __shared__ int sm[];
+    const int B = a.E + 1;              // the last for ids that are no expert's
+    int *wc = sm;                       // [SORT_WARPS][B]: counts, then cursors
+    int *tot = sm + SORT_WARPS * B;     // [B]: this CTA's counts
+    __shared__ int s_scan[SORT_WARPS];
+    wait_for_previous();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x;
+    const long n = static_cast<long>(a.T) * a.K;
+    const int part = rank * SORT_WARPS + warp, parts = SORT_CTAS * SORT_WARPS;
+    const int lo = static_cast<int>(n * part / parts), hi = static_cast<int>(n * (part + 1) / parts);
+    for (int i = tid; i < SORT_WARPS * B; i += SORT_WARPS * 32) wc[i] = 0;
+    __syncthreads();
+    const unsigned lt = (1u << lane) - 1u;
+    int *mine = wc + warp * B;
+    bool bad = false;
+    auto bucket = [&](int s) {          // lanes behind the end: a value of their own
+        if (s >= hi) return -1 - lane;
+        const int id = __ldg(a.ids + s);
+        const bool ok = static_cast<unsigned>(id) < static_cast<unsigned>(a.E);
+        bad = bad || (!ok && id != -1);
+        return ok ? id : a.E;
+    };
+    for (int base = lo; base < hi; base += 32) {
+        const int id = bucket(base + lane);
+        const unsigned peers = __match_any_sync(FULL, id);
+        if (id >= 0 && (peers & lt) == 0) mine[id] += __popc(peers);
+        __syncwarp();
+    }
+    if (bad) atomicOr(a.err, COLI_DEVERR_EXPERT_ID);
+    __syncthreads();
+    for (int e = tid; e < B; e += SORT_WARPS * 32) {
+        int run = 0;
+        for (int w = 0; w < SORT_WARPS; ++w) {
+            const int c = wc[w * B + e];
+            wc[w * B + e] = run;
+            run += c;
+        }
+        tot[e] = run;
+    }
+    cluster_sync_all();
+    // bucket e of thread e (and 1024): what lower CTAs hold of it, and all CTAs; then the scan over the buckets
+    int carry = 0;
+    for (int base = 0; base < B; base += SORT_WARPS * 32) {
+        const int e = base + tid;
+        int below = 0, all = 0;
+        if (e < B) {
+#pragma unroll
+            for (int c = 0; c < SORT_CTAS; ++c) {
+                const int v = *peer(tot + e, c);
+                below += c < rank ? v : 0;
+                all += v;
+            }
+        }
+        int inc = all;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(FULL, inc, o);
+            if (lane >= o) inc += v;
+        }
+        if (lane == 31) s_scan[warp] = inc;
+        __syncthreads();
+        int before = carry;
+        for (int w = 0; w < SORT_WARPS; ++w) {
+            const int v = s_scan[w];
+            before += w < warp ? v : 0;
+            carry += v;
+        }
+        const int first = before + inc - all;
+        if (e < B) {
+            if (rank == 0) a.offsets[e] = first;
+            for (int w = 0; w < SORT_WARPS; ++w) wc[w * B + e] += first + below;
+        }
+        __syncthreads();
+    }
+    for (int base = lo; base < hi; base += 32) {
+        const int s = base + lane, id = bucket(s);
+        const unsigned peers = __match_any_sync(FULL, id);
+        if (id >= 0) {
+            const int to = mine[id] + __popc(peers & lt);
+            a.place[s] = id < a.E ? to : -1;
+            a.perm[to] = id < a.E ? s : -1;
+        }
+        __syncwarp();
+        if (id >= 0 && (peers & lt) == 0) mine[id] += __popc(peers);
+        __syncwarp();
+    }
+    cluster_sync_all();  // no CTA leaves while another reads its counts
+}
+
+// Row t of x to the places of its K slots, a piece of the row per CTA.
+template <typename Item>
+__global__ void __launch_bounds__(256) sort_copy_kernel(const SortArgs a, int items, size_t px, size_t pr) {
+    wait_for_previous();
+    const int t = blockIdx.x, i = blockIdx.y * blockDim.x + threadIdx.x;
+    if (i >= items) return;
+    const Item v = __ldg(static_cast<const Item *>(a.x) + t * px + i);
+    const int32_t *place = a.place + static_cast<size_t>(t) * a.K;
+    for (int k = 0; k < a.K; ++k) {
+        const int to = place[k];
+        if (to >= 0) static_cast<Item *>(a.rows)[to * pr + i] = v;
+    }
+}
+
+template <typename Item>
+cudaError_t sort_rows(const SortArgs &a, int item, cudaStream_t st) {
+    const int ratio = sizeof(Item) / item, items = a.x ? a.hidden / ratio : 1;
+    const size_t px = a.ldx / ratio, pr = a.ldr / ratio;
+    const Cut c = cut(items, SMALL_T);
+    const int n = a.T * a.K;
+    if (n <= SMALL_N) {
+        // (eight warps count, whatever the row's length)
+        return launch_early(sort_small_kernel<Item>, dim3(a.T, a.x ? (items + SMALL_T - 1) / SMALL_T : 1), SMALL_T, 0, st, 1, a, items, px, pr);
+    }
+    const size_t smem = static_cast<size_t>(SORT_WARPS + 1) * (a.E + 1) * sizeof(int);
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        const int most = (SORT_WARPS + 1) * 1025 * static_cast<int>(sizeof(int));
+        if ((e = cudaFuncSetAttribute(sort_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    if ((e = launch_early(sort_cluster_kernel, dim3(SORT_CTAS), SORT_WARPS * 32, smem, st, SORT_CTAS, a)) != cudaSuccess || !a.x) return e;
+    return launch_early(sort_copy_kernel<Item>, dim3(a.T, c.pieces), c.threads, 0, st, 1, a, items, px, pr);
+}
+
+// ------------------------------------------------------------------ combine
+
+constexpr int CT = 256;         // threads at most
+constexpr int DEPTH = 8;        // rows of a token in flight
+
+template <typename Act, typename Out, int V>
+__global__ void __launch_bounds__(CT) combine_kernel(const CombineArgs a) {
+    wait_for_previous();
+    const int t = blockIdx.x, c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
+    if (c >= a.hidden) return;
+    const int32_t *place = a.place + static_cast<size_t>(t) * a.K;
+    const float *w = a.w ? a.w + static_cast<size_t>(t) * a.K : nullptr;
+    float acc[V];
+    if (a.add) {
+        load_row<Out, V>(acc, static_cast<const Out *>(a.add) + t * a.ld_add + c);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    }
+    for (int k0 = 0; k0 < a.K; k0 += DEPTH) {
+        float v[DEPTH][V], f[DEPTH];
+        bool have[DEPTH];
+#pragma unroll
+        for (int k = 0; k < DEPTH; ++k) {
+            have[k] = false;
+            if (k0 + k < a.K) {
+                const int at = __ldg(place + k0 + k);
+                have[k] = at >= 0 && at < a.rows;
+                if (at < -1 || at >= a.rows) atomicOr(a.err, COLI_DEVERR_GROUPING);
+                if (have[k]) {
+                    load_row<Act, V>(v[k], static_cast<const Act *>(a.y) + at * a.ldy + c);
+                    f[k] = w ? __ldg(w + k0 + k) : 1.f;
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < DEPTH; ++k)
+            if (have[k]) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] = fmaf(f[k], v[k][i], acc[i]);
+            }
+    }
+    store_row<Out, V>(static_cast<Out *>(a.out) + t * a.ldo + c, acc);
+}
+
+// ------------------------------------------------------------------ gradient
+
+// A CTA per token: DEPTH of its rows at a time, the products with dout summed over the CTA.
+template <typename Act, typename Out, int V>
+__global__ void __launch_bounds__(CT) combine_grad_kernel(const CombineGradArgs a) {
+    __shared__ float s_sum[CT / 32][DEPTH];
+    wait_for_previous();
+    const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int32_t *place = a.place + static_cast<size_t>(t) * a.K;
+    const float *w = a.w ? a.w + static_cast<size_t>(t) * a.K : nullptr;
+    for (int k0 = 0; k0 < a.K; k0 += DEPTH) {
+        int at[DEPTH];
+        float f[DEPTH], dot[DEPTH];
+#pragma unroll
+        for (int k = 0; k < DEPTH; ++k) {
+            at[k] = k0 + k < a.K ? __ldg(place + k0 + k) : -1;
+            if (at[k] < -1 || at[k] >= a.rows) {
+                at[k] = -1;
+                if (threadIdx.x == 0) atomicOr(a.err, COLI_DEVERR_GROUPING);
+            }
+            f[k] = w && at[k] >= 0 ? __ldg(w + k0 + k) : 1.f;
+            dot[k] = 0.f;
+        }
+        for (int c = threadIdx.x * V; c < a.hidden; c += blockDim.x * V) {
+            float d[V];
+            load_row<Out, V>(d, static_cast<const Out *>(a.dout) + t * a.ld_dout + c);
+            if (a.dw) {
+                float v[DEPTH][V];
+#pragma unroll
+                for (int k = 0; k < DEPTH; ++k)
+                    if (at[k] >= 0) load_row<Act, V>(v[k], static_cast<const Act *>(a.y) + at[k] * a.ldy + c);
+#pragma unroll
+                for (int k = 0; k < DEPTH; ++k)
+                    if (at[k] >= 0) {
+#pragma unroll
+                        for (int i = 0; i < V; ++i) dot[k] = fmaf(d[i], v[k][i], dot[k]);
+                    }
+            }
+            if (a.dy) {
+#pragma unroll
+                for (int k = 0; k < DEPTH; ++k)
+                    if (at[k] >= 0) {
+                        float v[V];
+#pragma unroll
+                        for (int i = 0; i < V; ++i) v[i] = f[k] * d[i];
+                        store_row<Act, V>(static_cast<Act *>(a.dy) + at[k] * a.ld_dy + c, v);
+                    }
+            }
+        }
+        if (!a.dw) continue;
+#pragma unroll
+        for (int k = 0; k < DEPTH; ++k) {
+#pragma unroll
+            for (int o = 16; o; o >>= 1) dot[k] += __shfl_xor_sync(FULL, dot[k], o);
+            if (lane == 0) s_sum[warp][k] = dot[k];
+        }
+        __syncthreads();
+        if (threadIdx.x < DEPTH && k0 + threadIdx.x < a.K) {
+            float sum = 0.f;
+            for (int i = 0; i < warps; ++i) sum += s_sum[i][threadIdx.x];
+            a.dw[static_cast<size_t>(t) * a.K + k0 + threadIdx.x] = sum;
+        }
+        __syncthreads();
+    }
+}
+
+// Whether rows of `item`-byte elements can be taken `v` elements at a time.
+bool whole(const void *p, size_t ld, size_t item, int v) {
+    return !p || ((reinterpret_cast<uintptr_t>(p) | ld * item) & (item * v < 16 ? item * v - 1 : 15)) == 0;
+}
+
+template <typename Act, typename Out>
+cudaError_t combine(const CombineArgs &a, cudaStream_t st) {
+    constexpr int V = 16 / sizeof(Act);
+    if (a.hidden % V == 0 && whole(a.y, a.ldy, sizeof(Act), V) && whole(a.add, a.ld_add, sizeof(Out), V) && whole(a.out, a.ldo, sizeof(Out), V)) {
+        const Cut c = cut(a.hidden / V, CT);
+        return launch_early(combine_kernel<Act, Out, V>, dim3(a.T, c.pieces), c.threads, 0, st, 1, a);
+    }
+    const Cut c = cut(a.hidden, CT);
+    return launch_early(combine_kernel<Act, Out, 1>, dim3(a.T, c.pieces), c.threads, 0, st, 1, a);
+}
+
+template <typename Act, typename Out>
+cudaError_t combine_grad(const CombineGradArgs &a, cudaStream_t st) {
+    constexpr int V = 16 / sizeof(Act);
+    if (a.hidden % V == 0 && whole(a.y, a.ldy, sizeof(Act), V) && whole(a.dout, a.ld_dout, sizeof(Out), V) && whole(a.dy, a.ld_dy, sizeof(Act), V))
+        return launch_early(combine_grad_kernel<Act, Out, V>, dim3(a.T), cut(a.hidden / V, CT).threads, 0, st, 1, a);
+    return launch_early(combine_grad_kernel<Act, Out, 1>, dim3(a.T), cut(a.hidden, CT).threads, 0, st, 1, a);
+}
+
+}  // namespace
+
+cudaError_t launch_sort_rows(int act, const SortArgs &a, cudaStream_t st) {
+    const int item = act == COLI_ACT_F32 ? 4 : 2;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.rows) | a.ldx * item | a.ldr * item | static_cast<size_t>(a.hidden) * item;
+    if (!a.x || (at & 15) == 0) return sort_rows<uint4>(a, item, st);
+    if ((at & 3) == 0) return sort_rows<uint32_t>(a, item, st);
+    return sort_rows<uint16_t>(a, item, st);
+}
+
+cudaError_t launch_combine(int act, int out_type, const CombineArgs &a, cudaStream_t st) {
+    if (act == COLI_ACT_F32)
+        return out_type == COLI_ACT_F32 ? combine<float, float>(a, st) : combine<float, __nv_bfloat16>(a, st);
+    return out_type == COLI_ACT_F32 ? combine<__nv_bfloat16, float>(a, st) : combine<__nv_bfloat16, __nv_bfloat16>(a, st);
+}
+
+cudaError_t launch_combine_grad(int act, int out_type, const CombineGradArgs &a, cudaStream_t st) {
+    if (act == COLI_ACT_F32)
+        return out_type == COLI_ACT_F32 ? combine_grad<float, float>(a, st) : combine_grad<float, __nv_bfloat16>(a, st);
+    return out_type == COLI_ACT_F32 ? combine_grad<__nv_bfloat16, float>(a, st) : combine_grad<__nv_bfloat16, __nv_bfloat16>(a, st);
+}
+
+}  // namespace coli
