@@ -27,36 +27,30 @@ constexpr unsigned FULL = 0xffffffffu;
 
 // ------------------------------------------------------------------ elements
 
-// V elements of a row in float32 registers and back, rounded once.
+// V elements of a row as they lie in memory.
 template <typename T, int V>
-__device__ __forceinline__ void load_row(float (&v)[V], const T *p) {
-    if constexpr (sizeof(T) == 4) {
-        if constexpr (V % 4 == 0) {
-#pragma unroll
-            for (int i = 0; i < V / 4; ++i) {
-                const float4 f = __ldg(reinterpret_cast<const float4 *>(p) + i);
-                v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
-            }
+struct Raw {
+    static constexpr int BYTES = sizeof(T) * V, WORDS = BYTES < 4 ? 1 : BYTES / 4;
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (BYTES == 32) {
+            asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "l"(p));
+        } else if constexpr (BYTES == 16) {
+            asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+        } else if constexpr (BYTES == 8) {
+            asm volatile("ld.global.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+        } else if constexpr (BYTES == 4) {
+            w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
         } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = __ldg(p + i);
-        }
-    } else {
-        uint32_t w[(V + 1) / 2];
-        if constexpr (V == 8) {
-            const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p));
-            w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
-        } else if constexpr (V == 4) {
-            const uint2 q = __ldg(reinterpret_cast<const uint2 *>(p));
-            w[0] = q.x; w[1] = q.y;
-        } else {
-            static_assert(V == 1, "");
             w[0] = __ldg(reinterpret_cast<const uint16_t *>(p));
         }
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
     }
-}
+    __device__ __forceinline__ float at(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    }
+};
 template <typename T, int V>
 __device__ __forceinline__ void store_row(T *p, const float (&v)[V]) {
     if constexpr (sizeof(T) == 4) {
@@ -299,111 +293,153 @@ cudaError_t sort_rows(const SortArgs &a, int item, cudaStream_t st) {
 
 constexpr int CT = 256;         // threads at most
 constexpr int DEPTH = 8;        // rows of a token in flight
+constexpr int CTAS = 4;         // resident per SM
 
-template <typename Act, typename Out, int V>
-__global__ void __launch_bounds__(CT) combine_kernel(const CombineArgs a) {
-    wait_for_previous();
-    const int t = blockIdx.x, c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
-    if (c >= a.hidden) return;
-    const int32_t *place = a.place + static_cast<size_t>(t) * a.K;
-    const float *w = a.w ? a.w + static_cast<size_t>(t) * a.K : nullptr;
-    float acc[V];
-    if (a.add) {
-        load_row<Out, V>(acc, static_cast<const Out *>(a.add) + t * a.ld_add + c);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = 0.f;
+// Rows place[k0 .. k0 + DEPTH) of a token and their weights, one per lane; -1 where there is none.
+struct Slots {
+    int at;
+    float f;
+    __device__ __forceinline__ void load(const int32_t *place, const float *w, size_t t, int K, int k0, int lane) {
+        const bool mine = lane < DEPTH && k0 + lane < K;
+        at = mine ? __ldg(place + t * K + k0 + lane) : -1;
+        f = mine && w ? __ldg(w + t * K + k0 + lane) : 1.f;
     }
-    for (int k0 = 0; k0 < a.K; k0 += DEPTH) {
-        float v[DEPTH][V], f[DEPTH];
-        bool have[DEPTH];
+    __device__ __forceinline__ void check(int rows, int *err) {
+        if (at < -1 || at >= rows) {
+            at = -1;
+            atomicOr(err, COLI_DEVERR_GROUPING);
+        }
+    }
+};
+
+// A CTA takes pieces of tokens' rows, one after another; the next one's places are on their way meanwhile.
+template <typename Act, typename Out, int V>
+__global__ void __launch_bounds__(CT, CTAS) combine_kernel(const CombineArgs a, int pieces) {
+    wait_for_previous();
+    const int lane = threadIdx.x & 31;
+    int t = blockIdx.x / pieces, piece = blockIdx.x - t * pieces;
+    const int dt = gridDim.x / pieces, dp = gridDim.x - dt * pieces;
+    Slots next;
+    if (t < a.T) next.load(a.place, a.w, t, a.K, 0, lane);
+    while (t < a.T) {
+        Slots s = next;
+        const int c = (piece * blockDim.x + threadIdx.x) * V;
+        const size_t t0 = t;
+        t += dt;
+        piece += dp;
+        if (piece >= pieces) {
+            piece -= pieces;
+            ++t;
+        }
+        if (t < a.T) next.load(a.place, a.w, t, a.K, 0, lane);
+        float acc[V];
+        if (a.add && c < a.hidden) {
+            Raw<Out, V> r;
+            r.load(static_cast<const Out *>(a.add) + t0 * a.ld_add + c);
 #pragma unroll
-        for (int k = 0; k < DEPTH; ++k) {
-            have[k] = false;
-            if (k0 + k < a.K) {
-                const int at = __ldg(place + k0 + k);
-                have[k] = at >= 0 && at < a.rows;
-                if (at < -1 || at >= a.rows) atomicOr(a.err, COLI_DEVERR_GROUPING);
-                if (have[k]) {
-                    load_row<Act, V>(v[k], static_cast<const Act *>(a.y) + at * a.ldy + c);
-                    f[k] = w ? __ldg(w + k0 + k) : 1.f;
+            for (int i = 0; i < V; ++i) acc[i] = r.at(i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = 0.f;
+        }
+        for (int k0 = 0; k0 < a.K; k0 += DEPTH) {
+            if (k0) s.load(a.place, a.w, t0, a.K, k0, lane);
+            s.check(a.rows, a.err);
+            Raw<Act, V> v[DEPTH];
+#pragma unroll
+            for (int k = 0; k < DEPTH; ++k) {
+                const int at = __shfl_sync(FULL, s.at, k);
+                if (at >= 0 && c < a.hidden) v[k].load(static_cast<const Act *>(a.y) + at * a.ldy + c);
+            }
+#pragma unroll
+            for (int k = 0; k < DEPTH; ++k) {
+                const float f = __shfl_sync(FULL, s.f, k);
+                if (__shfl_sync(FULL, s.at, k) >= 0) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) acc[i] = fmaf(f, v[k].at(i), acc[i]);
                 }
             }
         }
-#pragma unroll
-        for (int k = 0; k < DEPTH; ++k)
-            if (have[k]) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] = fmaf(f[k], v[k][i], acc[i]);
-            }
+        if (c < a.hidden) store_row<Out, V>(static_cast<Out *>(a.out) + t0 * a.ldo + c, acc);
     }
-    store_row<Out, V>(static_cast<Out *>(a.out) + t * a.ldo + c, acc);
 }
 
 // ------------------------------------------------------------------ gradient
 
-// A CTA per token: DEPTH of its rows at a time, the products with dout summed over the CTA.
+// A CTA takes tokens one after another, DEPTH of their rows at a time; the products with dout are summed over the CTA.
 template <typename Act, typename Out, int V>
-__global__ void __launch_bounds__(CT) combine_grad_kernel(const CombineGradArgs a) {
-    __shared__ float s_sum[CT / 32][DEPTH];
+__global__ void __launch_bounds__(CT, CTAS) combine_grad_kernel(const CombineGradArgs a) {
+    __shared__ float s_sum[2][CT / 32][DEPTH];
     wait_for_previous();
-    const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int32_t *place = a.place + static_cast<size_t>(t) * a.K;
-    const float *w = a.w ? a.w + static_cast<size_t>(t) * a.K : nullptr;
-    for (int k0 = 0; k0 < a.K; k0 += DEPTH) {
-        int at[DEPTH];
-        float f[DEPTH], dot[DEPTH];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    int buf = 0;
+    Slots next;
+    if (blockIdx.x < a.T) next.load(a.place, a.w, blockIdx.x, a.K, 0, lane);
+    for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+        Slots s = next;
+        if (t + static_cast<int>(gridDim.x) < a.T) next.load(a.place, a.w, t + gridDim.x, a.K, 0, lane);
+        for (int k0 = 0; k0 < a.K; k0 += DEPTH, buf ^= 1) {
+            if (k0) s.load(a.place, a.w, t, a.K, k0, lane);
+            s.check(a.rows, a.err);
+            float dot[DEPTH];
 #pragma unroll
-        for (int k = 0; k < DEPTH; ++k) {
-            at[k] = k0 + k < a.K ? __ldg(place + k0 + k) : -1;
-            if (at[k] < -1 || at[k] >= a.rows) {
-                at[k] = -1;
-                if (threadIdx.x == 0) atomicOr(a.err, COLI_DEVERR_GROUPING);
-            }
-            f[k] = w && at[k] >= 0 ? __ldg(w + k0 + k) : 1.f;
-            dot[k] = 0.f;
-        }
-        for (int c = threadIdx.x * V; c < a.hidden; c += blockDim.x * V) {
-            float d[V];
-            load_row<Out, V>(d, static_cast<const Out *>(a.dout) + t * a.ld_dout + c);
-            if (a.dw) {
-                float v[DEPTH][V];
+            for (int k = 0; k < DEPTH; ++k) dot[k] = 0.f;
+            for (int c0 = 0; c0 < a.hidden; c0 += blockDim.x * V) {
+                const int c = c0 + threadIdx.x * V;
+                const bool in = c < a.hidden;
+                Raw<Out, V> d;
+                Raw<Act, V> v[DEPTH];
+                if (in) d.load(static_cast<const Out *>(a.dout) + t * a.ld_dout + c);
+                if (a.dw) {
 #pragma unroll
-                for (int k = 0; k < DEPTH; ++k)
-                    if (at[k] >= 0) load_row<Act, V>(v[k], static_cast<const Act *>(a.y) + at[k] * a.ldy + c);
-#pragma unroll
-                for (int k = 0; k < DEPTH; ++k)
-                    if (at[k] >= 0) {
-#pragma unroll
-                        for (int i = 0; i < V; ++i) dot[k] = fmaf(d[i], v[k][i], dot[k]);
+                    for (int k = 0; k < DEPTH; ++k) {
+                        const int at = __shfl_sync(FULL, s.at, k);
+                        if (at >= 0 && in) v[k].load(static_cast<const Act *>(a.y) + at * a.ldy + c);
                     }
-            }
-            if (a.dy) {
+                }
+                if (a.dy) {
 #pragma unroll
-                for (int k = 0; k < DEPTH; ++k)
-                    if (at[k] >= 0) {
-                        float v[V];
+                    for (int k = 0; k < DEPTH; ++k) {
+                        const int at = __shfl_sync(FULL, s.at, k);
+                        const float f = __shfl_sync(FULL, s.f, k);
+                        if (at >= 0 && in) {
+                            float g[V];
 #pragma unroll
-                        for (int i = 0; i < V; ++i) v[i] = f[k] * d[i];
-                        store_row<Act, V>(static_cast<Act *>(a.dy) + at[k] * a.ld_dy + c, v);
+                            for (int i = 0; i < V; ++i) g[i] = f * d.at(i);
+                            store_row<Act, V>(static_cast<Act *>(a.dy) + at * a.ld_dy + c, g);
+                        }
                     }
+                }
+                if (a.dw) {
+#pragma unroll
+                    for (int k = 0; k < DEPTH; ++k)
+                        if (__shfl_sync(FULL, s.at, k) >= 0 && in) {
+#pragma unroll
+                            for (int i = 0; i < V; ++i) dot[k] = fmaf(d.at(i), v[k].at(i), dot[k]);
+                        }
+                }
+            }
+            if (!a.dw) continue;
+#pragma unroll
+            for (int k = 0; k < DEPTH; ++k) {
+#pragma unroll
+                for (int o = 16; o; o >>= 1) dot[k] += __shfl_xor_sync(FULL, dot[k], o);
+                if (lane == 0) s_sum[buf][warp][k] = dot[k];
+            }
+            __syncthreads();  // (the buffer is written again two rounds on: its readers have met the next round's barrier)
+            if (threadIdx.x < DEPTH && k0 + threadIdx.x < a.K) {
+                float sum = 0.f;
+                for (int i = 0; i < warps; ++i) sum += s_sum[buf][i][threadIdx.x];
+                a.dw[static_cast<size_t>(t) * a.K + k0 + threadIdx.x] = sum;
             }
         }
-        if (!a.dw) continue;
-#pragma unroll
-        for (int k = 0; k < DEPTH; ++k) {
-#pragma unroll
-            for (int o = 16; o; o >>= 1) dot[k] += __shfl_xor_sync(FULL, dot[k], o);
-            if (lane == 0) s_sum[warp][k] = dot[k];
-        }
-        __syncthreads();
-        if (threadIdx.x < DEPTH && k0 + threadIdx.x < a.K) {
-            float sum = 0.f;
-            for (int i = 0; i < warps; ++i) sum += s_sum[i][threadIdx.x];
-            a.dw[static_cast<size_t>(t) * a.K + k0 + threadIdx.x] = sum;
-        }
-        __syncthreads();
     }
+}
+
+// CTAs for n pieces of work: those that are resident at once.
+unsigned resident(long n) {
+    const long most = static_cast<long>(device_sm_count()) * CTAS;
+    return static_cast<unsigned>(n < most ? n : most);
 }
 
 // Whether rows of `item`-byte elements can be taken `v` elements at a time.
@@ -416,18 +452,18 @@ cudaError_t combine(const CombineArgs &a, cudaStream_t st) {
     constexpr int V = 16 / sizeof(Act);
     if (a.hidden % V == 0 && whole(a.y, a.ldy, sizeof(Act), V) && whole(a.add, a.ld_add, sizeof(Out), V) && whole(a.out, a.ldo, sizeof(Out), V)) {
         const Cut c = cut(a.hidden / V, CT);
-        return launch_early(combine_kernel<Act, Out, V>, dim3(a.T, c.pieces), c.threads, 0, st, 1, a);
+        return launch_early(combine_kernel<Act, Out, V>, dim3(resident(static_cast<long>(a.T) * c.pieces)), c.threads, 0, st, 1, a, c.pieces);
     }
     const Cut c = cut(a.hidden, CT);
-    return launch_early(combine_kernel<Act, Out, 1>, dim3(a.T, c.pieces), c.threads, 0, st, 1, a);
+    return launch_early(combine_kernel<Act, Out, 1>, dim3(resident(static_cast<long>(a.T) * c.pieces)), c.threads, 0, st, 1, a, c.pieces);
 }
 
 template <typename Act, typename Out>
 cudaError_t combine_grad(const CombineGradArgs &a, cudaStream_t st) {
     constexpr int V = 16 / sizeof(Act);
     if (a.hidden % V == 0 && whole(a.y, a.ldy, sizeof(Act), V) && whole(a.dout, a.ld_dout, sizeof(Out), V) && whole(a.dy, a.ld_dy, sizeof(Act), V))
-        return launch_early(combine_grad_kernel<Act, Out, V>, dim3(a.T), cut(a.hidden / V, CT).threads, 0, st, 1, a);
-    return launch_early(combine_grad_kernel<Act, Out, 1>, dim3(a.T), cut(a.hidden, CT).threads, 0, st, 1, a);
+        return launch_early(combine_grad_kernel<Act, Out, V>, dim3(resident(a.T)), cut(a.hidden / V, CT).threads, 0, st, 1, a);
+    return launch_early(combine_grad_kernel<Act, Out, 1>, dim3(resident(a.T)), cut(a.hidden, CT).threads, 0, st, 1, a);
 }
 
 }  // namespace
