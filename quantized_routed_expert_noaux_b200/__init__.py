@@ -495,19 +495,42 @@ _c_sort_rows, _c_combine, _c_combine_grad = lib.coli_moe_sort_rows, lib.coli_moe
 _c_i8_quantize, _c_i8_product = lib.coli_moe_i8_quantize, lib.coli_moe_i8_product
 
 
+def _quick(fn: str, stream, at: int, together: bool) -> Optional[int]:
+    """The stream of a call whose tensors lie on device `at`: the usual case without helpers in between."""
+    if together and stream is None and _torch_device is not None and at == _torch_device():
+        return _torch_stream(at)
+    return _stream_at(fn, stream, at, together)
+
+
 def coli_moe_sort_rows(n_experts, top_k, act, x, T, hidden, ldx, topk_ids, offsets, perm, place, rows, ldr, ws, stream=None) -> None:
     """Slots sorted by expert: offsets [n_experts + 1], perm and place [T * top_k], and the slots' rows of x
     (x and rows None: the sort alone).  An id of -1 leaves its slot out."""
-    x, topk_ids, offsets, perm, place, rows, ws, st = _pointers("coli_moe_sort_rows", stream, x, topk_ids, offsets, perm, place, rows, ws)
-    status = _c_sort_rows(n_experts, top_k, act, x, T, hidden, ldx, topk_ids, offsets, perm, place, rows, ldr, ws, st)
+    try:
+        at = ws.get_device()
+        together = (at == topk_ids.get_device() == offsets.get_device() == perm.get_device() == place.get_device() and
+                    (x is None or at == x.get_device()) and (rows is None or at == rows.get_device()))
+        st = _quick("coli_moe_sort_rows", stream, at, together)
+        status = _c_sort_rows(n_experts, top_k, act, None if x is None else x.data_ptr(), T, hidden, ldx, topk_ids.data_ptr(), offsets.data_ptr(),
+                              perm.data_ptr(), place.data_ptr(), None if rows is None else rows.data_ptr(), ldr, ws.data_ptr(), st)
+    except AttributeError:  # device pointers or None among them
+        x, topk_ids, offsets, perm, place, rows, ws, st = _pointers("coli_moe_sort_rows", stream, x, topk_ids, offsets, perm, place, rows, ws)
+        status = _c_sort_rows(n_experts, top_k, act, x, T, hidden, ldx, topk_ids, offsets, perm, place, rows, ldr, ws, st)
     if status:
         raise ColiError("coli_moe_sort_rows", status)
 
 
 def coli_moe_combine(act, y, rows, ldy, place, topk_w, T, top_k, hidden, out_type, add, ld_add, out, ldo, ws, stream=None) -> None:
     """out[t] = add[t] + sum_k topk_w[t, k] * y[place[t, k]] (topk_w None: 1; add None: 0)."""
-    y, place, topk_w, add, out, ws, st = _pointers("coli_moe_combine", stream, y, place, topk_w, add, out, ws)
-    status = _c_combine(act, y, rows, ldy, place, topk_w, T, top_k, hidden, out_type, add, ld_add, out, ldo, ws, st)
+    try:
+        at = out.get_device()
+        together = (at == y.get_device() == place.get_device() == ws.get_device() and
+                    (topk_w is None or at == topk_w.get_device()) and (add is None or at == add.get_device()))
+        st = _quick("coli_moe_combine", stream, at, together)
+        status = _c_combine(act, y.data_ptr(), rows, ldy, place.data_ptr(), None if topk_w is None else topk_w.data_ptr(), T, top_k, hidden, out_type,
+                            None if add is None else add.data_ptr(), ld_add, out.data_ptr(), ldo, ws.data_ptr(), st)
+    except AttributeError:
+        y, place, topk_w, add, out, ws, st = _pointers("coli_moe_combine", stream, y, place, topk_w, add, out, ws)
+        status = _c_combine(act, y, rows, ldy, place, topk_w, T, top_k, hidden, out_type, add, ld_add, out, ldo, ws, st)
     if status:
         raise ColiError("coli_moe_combine", status)
 
@@ -515,8 +538,17 @@ def coli_moe_combine(act, y, rows, ldy, place, topk_w, T, top_k, hidden, out_typ
 def coli_moe_combine_grad(act, y, rows, ldy, place, topk_w, T, top_k, hidden, out_type, dout, ld_dout, dy, ld_dy, dw, ws,
                           stream=None) -> None:
     """The gradient of coli_moe_combine: dy rows [place] and dw [T, top_k], either may be None."""
-    y, place, topk_w, dout, dy, dw, ws, st = _pointers("coli_moe_combine_grad", stream, y, place, topk_w, dout, dy, dw, ws)
-    status = _c_combine_grad(act, y, rows, ldy, place, topk_w, T, top_k, hidden, out_type, dout, ld_dout, dy, ld_dy, dw, ws, st)
+    try:
+        at = dout.get_device()
+        together = (at == place.get_device() == ws.get_device() and (y is None or at == y.get_device()) and
+                    (topk_w is None or at == topk_w.get_device()) and (dy is None or at == dy.get_device()) and (dw is None or at == dw.get_device()))
+        st = _quick("coli_moe_combine_grad", stream, at, together)
+        status = _c_combine_grad(act, None if y is None else y.data_ptr(), rows, ldy, place.data_ptr(), None if topk_w is None else topk_w.data_ptr(), T,
+                                 top_k, hidden, out_type, dout.data_ptr(), ld_dout, None if dy is None else dy.data_ptr(), ld_dy,
+                                 None if dw is None else dw.data_ptr(), ws.data_ptr(), st)
+    except AttributeError:
+        y, place, topk_w, dout, dy, dw, ws, st = _pointers("coli_moe_combine_grad", stream, y, place, topk_w, dout, dy, dw, ws)
+        status = _c_combine_grad(act, y, rows, ldy, place, topk_w, T, top_k, hidden, out_type, dout, ld_dout, dy, ld_dy, dw, ws, st)
     if status:
         raise ColiError("coli_moe_combine_grad", status)
 
@@ -524,20 +556,34 @@ def coli_moe_combine_grad(act, y, rows, ldy, place, topk_w, T, top_k, hidden, ou
 def coli_moe_i8_quantize(act, swiglu, x, src_rows, ldx, k, place, copies, rows, codes, ldc, scale, ws, stream=None) -> None:
     """Rows of x (row i at element i * ldx), or SiLU(gate) * up of rows of k gate and k up values, to 8-bit codes with a
     scale each; row i to the rows place[i * copies + c] of the result, or to row i."""
-    x, place, codes, scale, ws, st = _pointers("coli_moe_i8_quantize", stream, x, place, codes, scale, ws)
-    status = _c_i8_quantize(act, swiglu, x, src_rows, ldx, k, place, copies, rows, codes, ldc, scale, ws, st)
+    try:
+        at = x.get_device()
+        together = at == codes.get_device() == scale.get_device() == ws.get_device() and (place is None or at == place.get_device())
+        st = _quick("coli_moe_i8_quantize", stream, at, together)
+        status = _c_i8_quantize(act, swiglu, x.data_ptr(), src_rows, ldx, k, None if place is None else place.data_ptr(), copies, rows,
+                                codes.data_ptr(), ldc, scale.data_ptr(), ws.data_ptr(), st)
+    except AttributeError:
+        x, place, codes, scale, ws, st = _pointers("coli_moe_i8_quantize", stream, x, place, codes, scale, ws)
+        status = _c_i8_quantize(act, swiglu, x, src_rows, ldx, k, place, copies, rows, codes, ldc, scale, ws, st)
     if status:
         raise ColiError("coli_moe_i8_quantize", status)
 
 
 def coli_moe_i8_product(a: I8Rows, w: I8Mats, k, offsets, out_type, out, ldo, ws, stream=None) -> None:
     """out row i = a's row i times the matrix of its group (offsets [count + 1] int32; None: one matrix)."""
-    operands = {getattr(m, "device", None) for m in (a, w)} - {None}
-    operands |= {t.get_device() for t in (out, ws, offsets) if hasattr(t, "get_device")}
-    if len(operands) > 1:
-        raise ColiError("coli_moe_i8_product", 1)
-    offsets, out, ws, st = _pointers("coli_moe_i8_product", stream, offsets, out, ws)
-    status = _c_i8_product(a, w, k, offsets, out_type, out, ldo, ws, st)
+    try:
+        at = out.get_device()
+        together = (at == ws.get_device() and (offsets is None or at == offsets.get_device()) and
+                    (a.device is None or at == a.device) and (w.device is None or at == w.device))
+        st = _quick("coli_moe_i8_product", stream, at, together)
+        status = _c_i8_product(a, w, k, None if offsets is None else offsets.data_ptr(), out_type, out.data_ptr(), ldo, ws.data_ptr(), st)
+    except AttributeError:
+        operands = {getattr(m, "device", None) for m in (a, w)} - {None}
+        operands |= {t.get_device() for t in (out, ws, offsets) if hasattr(t, "get_device")}
+        if len(operands) > 1:
+            raise ColiError("coli_moe_i8_product", 1) from None
+        offsets, out, ws, st = _pointers("coli_moe_i8_product", stream, offsets, out, ws)
+        status = _c_i8_product(a, w, k, offsets, out_type, out, ldo, ws, st)
     if status:
         raise ColiError("coli_moe_i8_product", status)
 

@@ -185,11 +185,12 @@ __device__ __forceinline__ int scaled_sum(int v, float pw, float px) {
     const float s = __int_as_float(v);
     return __float_as_int((px < 1.f) == (pw < 1.f) ? s * px * pw : s * (px * pw));
 }
-// A run of 32 rows (rx: row `lane`'s) x a weight row per lane, whose part of the exponent is `pw`.
-__device__ __forceinline__ void split_scales(int (&v)[32], float pw, float &rx) {
+// A run of N rows (rx: row `lane`'s) x a weight row per lane, whose part of the exponent is `pw`.
+template <int N>
+__device__ __forceinline__ void split_scales(int (&v)[N], float pw, float &rx) {
     const float px = halve_exponent(rx);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = scaled_sum(v[j], pw, __shfl_sync(0xffffffffu, px, j));
+    for (int j = 0; j < N; ++j) v[j] = scaled_sum(v[j], pw, __shfl_sync(0xffffffffu, px, j));
 }
 
 // Split k, one epilogue warp's 32 weight rows: ranks above 0 send their sums to rank 0's shared memory by
@@ -250,10 +251,10 @@ __device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap *m,
     asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
                  ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(bar) : "memory");
 }
-// arrive on the barrier at this address in both CTAs once the MMAs issued so far have completed
-__device__ __forceinline__ void pair_commit(uint32_t mbar) {
+// arrive on the barrier at this address in both CTAs (`both`: the ranks' bits) once the MMAs issued so far have completed
+__device__ __forceinline__ void pair_commit(uint32_t mbar, uint16_t both = 3) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                 ::"r"(mbar), "h"(static_cast<uint16_t>(3)) : "memory");
+                 ::"r"(mbar), "h"(both) : "memory");
 }
 
 // Clusters of c CTAs, one CTA per SM, that run at once: with c = 4 some SMs of a GPC are left over (33

@@ -32,11 +32,11 @@ constexpr int A_BYTES = 128 * KB;        // weight codes of a k-block
 constexpr int W_PROD = 0, W_MMA = 1, W_EPI0 = 2, N_EPI = 4;
 constexpr int THREADS = (W_EPI0 + N_EPI) * 32;
 
-template <int NT>
+template <int NT, bool SPLIT>
 struct Plan {
     static constexpr int B_BYTES = NT * KB;
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int PART = NT <= 32 ? (MAX_SPLIT - 1) * 32 * 128 * 4 : 0;  // split k: the other ranks' sums
+    static constexpr int PART = SPLIT ? (MAX_SPLIT - 1) * NT / MAX_SPLIT * 128 * 4 : 0;  // split k: the other CTAs' sums (most with MAX_SPLIT of them)
     static constexpr int S = (216 * 1024 - PART) / STAGE;                       // ring stages
     static constexpr int ACC = NT <= 32 ? 32 : 128;                             // columns of an accumulator
     static constexpr size_t SMEM = static_cast<size_t>(S) * STAGE + PART + 1024;
@@ -75,26 +75,91 @@ __device__ __forceinline__ void prefetch_maps(const GemmMaps &m) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&m.b[0])) : "memory");
 }
 
-__device__ __forceinline__ int add_ints(int a, int b) { return a + b; }
-
-// The sums of a run of 32 rows, as float32, times what of the scales' exponents does not go through their product.
+// The sums of a run of N rows, as float32, times what of the scales' exponents does not go through their product.
 // (The sum is rounded to 24 bits once, the product of the scales once, and theirs once.)
-__device__ __forceinline__ void run_sums(int (&v)[32], float &rw, float &rx) {
+template <int N>
+__device__ __forceinline__ void run_sums(int (&v)[N], float &rw, float &rx) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = __float_as_int(__int2float_rn(v[j]));
+    for (int j = 0; j < N; ++j) v[j] = __float_as_int(__int2float_rn(v[j]));
     if (!__all_sync(0xffffffffu, ordinary(rw) && ordinary(rx))) {
         const float pw = halve_exponent(rw);
         split_scales(v, pw, rx);
     }
 }
+// Rows g .. of a tile x weight row r of this lane, from the lanes: out wants weight rows side by side.
+template <int OUT, int N>
+__device__ __forceinline__ void store_run(const GemmArgs &p, const Tile &x, int (&v)[N], int g, int r, float rw) {
+    const int lane = threadIdx.x & 31;
+    float rx = p.xscale && lane < N && g + lane < x.nr ? __ldg(p.xscale + x.n0 + g + lane) : 1.f;
+    run_sums(v, rw, rx);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        if (g + j >= x.nr) break;  // the same for the whole warp
+        const float y = __int_as_float(v[j]) * (rw * __shfl_sync(0xffffffffu, rx, j));
+        if (r < p.n) {
+            const size_t at = static_cast<size_t>(x.n0 + g + j) * p.ldo + r;
+            if (OUT == COLI_ACT_F32) static_cast<float *>(p.out)[at] = y;
+            else static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(y);
+        }
+    }
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, int (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]) : "r"(taddr) : "memory");
+}
+// Split k over the C CTAs of a cluster.  A tile's columns go in pieces of 8, `per` of them to each CTA in turn: every CTA
+// sends its sums of the others' pieces by stores that count on the owner's barrier as they land (no fence), adds
+// what comes in for its own, and stores those.  `part`: [C - 1 senders][2 per halves of a piece][128 weight rows] of 16 bytes.
+// pfull waits for every warp of the cluster, a CTA that owns nothing included: one that ran ahead could complete another's
+// pfree twice before that looked at it.  tl counts the tiles; `last`: none follows.  One epilogue warp's 32 weight rows; false
+// when a wait gave up.
+template <int OUT>
+__device__ __forceinline__ bool split_tile(const GemmArgs &p, const Tile &x, uint32_t dt, int C, int rank, int q, int r, float rw, uint32_t tl, bool last,
+                                           unsigned char *part, uint64_t *pfull, uint64_t *pfree, volatile int *abort) {
+    const int lane = threadIdx.x & 31, row = 32 * q + lane;
+    const int pieces = (x.nr + 7) / 8, per = (pieces + C - 1) / C;
+    const int lo = min(rank * per, pieces), own = min(pieces - lo, per);
+    if (lane == 0) mbar_expect_tx(smem_u32(pfull), (C - 1) * 32 * 32 * own);  // this warp's rows
+    if (tl > 0 && !__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(pfree), (tl & 1) ^ 1, abort, p.err))) return false;
+    for (int i = 0; i < pieces; ++i) {
+        const int to = i / per;
+        if (to == rank) continue;
+        int v[8];
+        tmem_ld8(dt + 8 * i, v);
+        const int unit = (rank < to ? rank : rank - 1) * 2 * per + 2 * (i - to * per);
+        const uint32_t dst = map_rank(smem_u32(part) + (unit * 128 + row) * 16, to), bar = map_rank(smem_u32(pfull), to);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];"
+                         ::"r"(dst + h * 2048), "r"(v[4 * h]), "r"(v[4 * h + 1]), "r"(v[4 * h + 2]), "r"(v[4 * h + 3]), "r"(bar) : "memory");
+    }
+    if (lane < C && lane != rank) remote_arrive(map_rank(smem_u32(pfull), lane));
+    if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(pfull), tl & 1, abort, p.err))) return false;
+    for (int i = 0; i < own; ++i) {
+        int v[8];
+        tmem_ld8(dt + 8 * (lo + i), v);
+        for (int c = 0; c < C - 1; ++c)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int4 f = *reinterpret_cast<const int4 *>(part + ((c * 2 * per + 2 * i + h) * 128 + row) * 16);
+                v[4 * h] += f.x;
+                v[4 * h + 1] += f.y;
+                v[4 * h + 2] += f.z;
+                v[4 * h + 3] += f.w;
+            }
+        store_run<OUT>(p, x, v, 8 * (lo + i), r, rw);
+    }
+    __syncwarp();
+    if (lane < C && lane != rank && !last) remote_arrive(map_rank(smem_u32(pfree), lane));
+    return true;
+}
 
-template <int NT, int OUT>
+template <int NT, int OUT, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1) i8_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs p) {
-    using P = Plan<NT>;
+    using P = Plan<NT, SPLIT>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char *sa = sm, *sb = sa + P::S * A_BYTES;
-    constexpr bool SPLIT = NT <= 32;
     __shared__ __align__(8) uint64_t bars[2 * P::S + 7];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_tiles;
@@ -103,8 +168,8 @@ __global__ void __launch_bounds__(THREADS, 1) i8_gemm_kernel(const __grid_consta
     uint64_t *full = bars, *empty = full + P::S;
     uint64_t *dfull = empty + P::S, *dempty = dfull + 2, *drain = dempty + 2;
     uint64_t *pfull = drain + 1, *pfree = pfull + 1;  // split k: partial sums there; their place free again
-    float *part = reinterpret_cast<float *>(sb + P::S * P::B_BYTES);
-    // split k: the CTAs of a cluster take a share of the k-blocks each; rank 0 adds and stores
+    unsigned char *part = sb + P::S * P::B_BYTES;
+    // split k: the CTAs of a cluster take a share of the k-blocks each
     const int C = SPLIT ? static_cast<int>(cluster_size()) : 1, rank = SPLIT ? static_cast<int>(cluster_rank()) : 0;
     const int first = blockIdx.x / C, stride = gridDim.x / C;
     volatile int *abort = &s_abort;
@@ -123,8 +188,8 @@ __global__ void __launch_bounds__(THREADS, 1) i8_gemm_kernel(const __grid_consta
             mbar_init(smem_u32(&dempty[i]), N_EPI * 32);
         }
         mbar_init(smem_u32(drain), 1);
-        mbar_init(smem_u32(pfull), N_EPI);
-        mbar_init(smem_u32(pfree), N_EPI);
+        mbar_init(smem_u32(pfull), C * N_EPI);
+        mbar_init(smem_u32(pfree), (C > 1 ? C - 1 : 1) * N_EPI);
         s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -224,24 +289,13 @@ __global__ void __launch_bounds__(THREADS, 1) i8_gemm_kernel(const __grid_consta
             if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&dfull[acc]), (tl >> 1) & 1, abort, p.err))) break;
             tc_fence_after();
             const uint32_t dt = tbase + acc * P::ACC + (static_cast<uint32_t>(32 * q) << 16);
-            for (int g = 0; g < x.nr; g += 32) {
-                int v[32];
-                tmem_ld32(dt + g, v);
-                if (SPLIT && C > 1) {
-                    if (!split_sum(v, x.nr, C, rank, q, lane, tl, t + stride >= ntiles, part, pfull, pfree, abort, p.err, add_ints)) break;
-                    if (rank != 0) break;
-                }
-                float rx = p.xscale && g + lane < x.nr ? __ldg(p.xscale + x.n0 + g + lane) : 1.f, rwg = rw;
-                run_sums(v, rwg, rx);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    if (g + j >= x.nr) break;  // the same for the whole warp
-                    const float y = __int_as_float(v[j]) * (rwg * __shfl_sync(0xffffffffu, rx, j));
-                    if (r < p.n) {
-                        const size_t at = static_cast<size_t>(x.n0 + g + j) * p.ldo + r;
-                        if (OUT == COLI_ACT_F32) static_cast<float *>(p.out)[at] = y;
-                        else static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(y);
-                    }
+            if (SPLIT && C > 1) {
+                if (!split_tile<OUT>(p, x, dt, C, rank, q, r, rw, tl, t + stride >= ntiles, part, pfull, pfree, abort)) break;
+            } else {
+                for (int g = 0; g < x.nr; g += 32) {
+                    int v[32];
+                    tmem_ld32(dt + g, v);
+                    store_run<OUT>(p, x, v, g, r, rw);
                 }
             }
             tc_fence_before();
@@ -266,21 +320,27 @@ __global__ void __launch_bounds__(THREADS, 1) i8_gemm_kernel(const __grid_consta
 // ------------------------------------------------------------------ CTA pairs --------------
 // Tiles of 256 weight rows x up to 256 rows on a pair of CTAs (cta_group::2): each CTA fetches its own 128 weight rows
 // and half of the tile's rows, the tensor cores read both halves.  Two accumulators of 256 columns per CTA.
+//
+// Split k (SPLIT): the C pairs of a cluster share a tile's k-blocks.  Columns go in runs of 32, run g to pair g % C: every
+// CTA sends its sums of the others' runs to the CTA there that has the same weight rows, adds what comes in for its
+// own, and stores those.  The ring takes them in: nothing else uses it any more when a CTA says that it may be written to.
 constexpr int P_THREADS = (W_EPI0 + P_EPI) * 32;
 constexpr int P_OUT = 8192;              // bytes of an epilogue half's staging buffer
+constexpr int RUN_BYTES = 128 * 32 * 4;  // a run's sums of a CTA's weight rows
 
 struct PairPlan {
     static constexpr int B_BYTES = P_NT / 2 * KB;
     static constexpr int STAGE = A_BYTES + B_BYTES;
     static constexpr int S = (216 * 1024 - 2 * P_OUT) / STAGE;
     static constexpr size_t SMEM = static_cast<size_t>(S) * STAGE + 2 * P_OUT + 1024;
+    static_assert((MAX_SPLIT - 1) * (P_NT / 32 / MAX_SPLIT) * RUN_BYTES <= S * STAGE && P_NT / 32 / 2 * RUN_BYTES <= S * STAGE, "a split's sums fit the ring");
 };
 
 // A run of 32 rows x this CTA's 128 weight rows through shared memory: lanes hold a weight row each, out wants weight
 // rows side by side.  `buf`: the half's P_OUT bytes; vec: 16-byte stores are aligned.
 template <int OUT>
 __device__ __forceinline__ void staged_run(const GemmArgs &p, const Tile &x, const int *v, int g, int row0, float rw, float rx,
-                                           unsigned char *buf, int half, int q, int lane, bool vec) {
+                                           unsigned char *buf, int half, int q, int lane) {
     constexpr int ITEM = OUT == COLI_ACT_F32 ? 4 : 2;
     constexpr int RUN = OUT == COLI_ACT_F32 ? 16 : 32;    // rows at a time
     constexpr int COLS = 128;
@@ -304,7 +364,7 @@ __device__ __forceinline__ void staged_run(const GemmArgs &p, const Tile &x, con
             if (row >= x.nr || c >= p.n) continue;
             unsigned char *dst = static_cast<unsigned char *>(p.out) + (static_cast<size_t>(x.n0 + row) * p.ldo + c) * ITEM;
             const uint4 w = *reinterpret_cast<const uint4 *>(buf + 16 * at);
-            if (vec && c + 16 / ITEM <= p.n) {
+            if (c + 16 / ITEM <= p.n) {
                 *reinterpret_cast<uint4 *>(dst) = w;
             } else {
                 const int n = min(16 / ITEM, p.n - c);
@@ -317,25 +377,28 @@ __device__ __forceinline__ void staged_run(const GemmArgs &p, const Tile &x, con
     }
 }
 
-template <int OUT>
-__global__ void __launch_bounds__(P_THREADS, 1) i8_pair_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs p) {  // clusters of 2
+template <int OUT, bool SPLIT>
+__global__ void __launch_bounds__(P_THREADS, 1) i8_pair_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs p) {  // clusters of 2 C CTAs
     using P = PairPlan;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    // the same offset in both CTAs: the dynamic array starts at the same address in each
+    // the same offset in all CTAs of the cluster: the dynamic array starts at the same address in each
     unsigned char *sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     unsigned char *sa = sm, *sb = sa + P::S * A_BYTES, *sout = sb + P::S * P::B_BYTES;
-    __shared__ __align__(8) uint64_t bars[2 * P::S + 5];
+    __shared__ __align__(8) uint64_t bars[2 * P::S + 7];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_tiles;
     __shared__ TileList list;
     __shared__ int s_scan[P_THREADS / 32];
     // full: the leader's, of both CTAs' copies; empty, dfull: in each CTA; dempty: the leader's
     uint64_t *full = bars, *empty = full + P::S, *dfull = empty + P::S, *dempty = dfull + 2, *drain = dempty + 2;
+    uint64_t *pready = drain + 1, *pfull = pready + 1;  // split k: the others may be written to; their sums are here
     volatile int *abort = &s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const int MB = (p.n + 255) / 256, KT = (p.k + KB - 1) / KB;
+    const int crank = static_cast<int>(cluster_rank()), rank = crank & 1, leader = crank & ~1;
+    const int C = SPLIT ? static_cast<int>(cluster_size()) >> 1 : 1, part = SPLIT ? crank >> 1 : 0;
+    const int first = blockIdx.x / (2 * C), stride = gridDim.x / (2 * C);
+    const int MB = (p.n + 255) / 256, KALL = (p.k + KB - 1) / KB;
+    const int kb0 = KALL * part / C, KT = KALL * (part + 1) / C - kb0;
     const int W = p.E;
 
     if (threadIdx.x == 0) {
@@ -348,6 +411,8 @@ __global__ void __launch_bounds__(P_THREADS, 1) i8_pair_kernel(const __grid_cons
             mbar_init(smem_u32(&dempty[i]), 2 * P_EPI);
         }
         mbar_init(smem_u32(drain), 1);
+        mbar_init(smem_u32(pready), C > 1 ? C - 1 : 1);
+        mbar_init(smem_u32(pfull), 1);
         s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -367,20 +432,26 @@ __global__ void __launch_bounds__(P_THREADS, 1) i8_pair_kernel(const __grid_cons
     tc_fence_after();
     const uint32_t tbase = s_tmem;
     const int ntiles = s_tiles;
+    // A cluster that splits k has one tile; should groups that overlap make more of them than the host counted, all its
+    // warps meet before the next one, whose copies need the ring.
+    auto next_tile = [&](int t) {
+        if (SPLIT && t != first) cluster_sync_all();
+    };
 
     if (warp == W_PROD) {
         // ------------------------------------------------------------------ TMA producer
         uint32_t s = 0, phase = 1;
-        for (int t = pair; t < ntiles; t += pairs) {
+        for (int t = first; t < ntiles; t += stride) {
+            next_tile(t);
             const Tile x = tile_at<P_NT>(t, list, p, W);
             const int n32 = (x.nr + 31) / 32;                        // N / 32; this CTA's share is 16 * n32 rows
-            const int row_lo = x.n0 + static_cast<int>(rank) * 16 * n32;
-            for (int kb = 0; kb < KT; ++kb) {
+            const int row_lo = x.n0 + rank * 16 * n32;
+            for (int kb = kb0; kb < kb0 + KT; ++kb) {
                 if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[s]), phase, abort, p.err))) goto prod_done;
-                const uint32_t fb = map_rank(smem_u32(&full[s]), 0);
+                const uint32_t fb = map_rank(smem_u32(&full[s]), leader);
                 if (elect_one()) {
                     remote_expect_tx(fb, A_BYTES + n32 * 16 * KB);
-                    pair_load_3d(smem_u32(sa + s * A_BYTES), &maps.a, kb * KB, x.m * 256 + static_cast<int>(rank) * 128, x.e, fb);
+                    pair_load_3d(smem_u32(sa + s * A_BYTES), &maps.a, kb * KB, x.m * 256 + rank * 128, x.e, fb);
 #pragma unroll
                     for (int bit = NBOX - 1; bit >= 0; --bit) {
                         const int row0 = 16 * ((n32 >> (bit + 1)) << (bit + 1));
@@ -402,7 +473,9 @@ __global__ void __launch_bounds__(P_THREADS, 1) i8_pair_kernel(const __grid_cons
         // ------------------------------------------------------------------ MMA issuer (the pair's)
         uint32_t s = 0, phase = 0, tl = 0;
         const uint64_t adesc0 = smem_desc_sw128(smem_u32(sa)), bdesc0 = smem_desc_sw128(smem_u32(sb));
-        for (int t = pair; t < ntiles; t += pairs, ++tl) {
+        const uint16_t both = static_cast<uint16_t>(3 << leader);
+        for (int t = first; t < ntiles; t += stride, ++tl) {
+            next_tile(t);
             const Tile x = tile_at<P_NT>(t, list, p, W);
             const int n32 = (x.nr + 31) / 32, acc = tl & 1;
             const uint32_t idesc = idesc_i8(256) | (static_cast<uint32_t>(4 * n32) << 17);
@@ -412,13 +485,13 @@ __global__ void __launch_bounds__(P_THREADS, 1) i8_pair_kernel(const __grid_cons
             for (int kb = 0; kb < KT; ++kb) {
                 if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&full[s]), phase, abort, p.err))) goto mma_done;
                 tc_fence_after();
-                const int steps = min(4, (p.k - kb * KB + 31) / 32);
+                const int steps = min(4, (p.k - (kb0 + kb) * KB + 31) / 32);
                 if (elect_one()) {
                     const uint64_t ad = adesc0 + static_cast<uint64_t>(s * (A_BYTES >> 4)), bd = bdesc0 + static_cast<uint64_t>(s * (P::B_BYTES >> 4));
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         if (kk < steps) mma_i8<2>(dt, ad + 2 * kk, bd + 2 * kk, idesc, (kb | kk) != 0);
-                    pair_commit(smem_u32(&empty[s]));
+                    pair_commit(smem_u32(&empty[s]), both);
                 }
                 __syncwarp();
                 if (++s == P::S) {
@@ -426,7 +499,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) i8_pair_kernel(const __grid_cons
                     phase ^= 1;
                 }
             }
-            if (elect_one()) pair_commit(smem_u32(&dfull[acc]));
+            if (elect_one()) pair_commit(smem_u32(&dfull[acc]), both);
             __syncwarp();
         }
     mma_done:
@@ -443,32 +516,77 @@ __global__ void __launch_bounds__(P_THREADS, 1) i8_pair_kernel(const __grid_cons
                 }
             }
         }
-    } else if (warp >= W_EPI0) {
+    } else if (warp == W_MMA) {
+        if (SPLIT)
+            for (int t = first; t < ntiles; t += stride) next_tile(t);
+    } else {
         // ------------------------------------------------------------------ epilogue
-        const int q = warp & 3, half = (warp - W_EPI0) >> 2;  // TMEM lane quarter, 128-column half
+        const int q = warp & 3, half = (warp - W_EPI0) >> 2;  // TMEM lane quarter; every other of this CTA's runs
         unsigned char *obuf = sout + half * P_OUT;
         constexpr int ITEM = OUT == COLI_ACT_F32 ? 4 : 2;
         const bool vec = ((reinterpret_cast<uintptr_t>(p.out) | (p.ldo * ITEM)) & 15) == 0;
         uint32_t tl = 0;
-        for (int t = pair; t < ntiles; t += pairs, ++tl) {
+        for (int t = first; t < ntiles; t += stride, ++tl) {
+            next_tile(t);
             const Tile x = tile_at<P_NT>(t, list, p, W);
-            const int acc = tl & 1, row0 = x.m * 256 + static_cast<int>(rank) * 128;
-            const int r = row0 + 32 * q + lane;
+            const int acc = tl & 1, row0 = x.m * 256 + rank * 128;
+            const int r = row0 + 32 * q + lane, runs = (x.nr + 31) / 32;
             const float rw = p.wscale && r < p.n ? __ldg(p.wscale + static_cast<size_t>(x.e) * p.wscale_stride + r) : 1.f;
             // (all eight warps meet in the staging barriers: they give up together, or not at all)
             if (epi_or(!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&dfull[acc]), (tl >> 1) & 1, abort, p.err)))) break;
             tc_fence_after();
             const uint32_t dt = tbase + acc * P_NT + (static_cast<uint32_t>(32 * q) << 16);
-            for (int g = 128 * half; g < min(x.nr, 128 * half + 128); g += 32) {
-                float rx = p.xscale && g + lane < x.nr ? __ldg(p.xscale + x.n0 + g + lane) : 1.f, rwg = rw;
+            const int own = runs > part ? (runs - part + C - 1) / C : 0;  // this CTA's runs
+            if (SPLIT) {
+                if (warp == W_EPI0) {
+                    // nothing reads or writes this CTA's ring any more: the products have been made, the copies came before them
+                    if (lane == 0) mbar_expect_tx(smem_u32(pfull), (C - 1) * own * RUN_BYTES);
+                    __syncwarp();
+                    if (lane < C && lane != part) remote_arrive(map_rank(smem_u32(pready), 2 * lane + rank));
+                    __syncwarp();
+                }
+                if (epi_or(!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(pready), tl & 1, abort, p.err)))) break;
+                for (int g = half; g < runs; g += 2) {
+                    const int to = g % C;
+                    if (to == part) continue;
+                    int v[32];
+                    tmem_ld32(dt + 32 * g, v);
+                    const int slot = (part < to ? part : part - 1) * ((runs - to + C - 1) / C) + g / C;
+                    const uint32_t dst = map_rank(smem_u32(sm) + slot * RUN_BYTES + (32 * q + lane) * 128, 2 * to + rank), bar = map_rank(smem_u32(pfull), 2 * to + rank);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];"
+                                     ::"r"(dst + ((i ^ (lane & 7)) << 4)), "r"(v[4 * i]), "r"(v[4 * i + 1]), "r"(v[4 * i + 2]), "r"(v[4 * i + 3]), "r"(bar) : "memory");
+                }
+                if (epi_or(!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(pfull), tl & 1, abort, p.err)))) break;
+            }
+            for (int i = half; i < own; i += 2) {
+                const int g = 32 * (part + i * C);
                 int v[32];
                 tmem_ld32(dt + g, v);
+                if (SPLIT)
+                    for (int c = 0; c < C - 1; ++c) {
+                        const int4 *from = reinterpret_cast<const int4 *>(sm + (c * own + i) * RUN_BYTES + (32 * q + lane) * 128);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int4 f = from[j ^ (lane & 7)];
+                            v[4 * j] += f.x;
+                            v[4 * j + 1] += f.y;
+                            v[4 * j + 2] += f.z;
+                            v[4 * j + 3] += f.w;
+                        }
+                    }
+                if (!vec) {
+                    store_run<OUT>(p, x, v, g, r, rw);
+                    continue;
+                }
+                float rx = p.xscale && g + lane < x.nr ? __ldg(p.xscale + x.n0 + g + lane) : 1.f, rwg = rw;
                 run_sums(v, rwg, rx);
-                staged_run<OUT>(p, x, v, g, row0, rwg, rx, obuf, half, q, lane, vec);
+                staged_run<OUT>(p, x, v, g, row0, rwg, rx, obuf, half, q, lane);
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) remote_arrive(map_rank(smem_u32(&dempty[acc]), 0));
+            if (lane == 0) remote_arrive(map_rank(smem_u32(&dempty[acc]), leader));
         }
     }
 
@@ -504,32 +622,33 @@ bool rows_maps(CUtensorMap *m, const coli_i8_rows &a, int k) {
     return true;
 }
 
-// Groups that have rows, at most.
+// Groups that have rows, and chunks of at most nt rows of one group, at most.
 long groups_of(const GemmArgs &g) { return g.rows < g.E ? g.rows : g.E; }
+long chunks_of(const GemmArgs &g, int nt) { return (g.rows - groups_of(g)) / nt + groups_of(g); }
 
 template <int OUT>
 cudaError_t launch_gemm(const GemmMaps &maps, const GemmArgs &g, cudaStream_t st) {
-    using P = Plan<128>;
-    auto kernel = i8_gemm_kernel<128, OUT>;
+    using P = Plan<128, false>;
+    auto kernel = i8_gemm_kernel<128, OUT, false>;
     static std::atomic<uint64_t> ready{0};
     const cudaError_t e = allow_smem(kernel, P::SMEM, ready);
     if (e != cudaSuccess) return e;
-    const long tiles = (g.rows / 128 + groups_of(g)) * ((g.n + 127) / 128);
+    const long tiles = chunks_of(g, 128) * ((g.n + 127) / 128);
     const int sms = device_sm_count();
     return launch_early(kernel, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), THREADS, P::SMEM, st, 1, maps, g);
 }
 
-// At most 32 rows: tiles of 128 weight rows x all rows of a matrix, their k-blocks split over clusters of 1, 2
-// or 4 CTAs, whichever leaves the busiest CTA the least (the matrices that have rows are at most as many as rows).
-template <int OUT>
+// Tiles of 128 weight rows x at most NT rows, their k-blocks split over clusters of 1, 2 or 4 CTAs, whichever leaves the busiest
+// CTA the least.
+template <int OUT, int NT>
 cudaError_t launch_split(const GemmMaps &maps, const GemmArgs &g, cudaStream_t st) {
-    using P = Plan<32>;
-    auto kernel = i8_gemm_kernel<32, OUT>;
+    using P = Plan<NT, true>;
+    auto kernel = i8_gemm_kernel<NT, OUT, true>;
     static std::atomic<uint64_t> ready{0};
     const cudaError_t e = allow_smem(kernel, P::SMEM, ready);
     if (e != cudaSuccess) return e;
     const int sms = device_sm_count(), kt = (g.k + KB - 1) / KB;
-    const int tiles = static_cast<int>(groups_of(g)) * ((g.n + 127) / 128);
+    const int tiles = static_cast<int>(chunks_of(g, NT) * ((g.n + 127) / 128));
     int C = 1;
     long best = 0;
     for (int c = 1; c <= MAX_SPLIT && c <= kt; c *= 2) {
@@ -544,32 +663,31 @@ cudaError_t launch_split(const GemmMaps &maps, const GemmArgs &g, cudaStream_t s
     return launch_early(kernel, dim3(C * (tiles < clusters ? tiles : clusters)), THREADS, P::SMEM, st, C, maps, g);
 }
 
-template <int OUT>
-cudaError_t launch_pair(const GemmMaps &maps, const GemmArgs &g, cudaStream_t st) {
+template <int OUT, bool SPLIT>
+cudaError_t launch_pair(const GemmMaps &maps, const GemmArgs &g, int C, cudaStream_t st) {
     using P = PairPlan;
-    auto kernel = i8_pair_kernel<OUT>;
+    auto kernel = i8_pair_kernel<OUT, SPLIT>;
     static std::atomic<uint64_t> ready{0};
     const cudaError_t e = allow_smem(kernel, P::SMEM, ready);
     if (e != cudaSuccess) return e;
-    const long tiles = (g.rows / P_NT + groups_of(g)) * ((g.n + 255) / 256);
-    const int pairs = device_sm_count() / 2;
-    return launch_early(kernel, dim3(2 * static_cast<unsigned>(tiles < pairs ? tiles : pairs)), P_THREADS, P::SMEM, st, 2, maps, g);
+    const long tiles = chunks_of(g, P_NT) * ((g.n + 255) / 256), clusters = SPLIT ? tiles : device_sm_count() / 2;
+    return launch_early(kernel, dim3(2 * C * static_cast<unsigned>(tiles < clusters ? tiles : clusters)), P_THREADS, P::SMEM, st, 2 * C, maps, g);
 }
 
+constexpr int PAIR_ROWS = 32, SPLIT_KT = 20;
+
 template <int OUT>
-cudaError_t launch_out(const GemmMaps &maps, const GemmArgs &g, bool pairs, cudaStream_t st) {
-    if (pairs) return launch_pair<OUT>(maps, g, st);
-    return g.rows <= 32 ? launch_split<OUT>(maps, g, st) : launch_gemm<OUT>(maps, g, st);
+cudaError_t launch_out(const GemmMaps &maps, const GemmArgs &g, cudaStream_t st) {
+    if (g.rows <= 32) return launch_split<OUT, 32>(maps, g, st);
+    const int sms = device_sm_count(), kt = (g.k + KB - 1) / KB;
+    const long small = chunks_of(g, 128) * ((g.n + 127) / 128), tiles = chunks_of(g, P_NT) * ((g.n + 255) / 256);
+    if (kt >= SPLIT_KT && small <= cluster_count(4, sms)) return launch_split<OUT, 128>(maps, g, st);
+    if (kt >= SPLIT_KT && tiles <= cluster_count(4, sms)) return launch_pair<OUT, true>(maps, g, 2, st);
+    if (g.rows / groups_of(g) < PAIR_ROWS && small >= sms) return launch_gemm<OUT>(maps, g, st);
+    return launch_pair<OUT, false>(maps, g, 1, st);
 }
 
 }  // namespace
-
-constexpr int PAIR_ROWS = 112;
-
-static bool use_pairs(const I8ProductArgs &p) {
-    const int avg = p.a.rows / p.w.count;
-    return avg >= PAIR_ROWS || (avg > 32 && static_cast<long>(p.w.count) * ((avg + 127) / 128) * ((p.w.n + 127) / 128) < device_sm_count());
-}
 
 cudaError_t launch_i8_product(const I8ProductArgs &p, cudaStream_t st) {
     GemmMaps maps;
@@ -587,8 +705,7 @@ cudaError_t launch_i8_product(const I8ProductArgs &p, cudaStream_t st) {
     g.k = p.k;
     g.out = p.out;
     g.ldo = p.ldo;
-    const bool pairs = use_pairs(p);
-    return p.out_type == COLI_ACT_F32 ? launch_out<COLI_ACT_F32>(maps, g, pairs, st) : launch_out<COLI_ACT_BF16>(maps, g, pairs, st);
+    return p.out_type == COLI_ACT_F32 ? launch_out<COLI_ACT_F32>(maps, g, st) : launch_out<COLI_ACT_BF16>(maps, g, st);
 }
 
 }  // namespace coli

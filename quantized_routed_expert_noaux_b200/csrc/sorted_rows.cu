@@ -13,11 +13,13 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "internal.h"
 #include "pdl.h"
 #include "sorted_rows.h"
+#include "tc_ptx.h"
 
 namespace coli {
 
@@ -88,129 +90,163 @@ inline Cut cut(int n, int most) {
 
 // ------------------------------------------------------------------ sort
 
-constexpr int SMALL_N = 2048;   // slots that every CTA counts by itself
-constexpr int SMALL_T = 256;    // threads at most
+// Slots up to which every CTA counts them by itself (below 2^13): 64 experts, 8 slots to a token, 2048 bf16 columns: 3.1, 5.6
+// and 7.2 us with 512, 2048 and 2560 slots against 6.2, 6.7 and 7.2 of the two kernels (1000 experts: 8.2 to 9.7).
+constexpr int SMALL_N = 2560;
+constexpr int SMALL_T = 256;    // threads
+
+// Keys below `key` of n (padded to whole runs of 128), by a warp.
+__device__ __forceinline__ int count_below(const uint32_t *keys, int n, uint32_t key, int lane) {
+    int before = 0;
+    for (int i = lane; i < (n + 3) / 4; i += 32) {
+        const uint4 v = reinterpret_cast<const uint4 *>(keys)[i];
+        before += (v.x < key) + (v.y < key) + (v.z < key) + (v.w < key);
+    }
+    return __reduce_add_sync(FULL, before);
+}
 
 // One kernel for few slots: CTA (token, piece of its row) counts where the token's slots go and copies the piece there.
-// An id that is no expert's sorts behind all experts; its slot is not placed.
+// Slot s with id e has the key (e, s); its place is the number of lower keys.  An id that is no expert's sorts
+// behind all experts; its slot is not placed.
 template <typename Item>
 __global__ void __launch_bounds__(SMALL_T) sort_small_kernel(const SortArgs a, int items, size_t px, size_t pr) {
-    __shared__ int s_id[SMALL_N];
+    __shared__ __align__(16) uint32_t s_key[SMALL_N];
     __shared__ int s_place[32];
     wait_for_previous();
-    const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int n = a.T * a.K;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const int id = __ldg(a.ids + i);
-        s_id[i] = static_cast<unsigned>(id) < static_cast<unsigned>(a.E) ? id : a.E;
-        if (id != -1 && s_id[i] == a.E && t == 0 && blockIdx.y == 0) atomicOr(a.err, COLI_DEVERR_EXPERT_ID);
+    const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int WARPS = SMALL_T / 32;
+    const int n = a.T * a.K, i0 = blockIdx.y * SMALL_T + threadIdx.x;
+    const Item *x = static_cast<const Item *>(a.x) + t * px;
+    Item v;
+    if (a.x && i0 < items) v = __ldg(x + i0);  // on its way while the slots are counted
+    for (int s = threadIdx.x; s < (n + 3 & ~3); s += SMALL_T) {
+        uint32_t key = 0xffffffffu;
+        if (s < n) {
+            const int id = __ldg(a.ids + s);
+            const bool ok = static_cast<unsigned>(id) < static_cast<unsigned>(a.E);
+            if (!ok && id != -1 && t == 0 && blockIdx.y == 0) atomicOr(a.err, COLI_DEVERR_EXPERT_ID);
+            key = static_cast<uint32_t>(ok ? id : a.E) << 13 | s;
+        }
+        s_key[s] = key;
     }
     __syncthreads();
-    for (int k = warp; k < a.K; k += warps) {
-        const int s = t * a.K + k, id = s_id[s];
-        int before = 0;
-        for (int i = lane; i < n; i += 32) before += s_id[i] < id || (s_id[i] == id && i < s);
-        before = __reduce_add_sync(FULL, before);
+    for (int k = warp; k < a.K; k += WARPS) {
+        const int s = t * a.K + k;
+        const uint32_t key = s_key[s];
+        const int before = count_below(s_key, n, key, lane);
         if (lane == 0) {
-            const int to = id < a.E ? before : -1;
-            s_place[k] = to;
+            const bool ok = static_cast<int>(key >> 13) < a.E;
+            s_place[k] = ok ? before : -1;
             if (blockIdx.y == 0) {
-                a.place[s] = to;
-                a.perm[before] = id < a.E ? s : -1;
+                a.place[s] = ok ? before : -1;
+                a.perm[before] = ok ? s : -1;
             }
         }
     }
     if (blockIdx.y == 0) {
         if (n <= 64) {
-            for (int e = t * blockDim.x + threadIdx.x; e <= a.E; e += a.T * blockDim.x) {
+            for (int e = t * SMALL_T + threadIdx.x; e <= a.E; e += a.T * SMALL_T) {
                 int before = 0;
-                for (int i = 0; i < n; ++i) before += s_id[i] < e;
+                for (int s = 0; s < n; ++s) before += s_key[s] < static_cast<uint32_t>(e) << 13;
                 a.offsets[e] = before;
             }
         } else {
-            for (int e = t * warps + warp; e <= a.E; e += a.T * warps) {
-                int before = 0;
-                for (int i = lane; i < n; i += 32) before += s_id[i] < e;
-                before = __reduce_add_sync(FULL, before);
+            for (int e = t * WARPS + warp; e <= a.E; e += a.T * WARPS) {
+                const int before = count_below(s_key, n, static_cast<uint32_t>(e) << 13, lane);
                 if (lane == 0) a.offsets[e] = before;
             }
         }
     }
     if (!a.x) return;
     __syncthreads();
-    const int i = blockIdx.y * blockDim.x + threadIdx.x;
-    if (i >= items) return;
-    const Item v = __ldg(static_cast<const Item *>(a.x) + t * px + i);
-    for (int k = 0; k < a.K; ++k) {
-        const int to = s_place[k];
-        if (to >= 0) static_cast<Item *>(a.rows)[to * pr + i] = v;
+    for (int i = i0; i < items; i += gridDim.y * SMALL_T) {
+        if (i != i0) v = __ldg(x + i);
+        for (int k = 0; k < a.K; ++k) {
+            const int to = s_place[k];
+            if (to >= 0) static_cast<Item *>(a.rows)[to * pr + i] = v;
+        }
     }
 }
 
 // Many slots: a cluster of SORT_CTAS CTAs sorts them (a share of the slots each, a warp its part of that, in order), then
 // a second kernel copies the rows.  Pass 1 counts by warp and expert; the scans over warps, CTAs (through each
 // other's shared memory) and experts turn the counts into first positions; pass 2 places the slots.
-constexpr int SORT_CTAS = 8, SORT_WARPS = 32;
+constexpr int SORT_CTAS = 8, SORT_WARPS = 16, SORT_T = SORT_WARPS * 32;
+constexpr int SORT_HOLD = 8;    // runs of 32 slots whose ids a warp keeps between the passes
 
-__device__ __forceinline__ const int *peer(const int *p, int rank) {
-    uint64_t r;
-    asm("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
-    return reinterpret_cast<const int *>(r);
+// A word into the shared memory of CTA `rank` of the cluster, where this CTA has `p`.
+__device__ __forceinline__ void put_peer(int *p, int rank, int v) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(r), "r"(v) : "memory");
 }
-__device__ __forceinline__ void cluster_sync_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-__global__ void __launch_bounds__(SORT_WARPS * 32) sort_cluster_kernel(const SortArgs a) {  // one cluster of SORT_CTAS
+__global__ void __launch_bounds__(SORT_T) sort_cluster_kernel(const SortArgs a) {  // one cluster of SORT_CTAS
     extern __shared__ int sm[];
     const int B = a.E + 1;              // the last for ids that are no expert's
     int *wc = sm;                       // [SORT_WARPS][B]: counts, then cursors
-    int *tot = sm + SORT_WARPS * B;     // [B]: this CTA's counts
+    int *tot = sm + SORT_WARPS * B;     // [SORT_CTAS][B]: every CTA's counts
     __shared__ int s_scan[SORT_WARPS];
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // this CTA has begun: its shared memory may be written to
     wait_for_previous();
+    dependents_may_launch();            // the copies fetch their rows meanwhile
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x;
     const long n = static_cast<long>(a.T) * a.K;
     const int part = rank * SORT_WARPS + warp, parts = SORT_CTAS * SORT_WARPS;
     const int lo = static_cast<int>(n * part / parts), hi = static_cast<int>(n * (part + 1) / parts);
-    for (int i = tid; i < SORT_WARPS * B; i += SORT_WARPS * 32) wc[i] = 0;
-    __syncthreads();
     const unsigned lt = (1u << lane) - 1u;
     int *mine = wc + warp * B;
     bool bad = false;
-    auto bucket = [&](int s) {          // lanes behind the end: a value of their own
-        if (s >= hi) return -1 - lane;
-        const int id = __ldg(a.ids + s);
-        const bool ok = static_cast<unsigned>(id) < static_cast<unsigned>(a.E);
-        bad = bad || (!ok && id != -1);
-        return ok ? id : a.E;
+    // the buckets of a batch of runs of 32 slots: -1 behind the end
+    int held[SORT_HOLD];
+    auto fetch = [&](int base) {
+#pragma unroll
+        for (int h = 0; h < SORT_HOLD; ++h) {
+            const int s = base + 32 * h + lane;
+            held[h] = s < hi ? __ldg(a.ids + s) : -2;
+        }
+#pragma unroll
+        for (int h = 0; h < SORT_HOLD; ++h) {
+            const bool ok = static_cast<unsigned>(held[h]) < static_cast<unsigned>(a.E), in = base + 32 * h + lane < hi;
+            bad = bad || (in && !ok && held[h] != -1);
+            held[h] = ok ? held[h] : in ? a.E : -1;
+        }
     };
-    for (int base = lo; base < hi; base += 32) {
-        const int id = bucket(base + lane);
-        const unsigned peers = __match_any_sync(FULL, id);
-        if (id >= 0 && (peers & lt) == 0) mine[id] += __popc(peers);
-        __syncwarp();
+    constexpr int BATCH = 32 * SORT_HOLD;
+    fetch(lo);
+    for (int i = tid; i < SORT_WARPS * B; i += SORT_T) wc[i] = 0;
+    __syncthreads();
+    for (int base = lo; base < hi; base += BATCH) {
+        if (base != lo) fetch(base);
+#pragma unroll
+        for (int h = 0; h < SORT_HOLD; ++h)
+            if (held[h] >= 0) atomicAdd(mine + held[h], 1);
     }
     if (bad) atomicOr(a.err, COLI_DEVERR_EXPERT_ID);
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     __syncthreads();
-    for (int e = tid; e < B; e += SORT_WARPS * 32) {
-        int run = 0;
+    for (int e = tid; e < B; e += SORT_T) {
+        int c[SORT_WARPS], run = 0;
+#pragma unroll
+        for (int w = 0; w < SORT_WARPS; ++w) c[w] = wc[w * B + e];
+#pragma unroll
         for (int w = 0; w < SORT_WARPS; ++w) {
-            const int c = wc[w * B + e];
             wc[w * B + e] = run;
-            run += c;
+            run += c[w];
         }
-        tot[e] = run;
+#pragma unroll
+        for (int c = 0; c < SORT_CTAS; ++c) put_peer(tot + rank * B + e, c, run);
     }
-    cluster_sync_all();
-    // bucket e of thread e (and 1024): what lower CTAs hold of it, and all CTAs; then the scan over the buckets
+    // (nobody touches another CTA's memory behind this barrier: each may leave when it is done)
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    // a bucket per thread: what lower CTAs hold of it, and all CTAs; then the scan over the buckets
     int carry = 0;
-    for (int base = 0; base < B; base += SORT_WARPS * 32) {
+    for (int base = 0; base < B; base += SORT_T) {
         const int e = base + tid;
         int below = 0, all = 0;
         if (e < B) {
 #pragma unroll
             for (int c = 0; c < SORT_CTAS; ++c) {
-                const int v = *peer(tot + e, c);
+                const int v = tot[c * B + e];
                 below += c < rank ? v : 0;
                 all += v;
             }
@@ -224,6 +260,7 @@ __global__ void __launch_bounds__(SORT_WARPS * 32) sort_cluster_kernel(const Sor
         if (lane == 31) s_scan[warp] = inc;
         __syncthreads();
         int before = carry;
+#pragma unroll
         for (int w = 0; w < SORT_WARPS; ++w) {
             const int v = s_scan[w];
             before += w < warp ? v : 0;
@@ -232,37 +269,111 @@ __global__ void __launch_bounds__(SORT_WARPS * 32) sort_cluster_kernel(const Sor
         const int first = before + inc - all;
         if (e < B) {
             if (rank == 0) a.offsets[e] = first;
-            for (int w = 0; w < SORT_WARPS; ++w) wc[w * B + e] += first + below;
+            int c[SORT_WARPS];
+#pragma unroll
+            for (int w = 0; w < SORT_WARPS; ++w) c[w] = wc[w * B + e];
+#pragma unroll
+            for (int w = 0; w < SORT_WARPS; ++w) wc[w * B + e] = c[w] + first + below;
         }
         __syncthreads();
     }
-    for (int base = lo; base < hi; base += 32) {
-        const int s = base + lane, id = bucket(s);
-        const unsigned peers = __match_any_sync(FULL, id);
-        if (id >= 0) {
-            const int to = mine[id] + __popc(peers & lt);
-            a.place[s] = id < a.E ? to : -1;
-            a.perm[to] = id < a.E ? s : -1;
+    for (int base = lo; base < hi; base += BATCH) {
+        if (hi - lo > BATCH) fetch(base);
+        unsigned peers[SORT_HOLD];  // the run's slots of the same bucket, from a ballot per bit of the bucket
+#pragma unroll
+        for (int h = 0; h < SORT_HOLD; ++h) peers[h] = FULL;
+        for (int bit = 1; bit <= a.E; bit <<= 1) {
+#pragma unroll
+            for (int h = 0; h < SORT_HOLD; ++h) {
+                const bool one = held[h] & bit;
+                const unsigned ones = __ballot_sync(FULL, one);
+                peers[h] &= one ? ones : ~ones;
+            }
         }
-        __syncwarp();
-        if (id >= 0 && (peers & lt) == 0) mine[id] += __popc(peers);
-        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < SORT_HOLD; ++h) {
+            if (base + 32 * h >= hi) break;
+            const int s = base + 32 * h + lane, id = held[h];
+            const int first = id >= 0 ? mine[id] : 0, to = first + __popc(peers[h] & lt);
+            __syncwarp();
+            if (id >= 0) {
+                if ((peers[h] & lt) == 0) mine[id] = first + __popc(peers[h]);
+                a.place[s] = id < a.E ? to : -1;
+                a.perm[to] = id < a.E ? s : -1;
+            }
+            __syncwarp();
+        }
     }
-    cluster_sync_all();  // no CTA leaves while another reads its counts
 }
 
-// Row t of x to the places of its K slots, a piece of the row per CTA.
+// Row t of x to the places of its K slots, a piece of the row per CTA.  The piece is fetched before the sort has ended:
+// x is older than the sort, which began when the kernels before it had ended.
 template <typename Item>
 __global__ void __launch_bounds__(256) sort_copy_kernel(const SortArgs a, int items, size_t px, size_t pr) {
+    const int t = blockIdx.x, i = blockIdx.y * blockDim.x + threadIdx.x, lane = threadIdx.x & 31;
+    Item v;
+    if (i < items) v = __ldg(static_cast<const Item *>(a.x) + t * px + i);
     wait_for_previous();
-    const int t = blockIdx.x, i = blockIdx.y * blockDim.x + threadIdx.x;
-    if (i >= items) return;
-    const Item v = __ldg(static_cast<const Item *>(a.x) + t * px + i);
-    const int32_t *place = a.place + static_cast<size_t>(t) * a.K;
+    const int at = lane < a.K ? __ldcg(a.place + static_cast<size_t>(t) * a.K + lane) : -1;
     for (int k = 0; k < a.K; ++k) {
-        const int to = place[k];
-        if (to >= 0) static_cast<Item *>(a.rows)[to * pr + i] = v;
+        const int to = __shfl_sync(FULL, at, k);
+        if (to >= 0 && i < items) static_cast<Item *>(a.rows)[to * pr + i] = v;
     }
+}
+
+// The same by bulk copies through shared memory, a warp per CTA: pieces of rows come into a ring of BULK_SLOTS, lane k sends
+// one on to the place of its token's slot k.  For long rows, where what is written is no more than BULK_ALL: 2048 tokens, 8 slots
+// each, 2048 / 6144 / 8192 bf16 columns 17.7 / 40.5 / 53 us against 19.4 / 44 / 58 by sort_copy_kernel, 1024 columns the same;
+// 16,384 tokens of 4096 234 against 219.
+constexpr int BULK_SLOTS = 4, BULK_PIECE = 16384, BULK_MIN = 4096;
+constexpr long BULK_ALL = 288L << 20;
+
+__global__ void __launch_bounds__(32) sort_bulk_kernel(const SortArgs a, int bytes, int pieces, size_t px, size_t pr) {
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ __align__(8) uint64_t bars[BULK_SLOTS];
+    __shared__ int s_abort;
+    const int lane = threadIdx.x;
+    volatile int *abort = &s_abort;
+    if (lane == 0) {
+        for (int i = 0; i < BULK_SLOTS; ++i) mbar_init(smem_u32(&bars[i]), 1);
+        s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
+    const int all = a.T * pieces, mine = blockIdx.x < all ? (all - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1 : 0;
+    auto load = [&](int i) {  // item i of this CTA into its slot of the ring
+        const int w = blockIdx.x + i * gridDim.x, t = w / pieces, piece = w - t * pieces;
+        const uint32_t bar = smem_u32(&bars[i % BULK_SLOTS]);
+        if (elect_one()) {
+            mbar_expect_tx(bar, bytes);
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                         ::"r"(smem_u32(ring + static_cast<size_t>(i % BULK_SLOTS) * bytes)), "l"(static_cast<const unsigned char *>(a.x) + t * px + static_cast<size_t>(piece) * bytes),
+                           "r"(bytes), "r"(bar) : "memory");
+        }
+        __syncwarp();
+    };
+    for (int i = 0; i < BULK_SLOTS && i < mine; ++i) load(i);
+    wait_for_previous();
+    auto place = [&](int i) {
+        const int t = (blockIdx.x + i * gridDim.x) / pieces;
+        return i < mine && lane < a.K ? __ldcg(a.place + static_cast<size_t>(t) * a.K + lane) : -1;
+    };
+    int next = place(0), i = 0;
+    for (; i < mine; ++i) {
+        const int at = next, w = blockIdx.x + i * gridDim.x, piece = w - w / pieces * pieces;
+        next = place(i + 1);
+        if (!__all_sync(FULL, mbar_wait(smem_u32(&bars[i % BULK_SLOTS]), (i / BULK_SLOTS) & 1, abort, a.err))) break;
+        if (at >= 0)
+            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+                         ::"l"(static_cast<unsigned char *>(a.rows) + at * pr + static_cast<size_t>(piece) * bytes), "r"(smem_u32(ring + static_cast<size_t>(i % BULK_SLOTS) * bytes)), "r"(bytes) : "memory");
+        asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 1;" ::: "memory");
+        __syncwarp();
+        // the copies out of the slot before have read it: the next item may come there
+        if (i > 0 && i - 1 + BULK_SLOTS < mine) load(i - 1 + BULK_SLOTS);
+    }
+    if (i < mine)  // given up: what was asked for lands before the ring is released
+        for (int j = i; j < mine && j < i - 1 + BULK_SLOTS; ++j) mbar_drain(smem_u32(&bars[j % BULK_SLOTS]), (j / BULK_SLOTS) & 1);
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 template <typename Item>
@@ -272,20 +383,30 @@ cudaError_t sort_rows(const SortArgs &a, int item, cudaStream_t st) {
     const Cut c = cut(items, SMALL_T);
     const int n = a.T * a.K;
     if (n <= SMALL_N) {
-        // (eight warps count, whatever the row's length)
-        return launch_early(sort_small_kernel<Item>, dim3(a.T, a.x ? (items + SMALL_T - 1) / SMALL_T : 1), SMALL_T, 0, st, 1, a, items, px, pr);
+        const int pieces = a.T < device_sm_count() ? (items + SMALL_T - 1) / SMALL_T : 1;
+        return launch_early(sort_small_kernel<Item>, dim3(a.T, pieces), SMALL_T, 0, st, 1, a, items, px, pr);
     }
-    const size_t smem = static_cast<size_t>(SORT_WARPS + 1) * (a.E + 1) * sizeof(int);
+    const size_t smem = static_cast<size_t>(SORT_WARPS + SORT_CTAS) * (a.E + 1) * sizeof(int);
     static std::atomic<uint64_t> ready{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-        const int most = (SORT_WARPS + 1) * 1025 * static_cast<int>(sizeof(int));
-        if ((e = cudaFuncSetAttribute(sort_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) != cudaSuccess) return e;
+        const int bytes = (SORT_WARPS + SORT_CTAS) * (1024 + 1) * static_cast<int>(sizeof(int));
+        if ((e = cudaFuncSetAttribute(sort_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+        if ((e = cudaFuncSetAttribute(sort_bulk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BULK_SLOTS * BULK_PIECE)) != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    if ((e = launch_early(sort_cluster_kernel, dim3(SORT_CTAS), SORT_WARPS * 32, smem, st, SORT_CTAS, a)) != cudaSuccess || !a.x) return e;
+    if ((e = launch_early(sort_cluster_kernel, dim3(SORT_CTAS), SORT_T, smem, st, SORT_CTAS, a)) != cudaSuccess || !a.x) return e;
+    const int row = a.hidden * item;
+    if (sizeof(Item) == 16 && row >= BULK_MIN && static_cast<long>(n) * row <= BULK_ALL) {
+        int pieces = (row + BULK_PIECE - 1) / BULK_PIECE;
+        while (row % (16 * pieces)) ++pieces;  // equal pieces of whole 16 bytes (row / 16 of them at most)
+        const int bytes = row / pieces;
+        const long ring = static_cast<long>(BULK_SLOTS) * bytes, most = device_sm_count() * std::min(200 * 1024 / ring, 16L);
+        return launch_early(sort_bulk_kernel, dim3(static_cast<unsigned>(std::min(static_cast<long>(a.T) * pieces, most))), 32, ring, st, 1, a, bytes, pieces,
+                            a.ldx * item, a.ldr * item);
+    }
     return launch_early(sort_copy_kernel<Item>, dim3(a.T, c.pieces), c.threads, 0, st, 1, a, items, px, pr);
 }
 
@@ -294,6 +415,7 @@ cudaError_t sort_rows(const SortArgs &a, int item, cudaStream_t st) {
 constexpr int CT = 256;         // threads at most
 constexpr int DEPTH = 8;        // rows of a token in flight
 constexpr int CTAS = 4;         // resident per SM
+constexpr int GT = CT * CTAS;   // threads of a token at most, where tokens are few (gradient)
 
 // Rows place[k0 .. k0 + DEPTH) of a token and their weights, one per lane; -1 where there is none.
 struct Slots {
@@ -368,8 +490,8 @@ __global__ void __launch_bounds__(CT, CTAS) combine_kernel(const CombineArgs a, 
 
 // A CTA takes tokens one after another, DEPTH of their rows at a time; the products with dout are summed over the CTA.
 template <typename Act, typename Out, int V>
-__global__ void __launch_bounds__(CT, CTAS) combine_grad_kernel(const CombineGradArgs a) {
-    __shared__ float s_sum[2][CT / 32][DEPTH];
+__global__ void __launch_bounds__(GT, 1) combine_grad_kernel(const CombineGradArgs a) {
+    __shared__ float s_sum[2][GT / 32][DEPTH];
     wait_for_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     int buf = 0;
@@ -461,9 +583,10 @@ cudaError_t combine(const CombineArgs &a, cudaStream_t st) {
 template <typename Act, typename Out>
 cudaError_t combine_grad(const CombineGradArgs &a, cudaStream_t st) {
     constexpr int V = 16 / sizeof(Act);
+    const int most = a.T <= device_sm_count() ? GT : CT;
     if (a.hidden % V == 0 && whole(a.y, a.ldy, sizeof(Act), V) && whole(a.dout, a.ld_dout, sizeof(Out), V) && whole(a.dy, a.ld_dy, sizeof(Act), V))
-        return launch_early(combine_grad_kernel<Act, Out, V>, dim3(resident(a.T)), cut(a.hidden / V, CT).threads, 0, st, 1, a);
-    return launch_early(combine_grad_kernel<Act, Out, 1>, dim3(resident(a.T)), cut(a.hidden, CT).threads, 0, st, 1, a);
+        return launch_early(combine_grad_kernel<Act, Out, V>, dim3(resident(a.T)), cut(a.hidden / V, most).threads, 0, st, 1, a);
+    return launch_early(combine_grad_kernel<Act, Out, 1>, dim3(resident(a.T)), cut(a.hidden, most).threads, 0, st, 1, a);
 }
 
 }  // namespace

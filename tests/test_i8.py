@@ -441,11 +441,12 @@ def test_product_scales_out_of_the_usual_range(counts):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("scale", [1, 12])
-@pytest.mark.parametrize("bad", [[0, 5, 3, 28], [0, 5, 25, 1000], [-1, 5, 25, 28], [25, 5, 20, 28], [30, 31, 32, 33], [3, 3, 3, 2]])
-def test_product_bad_offsets(scale, bad):
-    """A group is left out where its own bounds are not ascending within the rows; every other one is multiplied."""
-    p = Product([5 * scale, 20 * scale, 3 * scale], 72, 96, None, tail=9 * scale)
+@pytest.mark.parametrize("scale,k", [(1, 96), (12, 96), (12, 2100), (30, 2100)])
+@pytest.mark.parametrize("bad", [[0, 5, 3, 28], [0, 5, 25, 1000], [-1, 5, 25, 28], [25, 5, 20, 28], [30, 31, 32, 33], [3, 3, 3, 2], [0, 37, 0, 37]])
+def test_product_bad_offsets(scale, k, bad):
+    """A group is left out where its own bounds are not ascending within the rows; every other one is multiplied, also
+    where groups overlap and make more tiles than their rows would."""
+    p = Product([5 * scale, 20 * scale, 3 * scale], 72, k, None, tail=9 * scale)
     y = [p.a.astype(np.float64) @ w.astype(np.float64).T for w in p.w]
     off = [v * scale if v < 1000 else v * 1000 for v in bad]
     out = torch.full((p.rows, 72), -7.25, device="cuda")
@@ -477,6 +478,13 @@ def test_product_far_apart(rows):
     q.coli_moe_i8_product(q.i8_rows_for(p.d_a), q.i8_mats_for(w), k, p.d_off, 1, out, ld, W)
     got, v = out[:, :n].double().cpu().numpy(), p.want()
     assert q.coli_moe_error_word(W) == 0 and (np.abs(got - v) <= 2.0 ** -8 * 1.01 * np.abs(v)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("counts,n,k", [([1], 12288, 2000), ([9], 12200, 2100), ([20], 12288, 2300), ([2, 1, 0, 5, 1, 1, 1, 3], 4096, 1500)])
+def test_product_several_tiles_to_a_split(counts, n, k):
+    """Few rows, more tiles than there are clusters that split k: every cluster takes several."""
+    Product(counts, n, k, "random", tail=1).check()
 
 
 @pytest.mark.gpu
