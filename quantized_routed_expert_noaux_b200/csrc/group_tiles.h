@@ -3,11 +3,11 @@
 // family; all names stay local to it.
 #pragma once
 
-#include <atomic>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "coli_moe.h"
+#include "pdl.h"
 #include "tc_ptx.h"
 
 namespace coli {
@@ -260,18 +260,6 @@ __device__ __forceinline__ void pair_commit(uint32_t mbar, uint16_t both = 3) {
 // Clusters of c CTAs, one CTA per SM, that run at once: with c = 4 some SMs of a GPC are left over (33
 // clusters on B200's 148 SMs, by cudaOccupancyMaxActiveClusters).
 int cluster_count(int c, int sms) { return c <= 2 ? sms / c : (sms - 16) / 4; }
-
-// The kernel's shared-memory attribute lasts as long as the context: set once per device (twice is
-// harmless).
-template <typename K>
-cudaError_t allow_smem(K *kernel, size_t bytes, std::atomic<uint64_t> &ready) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || (dev < 64 && (ready.load(std::memory_order_relaxed) >> dev & 1))) return e;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-    if (e == cudaSuccess && dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
-    return e;
-}
 
 }  // namespace
 }  // namespace coli

@@ -18,6 +18,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "group_tiles.h"
 #include "i8.h"
 #include "internal.h"
@@ -31,15 +33,16 @@ constexpr int KB = 128;                  // elements (bytes) of a k-block's row
 constexpr int A_BYTES = 128 * KB;        // weight codes of a k-block
 constexpr int W_PROD = 0, W_MMA = 1, W_EPI0 = 2, N_EPI = 4;
 constexpr int THREADS = (W_EPI0 + N_EPI) * 32;
+constexpr int STAGED = 2048, WARP_BUF = STAGED + 128;  // an epilogue warp's shared memory: values on their way out, scales
 
 template <int NT, bool SPLIT>
 struct Plan {
     static constexpr int B_BYTES = NT * KB;
     static constexpr int STAGE = A_BYTES + B_BYTES;
     static constexpr int PART = SPLIT ? (MAX_SPLIT - 1) * NT / MAX_SPLIT * 128 * 4 : 0;  // split k: the other CTAs' sums (most with MAX_SPLIT of them)
-    static constexpr int S = (216 * 1024 - PART) / STAGE;                       // ring stages
+    static constexpr int S = (216 * 1024 - PART - N_EPI * WARP_BUF) / STAGE;    // ring stages
     static constexpr int ACC = NT <= 32 ? 32 : 128;                             // columns of an accumulator
-    static constexpr size_t SMEM = static_cast<size_t>(S) * STAGE + PART + 1024;
+    static constexpr size_t SMEM = static_cast<size_t>(S) * STAGE + PART + N_EPI * WARP_BUF + 1024;
 };
 
 // Instruction descriptor of kind::i8: D s32 (bits 4-5 = 2), A and B signed 8-bit (bits 7-9, 10-12 = 1),
@@ -86,22 +89,78 @@ __device__ __forceinline__ void run_sums(int (&v)[N], float &rw, float &rx) {
         split_scales(v, pw, rx);
     }
 }
-// Rows g .. of a tile x weight row r of this lane, from the lanes: out wants weight rows side by side.
+// Rows g .. g + N - 1 of a tile x this warp's 32 weight rows (from r0 on, one per lane).  out wants weight rows side by side:
+// where its rows start at multiples of 16 bytes (vec) the values go through the warp's shared memory and out in
+// 16-byte pieces, else straight from the lanes.
 template <int OUT, int N>
-__device__ __forceinline__ void store_run(const GemmArgs &p, const Tile &x, int (&v)[N], int g, int r, float rw) {
+__device__ __forceinline__ void store_run(const GemmArgs &p, const Tile &x, int (&v)[N], int g, int r0, float rw, unsigned char *buf, bool vec) {
+    constexpr int ITEM = OUT == COLI_ACT_F32 ? 4 : 2;
+    using Item = typename std::conditional<OUT == COLI_ACT_F32, float, __nv_bfloat16>::type;
     const int lane = threadIdx.x & 31;
     float rx = p.xscale && lane < N && g + lane < x.nr ? __ldg(p.xscale + x.n0 + g + lane) : 1.f;
     run_sums(v, rw, rx);
+    float *s_rx = reinterpret_cast<float *>(buf + STAGED);
+    __syncwarp();                                          // what was there has been read
+    if (lane < N) s_rx[lane] = rx;
+    __syncwarp();
+    auto item = [](float y) {
+        if constexpr (OUT == COLI_ACT_F32) return y;
+        else return __float2bfloat16_rn(y);
+    };
+    if (vec) {
+        constexpr int FIT = STAGED / (32 * ITEM), RUN = N < FIT ? N : FIT;  // rows at a time
+        constexpr int PIECES = 32 * ITEM / 16, ROWS = 32 / PIECES;          // 16-byte pieces of a row, rows of a step
+        const int c = r0 + lane % PIECES * (16 / ITEM);
+        unsigned char *dst = static_cast<unsigned char *>(p.out) + (static_cast<size_t>(x.n0 + g + lane / PIECES) * p.ldo + c) * ITEM;
+        const size_t step = ROWS * p.ldo * ITEM;
+        const int left = c < p.n ? x.nr - g - lane / PIECES : 0;            // rows from this lane's first on
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-        if (g + j >= x.nr) break;  // the same for the whole warp
-        const float y = __int_as_float(v[j]) * (rw * __shfl_sync(0xffffffffu, rx, j));
-        if (r < p.n) {
-            const size_t at = static_cast<size_t>(x.n0 + g + j) * p.ldo + r;
-            if (OUT == COLI_ACT_F32) static_cast<float *>(p.out)[at] = y;
-            else static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(y);
+        for (int h = 0; h < N; h += RUN) {
+            if (g + h >= x.nr) return;                                      // the same for the whole warp
+            if (h) __syncwarp();
+#pragma unroll
+            for (int j = 0; j < RUN; j += 4) {
+                const float4 s = *reinterpret_cast<const float4 *>(s_rx + h + j);
+                Item *to = reinterpret_cast<Item *>(buf) + j * 32 + lane;
+                to[0] = item(__int_as_float(v[h + j]) * (rw * s.x));
+                to[32] = item(__int_as_float(v[h + j + 1]) * (rw * s.y));
+                to[64] = item(__int_as_float(v[h + j + 2]) * (rw * s.z));
+                to[96] = item(__int_as_float(v[h + j + 3]) * (rw * s.w));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < RUN; i += ROWS, dst += step) {
+                if (h + i >= left) continue;
+                const uint4 w = *reinterpret_cast<const uint4 *>(buf + 16 * lane + i * 32 * ITEM);
+                if (c + 16 / ITEM <= p.n) {
+                    *reinterpret_cast<uint4 *>(dst) = w;
+                } else {
+                    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 16 / ITEM; ++e)
+                        if (c + e < p.n) {
+                            if (ITEM == 4) reinterpret_cast<uint32_t *>(dst)[e] = words[e];
+                            else reinterpret_cast<uint16_t *>(dst)[e] = static_cast<uint16_t>(words[e / 2] >> 16 * (e & 1));
+                        }
+                }
+            }
+        }
+    } else {
+        Item *dst = static_cast<Item *>(p.out) + static_cast<size_t>(x.n0 + g) * p.ldo + r0 + lane;
+        const int rows = r0 + lane < p.n ? x.nr - g : 0;
+#pragma unroll
+        for (int j = 0; j < N; j += 4) {
+            const float4 s = *reinterpret_cast<const float4 *>(s_rx + j);
+            const float f[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i, dst += p.ldo)
+                if (j + i < rows) *dst = item(__int_as_float(v[j + i]) * (rw * f[i]));
         }
     }
+}
+template <int OUT>
+__device__ __forceinline__ bool out_in_pieces(const GemmArgs &p) {
+    return ((reinterpret_cast<uintptr_t>(p.out) | p.ldo * (OUT == COLI_ACT_F32 ? 4 : 2)) & 15) == 0;
 }
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, int (&v)[8]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
@@ -114,8 +173,8 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, int (&v)[8]) {
 // pfree twice before that looked at it.  tl counts the tiles; `last`: none follows.  One epilogue warp's 32 weight rows; false
 // when a wait gave up.
 template <int OUT>
-__device__ __forceinline__ bool split_tile(const GemmArgs &p, const Tile &x, uint32_t dt, int C, int rank, int q, int r, float rw, uint32_t tl, bool last,
-                                           unsigned char *part, uint64_t *pfull, uint64_t *pfree, volatile int *abort) {
+__device__ __forceinline__ bool split_tile(const GemmArgs &p, const Tile &x, uint32_t dt, int C, int rank, int q, float rw, uint32_t tl, bool last,
+                                           unsigned char *buf, bool vec, unsigned char *part, uint64_t *pfull, uint64_t *pfree, volatile int *abort) {
     const int lane = threadIdx.x & 31, row = 32 * q + lane;
     const int pieces = (x.nr + 7) / 8, per = (pieces + C - 1) / C;
     const int lo = min(rank * per, pieces), own = min(pieces - lo, per);
@@ -147,7 +206,7 @@ __device__ __forceinline__ bool split_tile(const GemmArgs &p, const Tile &x, uin
                 v[4 * h + 2] += f.z;
                 v[4 * h + 3] += f.w;
             }
-        store_run<OUT>(p, x, v, 8 * (lo + i), r, rw);
+        store_run<OUT>(p, x, v, 8 * (lo + i), x.m * 128 + 32 * q, rw, buf, vec);
     }
     __syncwarp();
     if (lane < C && lane != rank && !last) remote_arrive(map_rank(smem_u32(pfree), lane));
@@ -279,6 +338,8 @@ __global__ void __launch_bounds__(THREADS, 1) i8_gemm_kernel(const __grid_consta
     } else {
         // ------------------------------------------------------------------ epilogue
         const int q = warp & 3;  // TMEM lane quarter (warp % 4)
+        unsigned char *buf = part + P::PART + q * WARP_BUF;
+        const bool vec = out_in_pieces<OUT>(p);
         uint32_t tl = 0;
         if (SPLIT && C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         for (int t = first; t < ntiles; t += stride, ++tl) {
@@ -290,12 +351,18 @@ __global__ void __launch_bounds__(THREADS, 1) i8_gemm_kernel(const __grid_consta
             tc_fence_after();
             const uint32_t dt = tbase + acc * P::ACC + (static_cast<uint32_t>(32 * q) << 16);
             if (SPLIT && C > 1) {
-                if (!split_tile<OUT>(p, x, dt, C, rank, q, r, rw, tl, t + stride >= ntiles, part, pfull, pfree, abort)) break;
+                if (!split_tile<OUT>(p, x, dt, C, rank, q, rw, tl, t + stride >= ntiles, buf, vec, part, pfull, pfree, abort)) break;
             } else {
-                for (int g = 0; g < x.nr; g += 32) {
+                int g = 0;
+                for (; x.nr - g > 8; g += 32) {
                     int v[32];
                     tmem_ld32(dt + g, v);
-                    store_run<OUT>(p, x, v, g, r, rw);
+                    store_run<OUT>(p, x, v, g, x.m * 128 + 32 * q, rw, buf, vec);
+                }
+                if (g < x.nr) {
+                    int v[8];
+                    tmem_ld8(dt + g, v);
+                    store_run<OUT>(p, x, v, g, x.m * 128 + 32 * q, rw, buf, vec);
                 }
             }
             tc_fence_before();
@@ -325,57 +392,15 @@ __global__ void __launch_bounds__(THREADS, 1) i8_gemm_kernel(const __grid_consta
 // CTA sends its sums of the others' runs to the CTA there that has the same weight rows, adds what comes in for its
 // own, and stores those.  The ring takes them in: nothing else uses it any more when a CTA says that it may be written to.
 constexpr int P_THREADS = (W_EPI0 + P_EPI) * 32;
-constexpr int P_OUT = 8192;              // bytes of an epilogue half's staging buffer
 constexpr int RUN_BYTES = 128 * 32 * 4;  // a run's sums of a CTA's weight rows
 
 struct PairPlan {
     static constexpr int B_BYTES = P_NT / 2 * KB;
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int S = (216 * 1024 - 2 * P_OUT) / STAGE;
-    static constexpr size_t SMEM = static_cast<size_t>(S) * STAGE + 2 * P_OUT + 1024;
+    static constexpr int S = (216 * 1024 - P_EPI * WARP_BUF) / STAGE;
+    static constexpr size_t SMEM = static_cast<size_t>(S) * STAGE + P_EPI * WARP_BUF + 1024;
     static_assert((MAX_SPLIT - 1) * (P_NT / 32 / MAX_SPLIT) * RUN_BYTES <= S * STAGE && P_NT / 32 / 2 * RUN_BYTES <= S * STAGE, "a split's sums fit the ring");
 };
-
-// A run of 32 rows x this CTA's 128 weight rows through shared memory: lanes hold a weight row each, out wants weight
-// rows side by side.  `buf`: the half's P_OUT bytes; vec: 16-byte stores are aligned.
-template <int OUT>
-__device__ __forceinline__ void staged_run(const GemmArgs &p, const Tile &x, const int *v, int g, int row0, float rw, float rx,
-                                           unsigned char *buf, int half, int q, int lane) {
-    constexpr int ITEM = OUT == COLI_ACT_F32 ? 4 : 2;
-    constexpr int RUN = OUT == COLI_ACT_F32 ? 16 : 32;    // rows at a time
-    constexpr int COLS = 128;
-    constexpr int VPR = COLS * ITEM / 16;                 // 16-byte pieces of a row
-    const int tid = 32 * q + lane;
-#pragma unroll
-    for (int h = 0; h < 32 / RUN; ++h) {
-        if (g + RUN * h >= x.nr) return;                  // the same for all four warps
-        half_sync(half);                                  // the buffer's last run has been read
-#pragma unroll
-        for (int j = 0; j < RUN; ++j) {
-            const float y = __int_as_float(v[RUN * h + j]) * (rw * __shfl_sync(0xffffffffu, rx, RUN * h + j));
-            if (OUT == COLI_ACT_F32) reinterpret_cast<float *>(buf)[j * COLS + tid] = y;
-            else reinterpret_cast<__nv_bfloat16 *>(buf)[j * COLS + tid] = __float2bfloat16_rn(y);
-        }
-        half_sync(half);
-#pragma unroll
-        for (int i = 0; i < RUN * VPR / 128; ++i) {
-            const int at = i * 128 + tid, j = at / VPR, c = row0 + (at % VPR) * (16 / ITEM);
-            const int row = g + RUN * h + j;
-            if (row >= x.nr || c >= p.n) continue;
-            unsigned char *dst = static_cast<unsigned char *>(p.out) + (static_cast<size_t>(x.n0 + row) * p.ldo + c) * ITEM;
-            const uint4 w = *reinterpret_cast<const uint4 *>(buf + 16 * at);
-            if (c + 16 / ITEM <= p.n) {
-                *reinterpret_cast<uint4 *>(dst) = w;
-            } else {
-                const int n = min(16 / ITEM, p.n - c);
-                for (int e = 0; e < n; ++e) {
-                    if (ITEM == 4) reinterpret_cast<float *>(dst)[e] = reinterpret_cast<const float *>(buf + 16 * at)[e];
-                    else reinterpret_cast<uint16_t *>(dst)[e] = reinterpret_cast<const uint16_t *>(buf + 16 * at)[e];
-                }
-            }
-        }
-    }
-}
 
 template <int OUT, bool SPLIT>
 __global__ void __launch_bounds__(P_THREADS, 1) i8_pair_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs p) {  // clusters of 2 C CTAs
@@ -522,9 +547,8 @@ __global__ void __launch_bounds__(P_THREADS, 1) i8_pair_kernel(const __grid_cons
     } else {
         // ------------------------------------------------------------------ epilogue
         const int q = warp & 3, half = (warp - W_EPI0) >> 2;  // TMEM lane quarter; every other of this CTA's runs
-        unsigned char *obuf = sout + half * P_OUT;
-        constexpr int ITEM = OUT == COLI_ACT_F32 ? 4 : 2;
-        const bool vec = ((reinterpret_cast<uintptr_t>(p.out) | (p.ldo * ITEM)) & 15) == 0;
+        unsigned char *buf = sout + (warp - W_EPI0) * WARP_BUF;
+        const bool vec = out_in_pieces<OUT>(p);
         uint32_t tl = 0;
         for (int t = first; t < ntiles; t += stride, ++tl) {
             next_tile(t);
@@ -532,8 +556,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) i8_pair_kernel(const __grid_cons
             const int acc = tl & 1, row0 = x.m * 256 + rank * 128;
             const int r = row0 + 32 * q + lane, runs = (x.nr + 31) / 32;
             const float rw = p.wscale && r < p.n ? __ldg(p.wscale + static_cast<size_t>(x.e) * p.wscale_stride + r) : 1.f;
-            // (all eight warps meet in the staging barriers: they give up together, or not at all)
-            if (epi_or(!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&dfull[acc]), (tl >> 1) & 1, abort, p.err)))) break;
+            if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&dfull[acc]), (tl >> 1) & 1, abort, p.err))) break;
             tc_fence_after();
             const uint32_t dt = tbase + acc * P_NT + (static_cast<uint32_t>(32 * q) << 16);
             const int own = runs > part ? (runs - part + C - 1) / C : 0;  // this CTA's runs
@@ -545,7 +568,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) i8_pair_kernel(const __grid_cons
                     if (lane < C && lane != part) remote_arrive(map_rank(smem_u32(pready), 2 * lane + rank));
                     __syncwarp();
                 }
-                if (epi_or(!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(pready), tl & 1, abort, p.err)))) break;
+                if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(pready), tl & 1, abort, p.err))) break;
                 for (int g = half; g < runs; g += 2) {
                     const int to = g % C;
                     if (to == part) continue;
@@ -558,7 +581,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) i8_pair_kernel(const __grid_cons
                         asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];"
                                      ::"r"(dst + ((i ^ (lane & 7)) << 4)), "r"(v[4 * i]), "r"(v[4 * i + 1]), "r"(v[4 * i + 2]), "r"(v[4 * i + 3]), "r"(bar) : "memory");
                 }
-                if (epi_or(!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(pfull), tl & 1, abort, p.err)))) break;
+                if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(pfull), tl & 1, abort, p.err))) break;
             }
             for (int i = half; i < own; i += 2) {
                 const int g = 32 * (part + i * C);
@@ -576,13 +599,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) i8_pair_kernel(const __grid_cons
                             v[4 * j + 3] += f.w;
                         }
                     }
-                if (!vec) {
-                    store_run<OUT>(p, x, v, g, r, rw);
-                    continue;
-                }
-                float rx = p.xscale && g + lane < x.nr ? __ldg(p.xscale + x.n0 + g + lane) : 1.f, rwg = rw;
-                run_sums(v, rwg, rx);
-                staged_run<OUT>(p, x, v, g, row0, rwg, rx, obuf, half, q, lane);
+                store_run<OUT>(p, x, v, g, row0 + 32 * q, rw, buf, vec);
             }
             tc_fence_before();
             __syncwarp();

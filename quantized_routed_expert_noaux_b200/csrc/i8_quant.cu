@@ -2,47 +2,39 @@
 // where asked for, every row written to the places of its copies.
 //
 // scale = m / 127, m = the row's largest |x| (at least 127 * 2^-126); code = the whole number nearest to x / (m / 127) of
-// the real numbers, ties to even.  y = x * fl(127 / m) is at most 2^-16 off the real quotient (|y| <= 127, two
-// roundings of 2^-24), so its nearest whole number is the right one unless y lies within 2^-15 of a half.  A chunk that
-// holds such a y is decided exactly: 127 |x| against (i + 1/2) m.  With p = fl((i + 1/2) m) and e = (i + 1/2) m - p (an FMA gives
-// it exactly), 127 |x| - p is a float32 too: the two are within 2^-13 of each other and 127 |x| has 31 bits; it is compared with
-// e.  (Both sides over 128, and times 2^64 where m is below 1, so that nothing overflows or underflows.)
+// the real numbers, ties to even.  With v within 2^-22 of 127 / m, the real quotient lies between x v (1 - 2^-21)
+// and x v (1 + 2^-21), and so does its nearest whole number between theirs (an FMA that adds 1.5 * 2^23 rounds each
+// once, to a whole number).  Where those two differ, once in 10^5 elements, the quotient is next to a half i + 1/2, and
+// 127 |x| is compared with (i + 1/2) m: with p = fl((i + 1/2) m) and e = (i + 1/2) m - p (an FMA gives it exactly), 127 |x| - p is
+// a float32 too, since the two are within 2^-13 of each other and 127 |x| has 31 bits; it is compared with e.  (Both
+// sides over 128, and times 2^64 where m is below 1, so that nothing overflows or underflows.)
 //
 // A thread takes chunks of 16 elements; the row's chunks stay in registers between the pass that finds m
-// and the one that writes, HOLD to a thread; what rows beyond HOLD * MOST_T chunks have more is read again, from L2.
+// and the one that writes, HOLD to a thread (what is done once a row and thread, 60 instructions, counts beside the 90 of a
+// chunk); what rows beyond HOLD * MOST_T chunks have more is read again, from L2.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <algorithm>
+#include <atomic>
 
 #include "chunk.h"
 #include "i8.h"
 #include "internal.h"
 #include "pdl.h"
+#include "tc_ptx.h"
 
 namespace coli {
 
 namespace {
 
 constexpr unsigned FULL = 0xffffffffu;
-#ifndef NB
-#define NB 3
-#define NF 2
-#endif
 constexpr int HOLD = 2;       // chunks a thread keeps in registers
 constexpr int MOST_T = 384;   // threads of a row at most
 constexpr int WARP_ROWS = 4;  // rows of a CTA where a warp takes a row
 
 // Two float32 operations in one instruction.
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -61,73 +53,171 @@ __device__ __forceinline__ void load_some(Chunk<In> &c, const In *p, int n) {
     }
 }
 // align: what every row's address is a multiple of, in bytes (32, 16 or less)
-template <typename In>
+template <typename In, bool SHARED>
 __device__ __forceinline__ void load_chunk(Chunk<In> &c, const In *p, int n, int align) {
+    if constexpr (SHARED) {  // whole 16-byte pieces
+        uint32_t w[sizeof(In) * 4] = {};
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(In)); ++i)
+            if (n > i * static_cast<int>(16 / sizeof(In))) {
+                const uint4 q = reinterpret_cast<const uint4 *>(p)[i];
+                w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
+            }
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(In)) * 4; ++i) {
+            if constexpr (sizeof(In) == 4) c.v[i] = __uint_as_float(w[i]);
+            else c.w[i] = w[i];
+        }
+        return;
+    }
     if (n >= 16 && align >= 16) c.load(p, align >= 32);
     else load_some(c, p, n);
+}
+
+// The largest magnitude so far as bits of a float32 (of two bf16 values side by side): a NaN stays.  (The signs
+// of the results mean nothing.)
+__device__ __forceinline__ void largest(uint32_t &top, const Chunk<float> &c) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm("max.NaN.xorsign.abs.f32 %0, %0, %1;" : "+r"(top) : "r"(__float_as_uint(c.v[i])));
+}
+__device__ __forceinline__ void largest(uint32_t &top, const Chunk<uint16_t> &c) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(c.w[i]));
+}
+template <typename Held>
+__device__ __forceinline__ uint32_t magnitude(uint32_t top) {
+    if constexpr (sizeof(Held) == sizeof(Chunk<float>)) return top & 0x7fffffffu;
+    else return max(top & 0x7fff0000u, top << 16 & 0x7fff0000u);
 }
 
 // What is quantised: the row's own elements, or SiLU(gate) * up in float32.
 template <typename In, bool GLU> struct Source { using Held = Chunk<In>; };
 template <typename In> struct Source<In, true> { using Held = Chunk<float>; };
 
-template <typename In, bool GLU>
-__device__ __forceinline__ void fetch(typename Source<In, GLU>::Held &h, const In *row, int k, int i, int align) {
+template <typename In, bool GLU, bool SHARED = false>
+__device__ __forceinline__ void fetch(typename Source<In, GLU>::Held &h, const In *row, int k, int up, int i, int align) {  // up: where up values begin
     const int n = k - 16 * i;
     if constexpr (GLU) {
         Chunk<In> g, u;
-        load_chunk(g, row + 16 * static_cast<size_t>(i), n, align);
-        load_chunk(u, row + k + 16 * static_cast<size_t>(i), n, align);
+        load_chunk<In, SHARED>(g, row + 16 * static_cast<size_t>(i), n, align);
+        load_chunk<In, SHARED>(u, row + up + 16 * static_cast<size_t>(i), n, align);
 #pragma unroll
         for (int j = 0; j < 16; ++j) h.v[j] = __fdividef(g.at(j), 1.0f + expf(-g.at(j))) * u.at(j);
     } else {
-        load_chunk(h, row + 16 * static_cast<size_t>(i), n, align);
+        load_chunk<In, SHARED>(h, row + 16 * static_cast<size_t>(i), n, align);
     }
 }
 
-constexpr float ROUND = 12582912.0f;                     // 1.5 * 2^23: added, the whole number is in the low bits
-constexpr float BORDER = 0.5f - 1.0f / 32768.0f;
+constexpr float ROUND = 12582912.0f;  // 1.5 * 2^23: added, the whole number is in the low bits
 
-__device__ __forceinline__ uint32_t pack4(const uint32_t *b) {  // the low bytes of four words
-    return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+__device__ __forceinline__ uint32_t pack4(const float *f) {  // the low bytes of four words
+    return __byte_perm(__byte_perm(__float_as_uint(f[0]), __float_as_uint(f[1]), 0x0040), __byte_perm(__float_as_uint(f[2]), __float_as_uint(f[3]), 0x0040), 0x5410);
 }
 
+// Codes of a chunk; `lo`, `hi`: v (1 - 2^-21) and v (1 + 2^-21), twice each.
 template <typename Held>
-__device__ __forceinline__ uint4 encode(const Held &h, float m, float inv) {
-    uint32_t b[16];
-    float off = 0.f;
-    const uint64_t inv2 = pack2(inv, inv), up = pack2(ROUND, ROUND), down = pack2(-ROUND, -ROUND), minus = pack2(-1.f, -1.f);
+__device__ __forceinline__ uint4 encode(const Held &h, float m, uint64_t lo, uint64_t hi) {
+    const uint64_t up = pack2(ROUND, ROUND);
+    uint32_t word[4], differ = 0u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint64_t y = mul2(pack2(h.at(2 * i), h.at(2 * i + 1)), inv2), r = add2(y, up);
-        float lo, hi, d0, d1;
-        unpack2(r, lo, hi);
-        unpack2(fma2(add2(r, down), minus, y), d0, d1);  // what rounding took away, exactly
-        off = fmaxf(off, fmaxf(fabsf(d0), fabsf(d1)));
-        b[2 * i] = __float_as_uint(lo);
-        b[2 * i + 1] = __float_as_uint(hi);
+    for (int w = 0; w < 4; ++w) {
+        float a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint64_t x = pack2(h.at(4 * w + 2 * i), h.at(4 * w + 2 * i + 1));
+            unpack2(fma2(x, lo, up), a[2 * i], a[2 * i + 1]);
+            unpack2(fma2(x, hi, up), b[2 * i], b[2 * i + 1]);
+        }
+        word[w] = pack4(a);
+        differ |= word[w] ^ pack4(b);
     }
-    if (off > BORDER) {
+    if (differ) {
+        float vl, vh;
+        unpack2(lo, vl, vh);
         const float up64 = m < 1.f ? 0x1p64f : 1.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const float x = h.at(i), y = fabsf(x * inv), f = floorf(y);
-            if (fabsf(y - f - 0.5f) < 1.0f / 16384.0f) {
-                const float g = (f + 0.5f) * 0x1p-7f, ms = m * up64, p = g * ms;
-                const float e = fmaf(g, ms, -p), d = fmaf(127.0f * 0x1p-7f, fabsf(x) * up64, -p);
-                int c = static_cast<int>(f);
-                c += d > e || (d == e && (c & 1));
-                b[i] = static_cast<uint32_t>(x < 0.f ? -c : c);
+            const float x = h.at(i), f = floorf(fabsf(x * vl)), r = rintf(fabsf(x * vl));
+            // (f: the half's i, or one more where x vl comes that close to the next whole number, which is no border then)
+            const float g = (f + 0.5f) * 0x1p-7f, ms = m * up64, p = g * ms;
+            const float e = fmaf(g, ms, -p), d = fmaf(127.0f * 0x1p-7f, fabsf(x) * up64, -p);
+            const bool near = fabsf(fabsf(x * vl) - f - 0.5f) < 1.0f / 8192.0f;
+            int c = static_cast<int>(f);
+            c += d > e || (d == e && (c & 1));
+            if (!near) c = static_cast<int>(r);
+            const uint32_t byte = static_cast<uint32_t>(x < 0.f ? -c : c) & 0xffu;
+            word[i >> 2] = (word[i >> 2] & ~(0xffu << 8 * (i & 3))) | byte << 8 * (i & 3);
+        }
+    }
+    return make_uint4(word[0], word[1], word[2], word[3]);
+}
+
+// What a row's codes are made with: from the bits of its largest magnitude.
+struct Scale {
+    bool finite;
+    float m;
+    uint64_t lo, hi;
+    __device__ __forceinline__ explicit Scale(uint32_t top) {
+        finite = top < INF_BITS;
+        m = fmaxf(__uint_as_float(top), 127.0f * 0x1p-126f);
+        float v;  // (of m / 16, whose inverse is a normal number)
+        asm("rcp.approx.f32 %0, %1;" : "=f"(v) : "f"(m * 0.0625f));
+        v *= 127.0f * 0.0625f;
+        const float vlo = v * (1.0f - 0x1p-21f), vhi = v * (1.0f + 0x1p-21f);
+        lo = pack2(vlo, vlo);
+        hi = pack2(vhi, vhi);
+    }
+    __device__ __forceinline__ float value() const { return finite ? __fdiv_rn(m, 127.0f) : __uint_as_float(0x7fffffffu); }
+    template <typename Held>
+    __device__ __forceinline__ uint4 codes(const Held &h) const {
+        return finite ? encode(h, m, lo, hi) : make_uint4(0u, 0u, 0u, 0u);
+    }
+};
+
+// Where row r goes.  With PLACE: the places of its first 32 copies are in `first`, one per lane.
+template <bool PLACE>
+struct Target {
+    const I8QuantArgs &a;
+    const int r, lane;
+    int first;
+    __device__ __forceinline__ Target(const I8QuantArgs &a, int r) : a(a), r(r), lane(threadIdx.x & 31), first(-1) {
+        if (PLACE && lane < a.copies) first = __ldg(a.place + static_cast<size_t>(r) * a.copies + lane);
+    }
+    __device__ __forceinline__ int named(int c0) const {  // copy c0 + lane
+        return c0 == 0 ? first : c0 + lane < a.copies ? __ldg(a.place + static_cast<size_t>(r) * a.copies + c0 + lane) : -1;
+    }
+    __device__ __forceinline__ void put_scale(float scale) const {  // by one warp
+        if constexpr (!PLACE) {
+            if (lane == 0) a.row_scale[r] = scale;
+        } else {
+            for (int c0 = 0; c0 < a.copies; c0 += 32) {
+                const int to = named(c0);
+                if (to >= 0 && to < a.rows) a.row_scale[to] = scale;
+                else if (to != -1) atomicOr(a.err, COLI_DEVERR_GROUPING);
             }
         }
     }
-    return make_uint4(pack4(b), pack4(b + 4), pack4(b + 8), pack4(b + 12));
-}
+    __device__ __forceinline__ void put(const uint4 &v, int i, int n) const {  // chunk i of n, by whole warps
+        int8_t *at = a.codes + 16 * static_cast<size_t>(i);
+        if constexpr (!PLACE) {
+            if (i < n) *reinterpret_cast<uint4 *>(at + static_cast<size_t>(r) * a.ldc) = v;
+        } else {
+            for (int c0 = 0; c0 < a.copies; c0 += 32) {
+                const int mine = named(c0);
+                for (int c = 0; c < min(32, a.copies - c0); ++c) {
+                    const int to = __shfl_sync(FULL, mine, c);
+                    if (to >= 0 && to < a.rows && i < n) *reinterpret_cast<uint4 *>(at + static_cast<size_t>(to) * a.ldc) = v;
+                }
+            }
+        }
+    }
+};
 
 // A row by a warp (WARP: WARP_ROWS rows to a CTA) or by a CTA.
-template <typename In, bool GLU, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * WARP_ROWS : MOST_T, (WARP ? 3 : 1) * (sizeof(In) == 2 && !GLU ? NB : NF)) i8_quantize_kernel(const I8QuantArgs a, int align) {
+template <typename In, bool GLU, bool WARP, bool PLACE>
+__global__ void __launch_bounds__(WARP ? 32 * WARP_ROWS : MOST_T, WARP ? 6 : 2) i8_quantize_kernel(const I8QuantArgs a, int align, bool staged) {
     using Held = typename Source<In, GLU>::Held;
+    extern __shared__ __align__(16) unsigned char stage[];
     __shared__ uint32_t s_max[MOST_T / 32];
     wait_for_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -137,80 +227,166 @@ __global__ void __launch_bounds__(WARP ? 32 * WARP_ROWS : MOST_T, (WARP ? 3 : 1)
     const int n = (a.k + 15) / 16;
     const In *row = static_cast<const In *>(a.x) + static_cast<size_t>(r) * a.ldx;
     Held held[HOLD];
+    const In *src = row;
+    int up = a.k;
+    if (staged) {
+        // rows at any address: by neighbouring lanes into shared memory, chunks from there
+        const int padded = n * 16;
+        In *mine = reinterpret_cast<In *>(stage) + static_cast<size_t>(WARP ? warp : 0) * padded * (GLU ? 2 : 1);
+#pragma unroll
+        for (int part = 0; part < (GLU ? 2 : 1); ++part)
+            for (int base = i0; base < padded; base += 16 * tpr) {
+                In v[16];  // all on their way together
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = base + j * tpr < a.k ? __ldg(row + part * a.k + base + j * tpr) : In(0);
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (base + j * tpr < padded) mine[part * padded + base + j * tpr] = v[j];
+            }
+        if (WARP) __syncwarp();
+        else __syncthreads();
+        src = mine;
+        up = padded;
+    }
 #pragma unroll
     for (int h = 0; h < HOLD; ++h) {
-        if (i0 + h * tpr < n) fetch<In, GLU>(held[h], row, a.k, i0 + h * tpr, align);
-        else held[h].zero();
+        const int i = i0 + h * tpr;
+        if (i >= n) held[h].zero();
+        else if (staged) fetch<In, GLU, true>(held[h], src, n * 16, up, i, 16);
+        else fetch<In, GLU>(held[h], src, a.k, up, i, align);
     }
-    const int32_t *places = a.place ? a.place + static_cast<size_t>(r) * a.copies : nullptr;
-    const int first = places ? (lane < a.copies ? __ldg(places + lane) : -1) : (lane ? -1 : r);  // of the first 32 copies, one per lane
+    const Target<PLACE> target(a, r);
     uint32_t top = 0u;
 #pragma unroll
-    for (int h = 0; h < HOLD; ++h) top = max(top, held[h].amax());
+    for (int h = 0; h < HOLD; ++h) largest(top, held[h]);
     for (int i = i0 + HOLD * tpr; i < n; i += tpr) {
         Held c;
-        fetch<In, GLU>(c, row, a.k, i, align);
-        top = max(top, c.amax());
+        fetch<In, GLU>(c, row, a.k, a.k, i, align);
+        largest(top, c);
     }
-    top = __reduce_max_sync(FULL, top);
+    top = __reduce_max_sync(FULL, magnitude<Held>(top));
     if (!WARP) {
         if (lane == 0) s_max[warp] = top;
         __syncthreads();
         top = __reduce_max_sync(FULL, lane < tpr / 32 ? s_max[lane] : 0u);
     }
-    const bool finite = top < INF_BITS;
-    const float m = fmaxf(__uint_as_float(top), 127.0f * 0x1p-126f);
-    const float scale = finite ? __fdiv_rn(m, 127.0f) : __uint_as_float(0x7fffffffu), inv = finite ? __fdiv_rn(127.0f, m) : 0.f;
-    auto where = [&](int c0) {  // of copies c0 .. c0 + 31, one per lane
-        const int to = c0 == 0 ? first : c0 + lane < a.copies ? __ldg(places + c0 + lane) : -1;
-        return to < -1 || to >= a.rows ? -1 : to;
-    };
-    if (WARP || warp == 0)
-        for (int c0 = 0; c0 < a.copies; c0 += 32) {
-            const int to = where(c0);
-            if (to >= 0) a.row_scale[to] = scale;
-            else if ((c0 == 0 ? first : c0 + lane < a.copies ? __ldg(places + c0 + lane) : -1) != -1) atomicOr(a.err, COLI_DEVERR_GROUPING);
-        }
-    uint4 code[HOLD];
-#pragma unroll
-    for (int h = 0; h < HOLD; ++h) code[h] = finite ? encode(held[h], m, inv) : make_uint4(0u, 0u, 0u, 0u);
-    auto put = [&](const uint4 &v, int i) {
-        const int at = where(0);
-        for (int c0 = 0; c0 < a.copies; c0 += 32) {
-            const int to = c0 == 0 ? at : where(c0);
-            for (unsigned left = __ballot_sync(FULL, to >= 0); left; left &= left - 1) {
-                const int row_to = __shfl_sync(FULL, to, __ffs(left) - 1);
-                if (i < n) *reinterpret_cast<uint4 *>(a.codes + static_cast<size_t>(row_to) * a.ldc + 16 * static_cast<size_t>(i)) = v;
-            }
-        }
-    };
+    const Scale s(top);
+    if (WARP || warp == 0) target.put_scale(s.value());
 #pragma unroll
     for (int h = 0; h < HOLD; ++h)
-        if (h * tpr < n) put(code[h], i0 + h * tpr);
+        if (h * tpr < n) target.put(s.codes(held[h]), i0 + h * tpr, n);
     for (int base = HOLD * tpr; base < n; base += tpr) {
         Held c;
-        if (base + i0 < n) fetch<In, GLU>(c, row, a.k, base + i0, align);
+        if (base + i0 < n) fetch<In, GLU>(c, row, a.k, a.k, base + i0, align);
         else c.zero();
-        put(finite ? encode(c, m, inv) : make_uint4(0u, 0u, 0u, 0u), base + i0);
+        target.put(s.codes(c), base + i0, n);
     }
 }
 
-template <typename In, bool GLU>
+// Many rows: a CTA takes them one after another out of a ring in shared memory that bulk copies fill, so that what is on its way
+// does not depend on registers.  Rows are whole 16-byte pieces that start at multiples of 16 bytes.
+constexpr int RING_ROWS = 1024, MOST_SLOTS = 8;
+template <typename In, bool GLU> constexpr int RING_HOLD = sizeof(In) == 2 && !GLU ? 4 : 2;
+constexpr size_t RING_SMEM = 208 * 1024;  // of all CTAs of an SM
+
+template <typename In, bool GLU, bool PLACE>
+__global__ void __launch_bounds__(MOST_T, 2) i8_quantize_ring_kernel(const I8QuantArgs a, int row_bytes, int slots) {
+    using Held = typename Source<In, GLU>::Held;
+    constexpr int HOLD = RING_HOLD<In, GLU>;
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ __align__(8) uint64_t bars[MOST_SLOTS];
+    __shared__ uint32_t s_max[2][MOST_T / 32];
+    __shared__ int s_abort;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = (a.k + 15) / 16;
+    volatile int *abort = &s_abort;
+    const int mine = (a.src_rows - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1;  // (no more CTAs than rows)
+    auto load = [&](int j, int slot) {  // by thread 0
+        const uint32_t bar = smem_u32(&bars[slot]);
+        mbar_expect_tx(bar, row_bytes);
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                     ::"r"(smem_u32(ring + slot * row_bytes)),
+                       "l"(static_cast<const In *>(a.x) + (blockIdx.x + static_cast<size_t>(j) * gridDim.x) * a.ldx), "r"(row_bytes), "r"(bar) : "memory");
+    };
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < slots; ++i) mbar_init(smem_u32(&bars[i]), 1);
+        s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    wait_for_previous();
+    if (threadIdx.x == 0)
+        for (int j = 0; j < slots && j < mine; ++j) load(j, j);
+    int j = 0, slot = 0;
+    uint32_t phase = 0;
+    for (; j < mine; ++j) {
+        const Target<PLACE> target(a, blockIdx.x + j * gridDim.x);
+        const bool ok = mbar_wait(smem_u32(&bars[slot]), phase, abort, a.err);
+        const In *row = reinterpret_cast<const In *>(ring + slot * row_bytes);
+        Held held[HOLD];
+        uint32_t top = 0u;
+#pragma unroll
+        for (int h = 0; h < HOLD; ++h) {
+            const int i = threadIdx.x + h * blockDim.x;
+            if (i < n) fetch<In, GLU, true>(held[h], row, a.k, a.k, i, 16);
+            else held[h].zero();
+            largest(top, held[h]);
+        }
+        top = __reduce_max_sync(FULL, magnitude<Held>(top));
+        if (lane == 0) s_max[j & 1][warp] = top;
+        if (__syncthreads_or(!ok)) break;
+        // the row is in registers: its slot takes the next one
+        if (threadIdx.x == 0 && j + slots < mine) load(j + slots, slot);
+        if (++slot == slots) {
+            slot = 0;
+            phase ^= 1;
+        }
+        top = __reduce_max_sync(FULL, lane < blockDim.x / 32 ? s_max[j & 1][lane] : 0u);
+        const Scale s(top);
+        if (warp == 0) target.put_scale(s.value());
+#pragma unroll
+        for (int h = 0; h < HOLD; ++h)
+            if (h * blockDim.x < n) target.put(s.codes(held[h]), threadIdx.x + h * blockDim.x, n);
+    }
+    if (j < mine && threadIdx.x == 0)  // given up: what was asked for lands before the ring is released
+        for (int i = j; i < mine && i < j + slots; ++i) mbar_drain(smem_u32(&bars[i % slots]), (i / slots) & 1);
+}
+
+template <typename In, bool GLU, bool PLACE>
 cudaError_t launch(const I8QuantArgs &a, cudaStream_t st) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(a.x) | a.ldx * sizeof(In) | (GLU ? static_cast<size_t>(a.k) * sizeof(In) : 0);
     const int align = at & 15 ? 1 : at & 31 ? 16 : 32;
     const int n = (a.k + 15) / 16;
+    const size_t staged = align < 16 ? static_cast<size_t>(n) * 16 * (GLU ? 2 : 1) * sizeof(In) : 0;  // bytes of a row in shared memory
     if (n <= HOLD * 32)
-        return launch_early(i8_quantize_kernel<In, GLU, true>, dim3((static_cast<unsigned>(a.src_rows) + WARP_ROWS - 1) / WARP_ROWS), 32 * WARP_ROWS, 0, st, 1, a, align);
-    const int threads = (n + HOLD - 1) / HOLD;
-    return launch_early(i8_quantize_kernel<In, GLU, false>, dim3(a.src_rows), threads < MOST_T ? (threads + 31) / 32 * 32 : MOST_T, 0, st, 1, a, align);
+        return launch_early(i8_quantize_kernel<In, GLU, true, PLACE>, dim3((static_cast<unsigned>(a.src_rows) + WARP_ROWS - 1) / WARP_ROWS), 32 * WARP_ROWS,
+                            WARP_ROWS * staged, st, 1, a, align, staged > 0);
+    auto threads_for = [n](int hold) { return std::min(((n + hold - 1) / hold + 31) / 32 * 32, MOST_T); };
+    const size_t row = static_cast<size_t>(a.k) * (GLU ? 2 : 1) * sizeof(In);
+    if (a.src_rows >= RING_ROWS && align >= 16 && row % 16 == 0 && n > RING_HOLD<In, GLU> * 32 && n <= RING_HOLD<In, GLU> * MOST_T && 2 * row <= RING_SMEM) {
+        const int threads = threads_for(RING_HOLD<In, GLU>);
+        auto kernel = i8_quantize_ring_kernel<In, GLU, PLACE>;
+        static std::atomic<uint64_t> ready{0};
+        const cudaError_t e = allow_smem(kernel, RING_SMEM, ready);
+        if (e != cudaSuccess) return e;
+        const int ctas = static_cast<int>(std::min<size_t>(std::min(2 * MOST_T / threads, 16), RING_SMEM / (2 * row)));  // of an SM
+        const int slots = static_cast<int>(std::min<size_t>(RING_SMEM / ctas / row, MOST_SLOTS));
+        return launch_early(kernel, dim3(std::min(a.src_rows, device_sm_count() * ctas)), threads, slots * row, st, 1, a, static_cast<int>(row), slots);
+    }
+    const bool fits = staged > 0 && staged <= 44 * 1024 && n <= HOLD * MOST_T;  // (of the 48 KB that need no attribute)
+    return launch_early(i8_quantize_kernel<In, GLU, false, PLACE>, dim3(a.src_rows), threads_for(HOLD), fits ? staged : 0, st, 1, a, align,
+                        fits);
 }
 
 }  // namespace
 
+template <typename In>
+static cudaError_t launch_of(bool glu, const I8QuantArgs &a, cudaStream_t st) {
+    if (a.place) return glu ? launch<In, true, true>(a, st) : launch<In, false, true>(a, st);
+    return glu ? launch<In, true, false>(a, st) : launch<In, false, false>(a, st);
+}
+
 cudaError_t launch_i8_quantize(int act, bool glu, const I8QuantArgs &a, cudaStream_t st) {
-    if (act == COLI_ACT_F32) return glu ? launch<float, true>(a, st) : launch<float, false>(a, st);
-    return glu ? launch<uint16_t, true>(a, st) : launch<uint16_t, false>(a, st);
+    return act == COLI_ACT_F32 ? launch_of<float>(glu, a, st) : launch_of<uint16_t>(glu, a, st);
 }
 
 }  // namespace coli

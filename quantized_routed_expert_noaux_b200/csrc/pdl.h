@@ -7,7 +7,9 @@
 // were slower (2048 tokens routed 6.5 us against 5.0, the expert half for one token 70 against 59).
 #pragma once
 
+#include <atomic>
 #include <cuda_runtime.h>
+#include <stdint.h>
 
 namespace coli {
 
@@ -31,6 +33,18 @@ cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int block, size_t
     cfg.attrs = at;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+
+// The kernel's shared-memory attribute lasts as long as the context: set once per device (twice is
+// harmless).
+template <typename K>
+cudaError_t allow_smem(K *kernel, size_t bytes, std::atomic<uint64_t> &ready) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (ready.load(std::memory_order_relaxed) >> dev & 1))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess && dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    return e;
 }
 
 }  // namespace coli
