@@ -395,7 +395,7 @@ coli_status coli_moe_fp4_pack_record(const coli_moe_config *cfg, int act, const 
  * An id of -1 leaves its slot out (an expert of another device, a padded token); other ids outside [0,
  * n_experts) do too and set COLI_DEVERR_EXPERT_ID in the error word of `ws`.  A token may name an expert twice.
  * The gradient in x is coli_moe_combine of the rows' gradients without weights.  T = 0 writes offsets alone.
- * One kernel, or two above 2048 slots; may be captured. */
+ * One kernel, or two for many slots; may be captured. */
 coli_status coli_moe_sort_rows(int n_experts, int top_k, int act, const void *x, int T, int hidden,
                                size_t ldx, const int32_t *topk_ids, int32_t *offsets, int32_t *perm,
                                int32_t *place, void *rows, size_t ldr, void *ws, void *stream);

@@ -220,6 +220,7 @@ __global__ void __launch_bounds__(WARP ? 32 * WARP_ROWS : MOST_T, WARP ? 6 : 2) 
     extern __shared__ __align__(16) unsigned char stage[];
     __shared__ uint32_t s_max[MOST_T / 32];
     wait_for_previous();
+    dependents_may_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int i0 = WARP ? lane : threadIdx.x, tpr = WARP ? 32 : blockDim.x;
     const int r = WARP ? blockIdx.x * WARP_ROWS + warp : blockIdx.x;
@@ -314,6 +315,7 @@ __global__ void __launch_bounds__(MOST_T, 2) i8_quantize_ring_kernel(const I8Qua
     }
     __syncthreads();
     wait_for_previous();
+    dependents_may_launch();
     if (threadIdx.x == 0)
         for (int j = 0; j < slots && j < mine; ++j) load(j, j);
     int j = 0, slot = 0;

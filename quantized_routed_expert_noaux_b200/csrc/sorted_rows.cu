@@ -29,7 +29,7 @@ constexpr unsigned FULL = 0xffffffffu;
 
 // ------------------------------------------------------------------ elements
 
-// V elements of a row as they lie in memory.
+// V elements of a row as they lie in memory.  (No read-only loads: an addend may be the result itself.)
 template <typename T, int V>
 struct Raw {
     static constexpr int BYTES = sizeof(T) * V, WORDS = BYTES < 4 ? 1 : BYTES / 4;
@@ -43,9 +43,9 @@ struct Raw {
         } else if constexpr (BYTES == 8) {
             asm volatile("ld.global.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
         } else if constexpr (BYTES == 4) {
-            w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+            w[0] = *reinterpret_cast<const uint32_t *>(p);
         } else {
-            w[0] = __ldg(reinterpret_cast<const uint16_t *>(p));
+            w[0] = *reinterpret_cast<const uint16_t *>(p);
         }
     }
     __device__ __forceinline__ float at(int i) const {
@@ -53,12 +53,17 @@ struct Raw {
         else return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
     }
 };
-template <typename T, int V>
+// (STREAM: rows that are written once and are more than L2 holds, where there are many: read data stays there longer.)
+template <typename T, int V, bool STREAM = false>
 __device__ __forceinline__ void store_row(T *p, const float (&v)[V]) {
     if constexpr (sizeof(T) == 4) {
         if constexpr (V % 4 == 0) {
 #pragma unroll
-            for (int i = 0; i < V / 4; ++i) reinterpret_cast<float4 *>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            for (int i = 0; i < V / 4; ++i) {
+                const float4 f = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                if (STREAM) __stcs(reinterpret_cast<float4 *>(p) + i, f);
+                else reinterpret_cast<float4 *>(p)[i] = f;
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i) p[i] = v[i];
@@ -72,8 +77,11 @@ __device__ __forceinline__ void store_row(T *p, const float (&v)[V]) {
             const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
             w[i] = *reinterpret_cast<const uint32_t *>(&b);
         }
-        if constexpr (V == 8) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-        else *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+        if constexpr (V == 8) {
+            const uint4 q = make_uint4(w[0], w[1], w[2], w[3]);
+            if (STREAM) __stcs(reinterpret_cast<uint4 *>(p), q);
+            else *reinterpret_cast<uint4 *>(p) = q;
+        } else *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
     }
 }
 
@@ -328,7 +336,8 @@ __global__ void __launch_bounds__(256) sort_copy_kernel(const SortArgs a, int it
 constexpr int BULK_SLOTS = 4, BULK_PIECE = 16384, BULK_MIN = 4096;
 constexpr long BULK_ALL = 288L << 20;
 
-__global__ void __launch_bounds__(32) sort_bulk_kernel(const SortArgs a, int bytes, int pieces, size_t px, size_t pr) {
+// (row, bytes: of a row and of its pieces, the last one shorter, multiples of 16; px, pr: from row to row.)
+__global__ void __launch_bounds__(32) sort_bulk_kernel(const SortArgs a, int row, int bytes, int pieces, size_t px, size_t pr) {
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ __align__(8) uint64_t bars[BULK_SLOTS];
     __shared__ int s_abort;
@@ -345,10 +354,11 @@ __global__ void __launch_bounds__(32) sort_bulk_kernel(const SortArgs a, int byt
         const int w = blockIdx.x + i * gridDim.x, t = w / pieces, piece = w - t * pieces;
         const uint32_t bar = smem_u32(&bars[i % BULK_SLOTS]);
         if (elect_one()) {
-            mbar_expect_tx(bar, bytes);
+            const uint32_t size = min(bytes, row - piece * bytes);
+            mbar_expect_tx(bar, size);
             asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                          ::"r"(smem_u32(ring + static_cast<size_t>(i % BULK_SLOTS) * bytes)), "l"(static_cast<const unsigned char *>(a.x) + t * px + static_cast<size_t>(piece) * bytes),
-                           "r"(bytes), "r"(bar) : "memory");
+                           "r"(size), "r"(bar) : "memory");
         }
         __syncwarp();
     };
@@ -365,14 +375,15 @@ __global__ void __launch_bounds__(32) sort_bulk_kernel(const SortArgs a, int byt
         if (!__all_sync(FULL, mbar_wait(smem_u32(&bars[i % BULK_SLOTS]), (i / BULK_SLOTS) & 1, abort, a.err))) break;
         if (at >= 0)
             asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
-                         ::"l"(static_cast<unsigned char *>(a.rows) + at * pr + static_cast<size_t>(piece) * bytes), "r"(smem_u32(ring + static_cast<size_t>(i % BULK_SLOTS) * bytes)), "r"(bytes) : "memory");
+                         ::"l"(static_cast<unsigned char *>(a.rows) + at * pr + static_cast<size_t>(piece) * bytes), "r"(smem_u32(ring + static_cast<size_t>(i % BULK_SLOTS) * bytes)),
+                           "r"(min(bytes, row - piece * bytes)) : "memory");
         asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 1;" ::: "memory");
         __syncwarp();
         // the copies out of the slot before have read it: the next item may come there
         if (i > 0 && i - 1 + BULK_SLOTS < mine) load(i - 1 + BULK_SLOTS);
     }
     if (i < mine)  // given up: what was asked for lands before the ring is released
-        for (int j = i; j < mine && j < i - 1 + BULK_SLOTS; ++j) mbar_drain(smem_u32(&bars[j % BULK_SLOTS]), (j / BULK_SLOTS) & 1);
+        for (int j = i; j < mine && j < max(i - 1, 0) + BULK_SLOTS; ++j) mbar_drain(smem_u32(&bars[j % BULK_SLOTS]), (j / BULK_SLOTS) & 1);
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
@@ -400,12 +411,10 @@ cudaError_t sort_rows(const SortArgs &a, int item, cudaStream_t st) {
     if ((e = launch_early(sort_cluster_kernel, dim3(SORT_CTAS), SORT_T, smem, st, SORT_CTAS, a)) != cudaSuccess || !a.x) return e;
     const int row = a.hidden * item;
     if (sizeof(Item) == 16 && row >= BULK_MIN && static_cast<long>(n) * row <= BULK_ALL) {
-        int pieces = (row + BULK_PIECE - 1) / BULK_PIECE;
-        while (row % (16 * pieces)) ++pieces;  // equal pieces of whole 16 bytes (row / 16 of them at most)
-        const int bytes = row / pieces;
+        const int pieces = (row + BULK_PIECE - 1) / BULK_PIECE, bytes = ((row + pieces - 1) / pieces + 15) / 16 * 16;
         const long ring = static_cast<long>(BULK_SLOTS) * bytes, most = device_sm_count() * std::min(200 * 1024 / ring, 16L);
-        return launch_early(sort_bulk_kernel, dim3(static_cast<unsigned>(std::min(static_cast<long>(a.T) * pieces, most))), 32, ring, st, 1, a, bytes, pieces,
-                            a.ldx * item, a.ldr * item);
+        return launch_early(sort_bulk_kernel, dim3(static_cast<unsigned>(std::min(static_cast<long>(a.T) * pieces, most))), 32, ring, st, 1, a, row, bytes,
+                            pieces, a.ldx * item, a.ldr * item);
     }
     return launch_early(sort_copy_kernel<Item>, dim3(a.T, c.pieces), c.threads, 0, st, 1, a, items, px, pr);
 }
@@ -528,7 +537,7 @@ __global__ void __launch_bounds__(GT, 1) combine_grad_kernel(const CombineGradAr
                             float g[V];
 #pragma unroll
                             for (int i = 0; i < V; ++i) g[i] = f * d.at(i);
-                            store_row<Act, V>(static_cast<Act *>(a.dy) + at * a.ld_dy + c, g);
+                            store_row<Act, V, true>(static_cast<Act *>(a.dy) + at * a.ld_dy + c, g);
                         }
                     }
                 }

@@ -441,15 +441,15 @@ def test_product_scales_out_of_the_usual_range(counts):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("scale,k", [(1, 96), (12, 96), (12, 2100), (30, 2100)])
+@pytest.mark.parametrize("scale,n,k", [(1, 72, 96), (12, 72, 96), (12, 72, 2700), (30, 1000, 2700)])
 @pytest.mark.parametrize("bad", [[0, 5, 3, 28], [0, 5, 25, 1000], [-1, 5, 25, 28], [25, 5, 20, 28], [30, 31, 32, 33], [3, 3, 3, 2], [0, 37, 0, 37]])
-def test_product_bad_offsets(scale, k, bad):
+def test_product_bad_offsets(scale, n, k, bad):
     """A group is left out where its own bounds are not ascending within the rows; every other one is multiplied, also
     where groups overlap and make more tiles than their rows would."""
-    p = Product([5 * scale, 20 * scale, 3 * scale], 72, k, None, tail=9 * scale)
+    p = Product([5 * scale, 20 * scale, 3 * scale], n, k, None, tail=9 * scale)
     y = [p.a.astype(np.float64) @ w.astype(np.float64).T for w in p.w]
     off = [v * scale if v < 1000 else v * 1000 for v in bad]
-    out = torch.full((p.rows, 72), -7.25, device="cuda")
+    out = torch.full((p.rows, n), -7.25, device="cuda")
     W = p.call(out, torch.tensor(off, dtype=torch.int32, device="cuda"))
     good = [0 <= off[e] <= off[e + 1] <= p.rows for e in range(3)]
     assert q.coli_moe_error_word(W) == (0 if all(good) else q.DEVERR_GROUPING)

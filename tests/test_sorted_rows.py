@@ -159,7 +159,7 @@ def check_sort(T, K, E, ids, hidden, dtype, ldx=None, ldr=None, off=0, bad=False
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("T,K,E,hidden", [(1, 1, 1, 1), (1, 8, 256, 6144), (3, 2, 5, 7), (8, 4, 16, 256), (61, 6, 64, 1001), (256, 8, 64, 64),
                                           (257, 8, 64, 96), (700, 3, 1024, 40), (1, 32, 1024, 24), (2049, 1, 1, 16), (3001, 7, 200, 30), (9000, 8, 300, 8),
-                                          (641, 4, 8, 6144), (2600, 1, 3, 20008), (1300, 2, 16, 2048), (330, 8, 1000, 10240)])
+                                          (641, 4, 8, 6144), (2600, 1, 3, 20008), (2700, 1, 3, 8248), (1300, 2, 16, 2048), (330, 8, 1000, 10240)])
 def test_sort(T, K, E, hidden, dtype):
     rng = np.random.default_rng(T + E)
     check_sort(T, K, E, rng.integers(0, E, (T, K)), hidden, dtype)            # (a token may name an expert twice)
