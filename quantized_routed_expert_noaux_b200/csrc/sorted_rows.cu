@@ -7,8 +7,8 @@
 //   dy[place[t K + k]] = w[t][k] dout[t],  dw[t][k] = sum_h dout[t][h] y[place[t K + k]][h]
 //
 // All three move rows and compute next to nothing: HBM bounds them.  Every row is read once, by 16-byte pieces where
-// its address allows it; a token's K rows are in flight together.  No atomics on data: the same call gives the same
-// bits.
+// its address allows it, else element by element; a token's rows are in flight together.  No atomics on data: the same
+// call gives the same bits.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -53,17 +53,12 @@ struct Raw {
         else return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
     }
 };
-// (STREAM: rows that are written once and are more than L2 holds, where there are many: read data stays there longer.)
-template <typename T, int V, bool STREAM = false>
+template <typename T, int V>
 __device__ __forceinline__ void store_row(T *p, const float (&v)[V]) {
     if constexpr (sizeof(T) == 4) {
         if constexpr (V % 4 == 0) {
 #pragma unroll
-            for (int i = 0; i < V / 4; ++i) {
-                const float4 f = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                if (STREAM) __stcs(reinterpret_cast<float4 *>(p) + i, f);
-                else reinterpret_cast<float4 *>(p)[i] = f;
-            }
+            for (int i = 0; i < V / 4; ++i) reinterpret_cast<float4 *>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i) p[i] = v[i];
@@ -77,13 +72,12 @@ __device__ __forceinline__ void store_row(T *p, const float (&v)[V]) {
             const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
             w[i] = *reinterpret_cast<const uint32_t *>(&b);
         }
-        if constexpr (V == 8) {
-            const uint4 q = make_uint4(w[0], w[1], w[2], w[3]);
-            if (STREAM) __stcs(reinterpret_cast<uint4 *>(p), q);
-            else *reinterpret_cast<uint4 *>(p) = q;
-        } else *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+        if constexpr (V == 8) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        else *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
     }
 }
+
+constexpr int LOOSE = 8;  // elements of a thread, 32 apart, where rows go element by element and are many
 
 // Threads and pieces of a row of n items: at most `most` threads, rows cut evenly.
 struct Cut {
@@ -103,7 +97,27 @@ inline Cut cut(int n, int most) {
 constexpr int SMALL_N = 2560;
 constexpr int SMALL_T = 256;    // threads
 
-// Keys below `key` of n (padded to whole runs of 128), by a warp.
+// A warp's LOOSE * 32 items of a row, from i on (lane 0's; i: this lane's first).
+template <typename Item>
+struct LooseRow {
+    Item v[LOOSE];
+    __device__ __forceinline__ LooseRow(const Item *x, int i, int items) {
+        x += i;
+        const int left = items - i;
+#pragma unroll
+        for (int u = 0; u < LOOSE; ++u)
+            if (32 * u < left) v[u] = __ldg(x + 32 * u);
+    }
+    __device__ __forceinline__ void put(Item *row, int i, int items) const {
+        row += i;
+        const int left = items - i;
+#pragma unroll
+        for (int u = 0; u < LOOSE; ++u)
+            if (32 * u < left) row[32 * u] = v[u];
+    }
+};
+
+// Keys below `key` of n (padded to a multiple of 4), by a warp.
 __device__ __forceinline__ int count_below(const uint32_t *keys, int n, uint32_t key, int lane) {
     int before = 0;
     for (int i = lane; i < (n + 3) / 4; i += 32) {
@@ -126,7 +140,7 @@ __global__ void __launch_bounds__(SMALL_T) sort_small_kernel(const SortArgs a, i
     const int n = a.T * a.K, i0 = blockIdx.y * SMALL_T + threadIdx.x;
     const Item *x = static_cast<const Item *>(a.x) + t * px;
     Item v;
-    if (a.x && i0 < items) v = __ldg(x + i0);  // on its way while the slots are counted
+    if (sizeof(Item) == 16 && a.x && i0 < items) v = __ldg(x + i0);  // on its way while the slots are counted
     for (int s = threadIdx.x; s < (n + 3 & ~3); s += SMALL_T) {
         uint32_t key = 0xffffffffu;
         if (s < n) {
@@ -167,11 +181,21 @@ __global__ void __launch_bounds__(SMALL_T) sort_small_kernel(const SortArgs a, i
     }
     if (!a.x) return;
     __syncthreads();
-    for (int i = i0; i < items; i += gridDim.y * SMALL_T) {
-        if (i != i0) v = __ldg(x + i);
-        for (int k = 0; k < a.K; ++k) {
-            const int to = s_place[k];
-            if (to >= 0) static_cast<Item *>(a.rows)[to * pr + i] = v;
+    if constexpr (sizeof(Item) == 16) {
+        for (int i = i0; i < items; i += gridDim.y * SMALL_T) {
+            if (i != i0) v = __ldg(x + i);
+            for (int k = 0; k < a.K; ++k) {
+                const int to = s_place[k];
+                if (to >= 0) static_cast<Item *>(a.rows)[to * pr + i] = v;
+            }
+        }
+    } else {
+        for (int i = (blockIdx.y * WARPS + warp) * 32 * LOOSE + lane; i < items + lane; i += gridDim.y * SMALL_T * LOOSE) {
+            const LooseRow<Item> r(x, i, items);
+            for (int k = 0; k < a.K; ++k) {
+                const int to = s_place[k];
+                if (to >= 0) r.put(static_cast<Item *>(a.rows) + to * pr, i, items);
+            }
         }
     }
 }
@@ -317,15 +341,29 @@ __global__ void __launch_bounds__(SORT_T) sort_cluster_kernel(const SortArgs a) 
 // Row t of x to the places of its K slots, a piece of the row per CTA.  The piece is fetched before the sort has ended:
 // x is older than the sort, which began when the kernels before it had ended.
 template <typename Item>
-__global__ void __launch_bounds__(256) sort_copy_kernel(const SortArgs a, int items, size_t px, size_t pr) {
-    const int t = blockIdx.x, i = blockIdx.y * blockDim.x + threadIdx.x, lane = threadIdx.x & 31;
-    Item v;
-    if (i < items) v = __ldg(static_cast<const Item *>(a.x) + t * px + i);
-    wait_for_previous();
-    const int at = lane < a.K ? __ldcg(a.place + static_cast<size_t>(t) * a.K + lane) : -1;
-    for (int k = 0; k < a.K; ++k) {
-        const int to = __shfl_sync(FULL, at, k);
-        if (to >= 0 && i < items) static_cast<Item *>(a.rows)[to * pr + i] = v;
+__global__ void __launch_bounds__(SMALL_T) sort_copy_kernel(const SortArgs a, int items, size_t px, size_t pr) {
+    const int t = blockIdx.x, lane = threadIdx.x & 31;
+    const Item *x = static_cast<const Item *>(a.x) + t * px;
+    auto place = [&] { return lane < a.K ? __ldcg(a.place + static_cast<size_t>(t) * a.K + lane) : -1; };
+    if constexpr (sizeof(Item) == 16) {
+        const int i = blockIdx.y * blockDim.x + threadIdx.x;
+        Item v;
+        if (i < items) v = __ldg(x + i);
+        wait_for_previous();
+        const int at = place();
+        for (int k = 0; k < a.K; ++k) {
+            const int to = __shfl_sync(FULL, at, k);
+            if (to >= 0 && i < items) static_cast<Item *>(a.rows)[to * pr + i] = v;
+        }
+    } else {
+        const int i = (blockIdx.y * blockDim.x + threadIdx.x - lane) * LOOSE + lane;
+        const LooseRow<Item> r(x, i, items);
+        wait_for_previous();
+        const int at = place();
+        for (int k = 0; k < a.K; ++k) {
+            const int to = __shfl_sync(FULL, at, k);
+            if (to >= 0) r.put(static_cast<Item *>(a.rows) + to * pr, i, items);
+        }
     }
 }
 
@@ -391,10 +429,11 @@ template <typename Item>
 cudaError_t sort_rows(const SortArgs &a, int item, cudaStream_t st) {
     const int ratio = sizeof(Item) / item, items = a.x ? a.hidden / ratio : 1;
     const size_t px = a.ldx / ratio, pr = a.ldr / ratio;
-    const Cut c = cut(items, SMALL_T);
+    constexpr int U = sizeof(Item) == 16 ? 1 : LOOSE;
+    const Cut c = cut((items + U - 1) / U, SMALL_T);
     const int n = a.T * a.K;
     if (n <= SMALL_N) {
-        const int pieces = a.T < device_sm_count() ? (items + SMALL_T - 1) / SMALL_T : 1;
+        const int pieces = a.T < device_sm_count() ? (items + SMALL_T * U - 1) / (SMALL_T * U) : 1;
         return launch_early(sort_small_kernel<Item>, dim3(a.T, pieces), SMALL_T, 0, st, 1, a, items, px, pr);
     }
     const size_t smem = static_cast<size_t>(SORT_WARPS + SORT_CTAS) * (a.E + 1) * sizeof(int);
@@ -422,16 +461,18 @@ cudaError_t sort_rows(const SortArgs &a, int item, cudaStream_t st) {
 // ------------------------------------------------------------------ combine
 
 constexpr int CT = 256;         // threads at most
-constexpr int DEPTH = 8;        // rows of a token in flight
-constexpr int CTAS = 4;         // resident per SM
-constexpr int GT = CT * CTAS;   // threads of a token at most, where tokens are few (gradient)
+constexpr int SM_T = 1024;      // threads of an SM with 64 registers each
+// A thread takes V elements side by side, U times: rows with boundaries of 16 bytes once; others element by element, once where
+// threads are over, LOOSE times where elements are many, fewer rows of a token in flight then and half the threads.
+template <int U> constexpr int ROWS = U == 1 ? 8 : 4;
+template <int U> constexpr int CTAS = U == 1 ? 4 : 2;   // resident per SM
 
-// Rows place[k0 .. k0 + DEPTH) of a token and their weights, one per lane; -1 where there is none.
+// Rows place[k0 .. k0 + depth) of a token and their weights, one per lane; -1 where there is none.
 struct Slots {
     int at;
     float f;
-    __device__ __forceinline__ void load(const int32_t *place, const float *w, size_t t, int K, int k0, int lane) {
-        const bool mine = lane < DEPTH && k0 + lane < K;
+    __device__ __forceinline__ void load(const int32_t *place, const float *w, size_t t, int K, int k0, int depth, int lane) {
+        const bool mine = lane < depth && k0 + lane < K;
         at = mine ? __ldg(place + t * K + k0 + lane) : -1;
         f = mine && w ? __ldg(w + t * K + k0 + lane) : 1.f;
     }
@@ -443,18 +484,20 @@ struct Slots {
     }
 };
 
-// A CTA takes pieces of tokens' rows, one after another; the next one's places are on their way meanwhile.
-template <typename Act, typename Out, int V>
-__global__ void __launch_bounds__(CT, CTAS) combine_kernel(const CombineArgs a, int pieces) {
+// A CTA takes pieces of tokens' rows, one after another; the next one's places are on their way meanwhile.  Loads are
+// behind predicates, not branches: those kept them apart (2048 tokens, 8 rows of 2047 bf16 elements: 31 us against 40).
+template <typename Act, typename Out, int V, int U>
+__global__ void __launch_bounds__(CT, CTAS<U>) combine_kernel(const CombineArgs a, int pieces) {
+    constexpr int D = ROWS<U>, STEP = 32 * V;
     wait_for_previous();
     const int lane = threadIdx.x & 31;
     int t = blockIdx.x / pieces, piece = blockIdx.x - t * pieces;
     const int dt = gridDim.x / pieces, dp = gridDim.x - dt * pieces;
     Slots next;
-    if (t < a.T) next.load(a.place, a.w, t, a.K, 0, lane);
+    if (t < a.T) next.load(a.place, a.w, t, a.K, 0, D, lane);
     while (t < a.T) {
         Slots s = next;
-        const int c = (piece * blockDim.x + threadIdx.x) * V;
+        const int c = (piece * blockDim.x + threadIdx.x - lane) * V * U + lane * V;
         const size_t t0 = t;
         t += dt;
         piece += dp;
@@ -462,103 +505,131 @@ __global__ void __launch_bounds__(CT, CTAS) combine_kernel(const CombineArgs a, 
             piece -= pieces;
             ++t;
         }
-        if (t < a.T) next.load(a.place, a.w, t, a.K, 0, lane);
-        float acc[V];
-        if (a.add && c < a.hidden) {
-            Raw<Out, V> r;
-            r.load(static_cast<const Out *>(a.add) + t0 * a.ld_add + c);
+        if (t < a.T) next.load(a.place, a.w, t, a.K, 0, D, lane);
+        bool in[U];
+        float acc[U][V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = r.at(i);
-        } else {
+        for (int u = 0; u < U; ++u) {
+            in[u] = c + STEP * u < a.hidden;
+            if (a.add && in[u]) {
+                Raw<Out, V> r;
+                r.load(static_cast<const Out *>(a.add) + t0 * a.ld_add + c + STEP * u);
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = 0.f;
+                for (int i = 0; i < V; ++i) acc[u][i] = r.at(i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[u][i] = 0.f;
+            }
         }
-        for (int k0 = 0; k0 < a.K; k0 += DEPTH) {
-            if (k0) s.load(a.place, a.w, t0, a.K, k0, lane);
+        for (int k0 = 0; k0 < a.K; k0 += D) {
+            if (k0) s.load(a.place, a.w, t0, a.K, k0, D, lane);
             s.check(a.rows, a.err);
-            Raw<Act, V> v[DEPTH];
+            Raw<Act, V> v[D][U];
 #pragma unroll
-            for (int k = 0; k < DEPTH; ++k) {
+            for (int k = 0; k < D; ++k) {
                 const int at = __shfl_sync(FULL, s.at, k);
-                if (at >= 0 && c < a.hidden) v[k].load(static_cast<const Act *>(a.y) + at * a.ldy + c);
+                const Act *row = static_cast<const Act *>(a.y) + at * a.ldy + c;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (at >= 0 && in[u]) v[k][u].load(row + STEP * u);
             }
 #pragma unroll
-            for (int k = 0; k < DEPTH; ++k) {
+            for (int k = 0; k < D; ++k) {
                 const float f = __shfl_sync(FULL, s.f, k);
-                if (__shfl_sync(FULL, s.at, k) >= 0) {
+                const bool have = __shfl_sync(FULL, s.at, k) >= 0;
 #pragma unroll
-                    for (int i = 0; i < V; ++i) acc[i] = fmaf(f, v[k].at(i), acc[i]);
-                }
+                for (int u = 0; u < U; ++u)
+                    if (have && in[u]) {
+#pragma unroll
+                        for (int i = 0; i < V; ++i) acc[u][i] = fmaf(f, v[k][u].at(i), acc[u][i]);
+                    }
             }
         }
-        if (c < a.hidden) store_row<Out, V>(static_cast<Out *>(a.out) + t0 * a.ldo + c, acc);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (in[u]) store_row<Out, V>(static_cast<Out *>(a.out) + t0 * a.ldo + c + STEP * u, acc[u]);
     }
 }
 
 // ------------------------------------------------------------------ gradient
 
-// A CTA takes tokens one after another, DEPTH of their rows at a time; the products with dout are summed over the CTA.
-template <typename Act, typename Out, int V>
-__global__ void __launch_bounds__(GT, 1) combine_grad_kernel(const CombineGradArgs a) {
-    __shared__ float s_sum[2][GT / 32][DEPTH];
+// A CTA takes tokens one after another, some of their rows at a time; the products with dout are summed over the CTA.
+template <typename Act, typename Out, int V, int U>
+__global__ void __launch_bounds__(U == 1 ? SM_T : CT, U == 1 ? 1 : CTAS<U>) combine_grad_kernel(const CombineGradArgs a) {
+    constexpr int D = ROWS<U>, STEP = 32 * V;
+    __shared__ float s_sum[2][SM_T / 32][D];
     wait_for_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     int buf = 0;
     Slots next;
-    if (blockIdx.x < a.T) next.load(a.place, a.w, blockIdx.x, a.K, 0, lane);
+    if (blockIdx.x < a.T) next.load(a.place, a.w, blockIdx.x, a.K, 0, D, lane);
     for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
         Slots s = next;
-        if (t + static_cast<int>(gridDim.x) < a.T) next.load(a.place, a.w, t + gridDim.x, a.K, 0, lane);
-        for (int k0 = 0; k0 < a.K; k0 += DEPTH, buf ^= 1) {
-            if (k0) s.load(a.place, a.w, t, a.K, k0, lane);
+        if (t + static_cast<int>(gridDim.x) < a.T) next.load(a.place, a.w, t + gridDim.x, a.K, 0, D, lane);
+        for (int k0 = 0; k0 < a.K; k0 += D, buf ^= 1) {
+            if (k0) s.load(a.place, a.w, t, a.K, k0, D, lane);
             s.check(a.rows, a.err);
-            float dot[DEPTH];
+            float dot[D];
 #pragma unroll
-            for (int k = 0; k < DEPTH; ++k) dot[k] = 0.f;
-            for (int c0 = 0; c0 < a.hidden; c0 += blockDim.x * V) {
-                const int c = c0 + threadIdx.x * V;
-                const bool in = c < a.hidden;
-                Raw<Out, V> d;
-                Raw<Act, V> v[DEPTH];
-                if (in) d.load(static_cast<const Out *>(a.dout) + t * a.ld_dout + c);
+            for (int k = 0; k < D; ++k) dot[k] = 0.f;
+            for (int c0 = 0; c0 < a.hidden; c0 += blockDim.x * V * U) {
+                const int c = c0 + (threadIdx.x - lane) * V * U + lane * V;
+                bool in[U];
+                Raw<Out, V> d[U];
+                Raw<Act, V> v[D][U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    in[u] = c + STEP * u < a.hidden;
+                    if (in[u]) d[u].load(static_cast<const Out *>(a.dout) + t * a.ld_dout + c + STEP * u);
+                }
                 if (a.dw) {
 #pragma unroll
-                    for (int k = 0; k < DEPTH; ++k) {
+                    for (int k = 0; k < D; ++k) {
                         const int at = __shfl_sync(FULL, s.at, k);
-                        if (at >= 0 && in) v[k].load(static_cast<const Act *>(a.y) + at * a.ldy + c);
+                        const Act *row = static_cast<const Act *>(a.y) + at * a.ldy + c;
+#pragma unroll
+                        for (int u = 0; u < U; ++u)
+                            if (at >= 0 && in[u]) v[k][u].load(row + STEP * u);
                     }
                 }
                 if (a.dy) {
 #pragma unroll
-                    for (int k = 0; k < DEPTH; ++k) {
+                    for (int k = 0; k < D; ++k) {
                         const int at = __shfl_sync(FULL, s.at, k);
                         const float f = __shfl_sync(FULL, s.f, k);
-                        if (at >= 0 && in) {
-                            float g[V];
+                        Act *row = static_cast<Act *>(a.dy) + at * a.ld_dy + c;
 #pragma unroll
-                            for (int i = 0; i < V; ++i) g[i] = f * d.at(i);
-                            store_row<Act, V, true>(static_cast<Act *>(a.dy) + at * a.ld_dy + c, g);
-                        }
+                        for (int u = 0; u < U; ++u)
+                            if (at >= 0 && in[u]) {
+                                float g[V];
+#pragma unroll
+                                for (int i = 0; i < V; ++i) g[i] = f * d[u].at(i);
+                                store_row<Act, V>(row + STEP * u, g);
+                            }
                     }
                 }
                 if (a.dw) {
 #pragma unroll
-                    for (int k = 0; k < DEPTH; ++k)
-                        if (__shfl_sync(FULL, s.at, k) >= 0 && in) {
+                    for (int k = 0; k < D; ++k) {
+                        const bool have = __shfl_sync(FULL, s.at, k) >= 0;
 #pragma unroll
-                            for (int i = 0; i < V; ++i) dot[k] = fmaf(d.at(i), v[k].at(i), dot[k]);
-                        }
+                        for (int u = 0; u < U; ++u)
+                            if (have && in[u]) {
+#pragma unroll
+                                for (int i = 0; i < V; ++i) dot[k] = fmaf(d[u].at(i), v[k][u].at(i), dot[k]);
+                            }
+                    }
                 }
             }
             if (!a.dw) continue;
 #pragma unroll
-            for (int k = 0; k < DEPTH; ++k) {
+            for (int k = 0; k < D; ++k) {
 #pragma unroll
                 for (int o = 16; o; o >>= 1) dot[k] += __shfl_xor_sync(FULL, dot[k], o);
                 if (lane == 0) s_sum[buf][warp][k] = dot[k];
             }
             __syncthreads();  // (the buffer is written again two rounds on: its readers have met the next round's barrier)
-            if (threadIdx.x < DEPTH && k0 + threadIdx.x < a.K) {
+            if (threadIdx.x < D && k0 + threadIdx.x < a.K) {
                 float sum = 0.f;
                 for (int i = 0; i < warps; ++i) sum += s_sum[buf][i][threadIdx.x];
                 a.dw[static_cast<size_t>(t) * a.K + k0 + threadIdx.x] = sum;
@@ -567,11 +638,14 @@ __global__ void __launch_bounds__(GT, 1) combine_grad_kernel(const CombineGradAr
     }
 }
 
-// CTAs for n pieces of work: those that are resident at once.
-unsigned resident(long n) {
-    const long most = static_cast<long>(device_sm_count()) * CTAS;
+// CTAs of so many threads for n pieces of work: those that are resident at once, `all` threads to an SM.
+unsigned resident(long n, int threads, int all) {
+    const long most = static_cast<long>(device_sm_count()) * std::min(all / threads, 32);
     return static_cast<unsigned>(n < most ? n : most);
 }
+
+// Whether single elements would keep all threads busy more than once or twice.
+bool many(int T, int hidden) { return static_cast<long>(T) * hidden > 2L * device_sm_count() * SM_T; }
 
 // Whether rows of `item`-byte elements can be taken `v` elements at a time.
 bool whole(const void *p, size_t ld, size_t item, int v) {
@@ -581,21 +655,28 @@ bool whole(const void *p, size_t ld, size_t item, int v) {
 template <typename Act, typename Out>
 cudaError_t combine(const CombineArgs &a, cudaStream_t st) {
     constexpr int V = 16 / sizeof(Act);
-    if (a.hidden % V == 0 && whole(a.y, a.ldy, sizeof(Act), V) && whole(a.add, a.ld_add, sizeof(Out), V) && whole(a.out, a.ldo, sizeof(Out), V)) {
-        const Cut c = cut(a.hidden / V, CT);
-        return launch_early(combine_kernel<Act, Out, V>, dim3(resident(static_cast<long>(a.T) * c.pieces)), c.threads, 0, st, 1, a, c.pieces);
-    }
-    const Cut c = cut(a.hidden, CT);
-    return launch_early(combine_kernel<Act, Out, 1>, dim3(resident(static_cast<long>(a.T) * c.pieces)), c.threads, 0, st, 1, a, c.pieces);
+    auto run = [&](auto kernel, int n, int ctas) {
+        const Cut c = cut(n, CT);
+        return launch_early(kernel, dim3(resident(static_cast<long>(a.T) * c.pieces, c.threads, CT * ctas)), c.threads, 0, st, 1, a, c.pieces);
+    };
+    if (a.hidden % V == 0 && whole(a.y, a.ldy, sizeof(Act), V) && whole(a.add, a.ld_add, sizeof(Out), V) && whole(a.out, a.ldo, sizeof(Out), V))
+        return run(combine_kernel<Act, Out, V, 1>, a.hidden / V, CTAS<1>);
+    if (many(a.T, a.hidden)) return run(combine_kernel<Act, Out, 1, LOOSE>, (a.hidden + LOOSE - 1) / LOOSE, CTAS<LOOSE>);
+    return run(combine_kernel<Act, Out, 1, 1>, a.hidden, CTAS<1>);
 }
 
 template <typename Act, typename Out>
 cudaError_t combine_grad(const CombineGradArgs &a, cudaStream_t st) {
     constexpr int V = 16 / sizeof(Act);
-    const int most = a.T <= device_sm_count() ? GT : CT;
+    auto run = [&](auto kernel, int n, int most, int ctas) {
+        const int threads = cut(n, most).threads;
+        return launch_early(kernel, dim3(resident(a.T, threads, CT * ctas)), threads, 0, st, 1, a);
+    };
+    const int most = a.T <= device_sm_count() ? SM_T : CT;  // (few tokens: all threads of an SM to each)
     if (a.hidden % V == 0 && whole(a.y, a.ldy, sizeof(Act), V) && whole(a.dout, a.ld_dout, sizeof(Out), V) && whole(a.dy, a.ld_dy, sizeof(Act), V))
-        return launch_early(combine_grad_kernel<Act, Out, V>, dim3(resident(a.T)), cut(a.hidden / V, most).threads, 0, st, 1, a);
-    return launch_early(combine_grad_kernel<Act, Out, 1>, dim3(resident(a.T)), cut(a.hidden, most).threads, 0, st, 1, a);
+        return run(combine_grad_kernel<Act, Out, V, 1>, a.hidden / V, most, CTAS<1>);
+    if (many(a.T, a.hidden)) return run(combine_grad_kernel<Act, Out, 1, LOOSE>, (a.hidden + LOOSE - 1) / LOOSE, CT, CTAS<LOOSE>);
+    return run(combine_grad_kernel<Act, Out, 1, 1>, a.hidden, most, CTAS<1>);
 }
 
 }  // namespace
