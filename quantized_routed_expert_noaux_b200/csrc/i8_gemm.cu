@@ -4,11 +4,17 @@
 // The sums are whole numbers in 32 bits (exact); they become float32 and take the two scales in the epilogue.
 //
 // Swap-AB, tiles, groups and split k as in the product of 4-bit operands: weight rows of one matrix are the MMA's M side,
-// rows of the matrix's group its N side; a k-block is 128 bytes of every row, 128 elements here.  Three
-// tiles, chosen on the host:
-//   at most 32 rows in all      128 weight rows x 32, k split over a cluster where tiles are few
-//   few each (use_pairs)        128 weight rows x 128
-//   more                        256 weight rows x 256 on a pair of CTAs
+// rows of the matrix's group its N side; a k-block is 128 bytes of every row, 128 elements here.  Tiles, chosen on the host
+// (launch_out):
+//   128 weight rows x 32 or 128    k split over a cluster of CTAs where tiles are few
+//   128 weight rows x 128          few rows to a matrix, many matrices
+//   256 weight rows x 256          on a pair of CTAs, from 32 rows to a matrix; k split over two pairs where tiles are few
+//
+// Few rows to a matrix make it a stream of weights: 64 matrices of 4096 x 6144 with 4 / 16 / 32 / 64 / 128 rows each take 240 / 245 /
+// 253 / 261 / 285 us (6.7 to 6.1 TB/s; copy peak 6.5); of 6144 x 2048 127 / 131 / 137 / 143 / 159.  From 64 rows on the operands'
+// way from L2 counts (64 matrices 6144 x 2048, 4096 rows: 1.65 GB in 144 us, 40 bytes per cycle and SM), which is why
+// pairs, whose CTAs share a tile's rows, take over at 32.  Many rows are bound by the power cap: 8192 rows, 4096 x 6144 in
+// 125 us at 1594 MHz (3.3 POPS, tensor pipe active in 85% of the cycles), 145 us in long runs.
 //
 // One persistent CTA per SM, warp-specialised; tiles are taken round-robin:
 //   warp 0      TMA producer: weight codes and the rows' codes (128-byte swizzle)
@@ -691,6 +697,11 @@ cudaError_t launch_pair(const GemmMaps &maps, const GemmArgs &g, int C, cudaStre
     return launch_early(kernel, dim3(2 * C * static_cast<unsigned>(tiles < clusters ? tiles : clusters)), P_THREADS, P::SMEM, st, 2 * C, maps, g);
 }
 
+// Which tiles.  Split k costs 2 to 3 us and pays from SPLIT_KT k-blocks on: 40 / 64 / 128 rows, 4096 x 6144, in 9.6 / 10.2 / 12.8 us on
+// single CTAs against 15.0 / 15.2 / 16.4 on pairs unsplit; 256 / 512 rows, two pairs to a tile, 18 / 20 us against 21 / 22;
+// but 40 rows, 6144 x 2048, 8.9 against 8.2.  (Four pairs to a tile: clusters of 8 do not all fit at once, 30 us against 21.)
+// Pairs against single CTAs with 64 matrices of 6144 x 2048, 16 / 32 / 64 / 128 rows each: 137 / 140 / 148 / 163 us against 134 /
+// 139 / 154 / 243; 2048 x 1024, 8 / 32 rows: 26.7 / 28.1 against 26.0 / 31.0.
 constexpr int PAIR_ROWS = 32, SPLIT_KT = 20;
 
 template <int OUT>

@@ -285,7 +285,9 @@ __global__ void __launch_bounds__(WARP ? 32 * WARP_ROWS : MOST_T, WARP ? 6 : 2) 
 }
 
 // Many rows: a CTA takes them one after another out of a ring in shared memory that bulk copies fill, so that what is on its way
-// does not depend on registers.  Rows are whole 16-byte pieces that start at multiples of 16 bytes.
+// does not depend on registers.  Rows are whole 16-byte pieces that start at multiples of 16 bytes.  8192 rows of 6144
+// bf16 30 us (HBM would take 23; 37 by i8_quantize_kernel), 16,384 SwiGLU rows of 2048 36 us (26), 4096 of them 12.3 us:
+// instructions, issued in half of the cycles with the warps that 80 registers leave room for.
 constexpr int RING_ROWS = 1024, MOST_SLOTS = 8;
 template <typename In, bool GLU> constexpr int RING_HOLD = sizeof(In) == 2 && !GLU ? 4 : 2;
 constexpr size_t RING_SMEM = 208 * 1024;  // of all CTAs of an SM
