@@ -436,7 +436,7 @@ coli_status coli_moe_combine_grad(int act, const void *y, int rows, size_t ldy, 
  * Row i goes to the rows place[i * copies + c], c < copies, of the result (device int32; a place of -1 is left out, another
  * one outside [0, rows) too and sets COLI_DEVERR_GROUPING in the error word of `ws`; the places differ), as
  * coli_moe_sort_rows gives them with copies = top_k.  place NULL: row i to row i, copies == 1, rows == src_rows.
- * Rows of the result that nothing names are left as they are.  codes 16-byte aligned, ldc bytes from row to row, a
+ * Rows of the result that nothing names are left as they are.  codes overlap nothing, 16-byte aligned, ldc bytes from row to row, a
  * multiple of 16; bytes from k to the next multiple of 16 become 0.  src_rows = 0 is a no-op.  One kernel. */
 coli_status coli_moe_i8_quantize(int act, int swiglu, const void *x, int src_rows, size_t ldx, int k,
                                  const int32_t *place, int copies, int rows, int8_t *codes, size_t ldc,

@@ -2,9 +2,12 @@
 // ends.  Every thread of every CTA of a kernel that is launched so calls wait_for_previous() before its first access
 // to memory that an earlier kernel may touch; the wait ends when the kernels before have completed and their
 // writes are visible.  (A kernel that returned without waiting could complete before its predecessor, and let
-// its successor run too early.)  Only the products call dependents_may_launch(), at their end; elsewhere the end
-// of the kernel is the trigger.  Earlier triggers gave the next kernel's CTAs room beside the running ones and
-// were slower (2048 tokens routed 6.5 us against 5.0, the expert half for one token 70 against 59).
+// its successor run too early.)  The products call dependents_may_launch() at their end.  The 8-bit quantiser calls
+// it first (the product behind it is set up meanwhile), and so does the sort of many slots (the copies behind it
+// load their rows meanwhile): after wait_for_previous(), so that what is read before the successor's own wait
+// is complete.  Elsewhere the end of the kernel is the trigger; earlier ones gave the next kernel's CTAs room
+// beside the running ones and were slower (2048 tokens routed 6.5 us against 5.0, the fp4 expert half for one
+// token 70 against 59).
 #pragma once
 
 #include <atomic>

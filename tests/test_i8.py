@@ -160,7 +160,8 @@ def check_quantize(x, **kw):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("rows,k", [(1, 1), (1, 6144), (3, 15), (5, 16), (9, 17), (37, 1001), (130, 2048), (131, 2064), (3, 8192), (2, 20000), (5, 2047)])
+@pytest.mark.parametrize("rows,k", [(1, 1), (1, 6144), (3, 15), (5, 16), (9, 17), (37, 1001), (130, 2048), (131, 2064), (3, 8192), (2, 20000), (5, 2047),
+                                    (3, 12301), (2, 20001), (1100, 2304), (1030, 1040), (1500, 6144), (1024, 12288), (1200, 1001), (1025, 3001)])
 def test_quantize(rows, k, dtype):
     g = torch.Generator().manual_seed(rows + k)
     x = torch.randn(rows, k, generator=g) * torch.exp2(torch.randint(-40, 40, (rows, 1), generator=g).float())
@@ -232,8 +233,25 @@ def test_quantize_extremes(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("swiglu", [0, 1])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("T,copies,k", [(1, 8, 6144), (37, 3, 100), (300, 8, 2100), (5, 32, 16)])
+def test_quantize_rows_that_are_not_finite_among_many(dtype, swiglu):
+    k, rows = 2320, 1300
+    x = torch.randn(rows, k * (1 + swiglu), generator=torch.Generator().manual_seed(6)).to(DT[dtype])
+    bad = np.array([0, 7, 500, 1299])
+    for r, v in zip(bad, (float("nan"), float("inf"), float("-inf"), float("nan"))):
+        x[r, (r * 37) % k] = v
+    codes, scale, err = run_quantize(x.cuda(), k=k, swiglu=swiglu)
+    good = np.setdiff1d(np.arange(rows), bad)
+    assert err == 0 and np.isnan(scale[bad]).all() and not codes[bad].any() and np.isfinite(scale[good]).all()
+    if not swiglu:
+        wc, ws_ = plain_quantize(x[torch.from_numpy(good)].double().numpy())
+        assert np.array_equal(codes[good][:, :k], wc) and np.array_equal(scale[good], ws_)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,copies,k", [(1, 8, 6144), (37, 3, 100), (300, 8, 2100), (5, 32, 16), (1100, 2, 2304), (3, 40, 1500), (1030, 3, 1040)])
 def test_quantize_to_places(T, copies, k, dtype):
     rng = np.random.default_rng(T)
     rows = T * copies + 3
@@ -289,7 +307,7 @@ def check_swiglu(x, k):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("rows,k", [(1, 1), (1, 2048), (7, 100), (130, 1024), (3, 4999), (2, 10000)])
+@pytest.mark.parametrize("rows,k", [(1, 1), (1, 2048), (7, 100), (130, 1024), (3, 4999), (2, 10000), (2, 6001), (1030, 1040), (1100, 2048), (1024, 1001)])
 def test_quantize_swiglu(rows, k, dtype):
     g = torch.Generator().manual_seed(rows + k)
     check_swiglu((torch.randn(rows, 2 * k, generator=g) * 3).to(DT[dtype]).cuda(), k)

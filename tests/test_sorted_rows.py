@@ -260,7 +260,8 @@ class Batch:
         return got
 
 
-SHAPES = [(1, 1, 1), (1, 8, 6144), (7, 3, 8), (4, 32, 264), (61, 6, 1001), (300, 8, 512), (5, 9, 2056), (2, 10, 4100)]
+SHAPES = [(1, 1, 1), (1, 8, 6144), (7, 3, 8), (4, 32, 264), (61, 6, 1001), (300, 8, 512), (5, 9, 2056), (2, 10, 4100), (700, 5, 1001), (90, 9, 4100),
+          (2500, 2, 130), (6000, 1, 77)]
 
 
 @pytest.mark.gpu
@@ -282,9 +283,10 @@ def test_combine(T, K, hidden, act, out):
 @pytest.mark.parametrize("hidden,ldy,ldo,off", [(64, 72, 80, 0), (64, 65, 64, 0), (64, 64, 64, 1), (63, 64, 64, 0), (68, 68, 76, 4), (72, 72, 74, 2)])
 def test_combine_strides(act, hidden, ldy, ldo, off):
     for out in ("f32", "bf16"):
-        b = Batch(37, 5, hidden, act, out, ldy=ldy, ldo=ldo, off=off)
-        b.check()
-        check_grad(b)
+        for T in (37, 6000):
+            b = Batch(T, 5 if T == 37 else 2, hidden, act, out, ldy=ldy, ldo=ldo, off=off)
+            b.check()
+            check_grad(b)
 
 
 @pytest.mark.gpu
@@ -469,3 +471,42 @@ def test_training_step_in_a_graph():
     assert q.coli_moe_error_word(W) == 0
 
 
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hidden", [1024, 64, 33])
+@pytest.mark.parametrize("T", [400, 1200])
+def test_chain_of_layers(T, hidden):
+    """Every call reads what the one before it has just written, over and over, eagerly and in a graph: x -> rows -> their
+    weighted sum with x -> the next x; all terms of a sum have one sign, so that a layer is within its roundings of the value."""
+    K, E, L = 4, 24, 6
+    rng = np.random.default_rng(T + hidden)
+    i32 = lambda v: torch.from_numpy(np.ascontiguousarray(v)).int().cuda()  # noqa: E731
+    ids = [np.argsort(rng.random((T, E)), 1)[:, :K] for _ in range(L)]
+    w = [np.exp2(rng.integers(-2, 1, (T, K))).astype(np.float32) for _ in range(L)]
+    dev_ids, dev_w = [i32(v) for v in ids], [torch.from_numpy(v).cuda() for v in w]
+    xs = [torch.zeros(T, hidden, device="cuda") for _ in range(L + 1)]
+    rows = torch.zeros(T * K, hidden, device="cuda")
+    offsets, perm, place, W = i32(np.zeros(E + 1)), i32(np.zeros(T * K)), i32(np.zeros(T * K)), ws()
+
+    def run():
+        for i in range(L):
+            q.coli_moe_sort_rows(E, K, 0, xs[i], T, hidden, hidden, dev_ids[i], offsets, perm, place, rows, hidden, W)
+            q.coli_moe_combine(0, rows, T * K, hidden, place, dev_w[i], T, K, hidden, 0, xs[i], hidden, xs[i + 1], hidden, W)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        run()
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            run()
+        for call in (run, graph.replay, run, graph.replay):
+            x = torch.from_numpy(rng.integers(-3, 4, (T, hidden))).float()
+            xs[0].copy_(x)
+            call()
+            want = x.double().numpy()
+            for i in range(L):
+                want = want * (1 + w[i].astype(np.float64).sum(1, keepdims=True))
+            got = xs[L].double().cpu().numpy()
+            assert (np.abs(got - want) <= L * (K + 1) * 2.0 ** -24 * np.abs(want)).all()
+    assert q.coli_moe_error_word(W) == 0
