@@ -31,15 +31,17 @@ constexpr unsigned FULL = 0xffffffffu;
 
 // ------------------------------------------------------------------ elements
 
-// V elements of a row as they lie in memory.  (No read-only loads: an addend may be the result itself.)
+// V elements of a row as they lie in memory, at a multiple of their bytes or of 16.  (No read-only loads: an addend may be the result
+// itself.)  32 bytes go in two loads: one would want a multiple of 32, and is no faster (2048 tokens x 8 rows of 6144 with a float32
+// addend 48 us either way, the gradient 82; at odd multiples of 16 bytes 48 and 82 too).
 template <typename T, int V>
 struct Raw {
     static constexpr int BYTES = sizeof(T) * V, WORDS = BYTES < 4 ? 1 : BYTES / 4;
     uint32_t w[WORDS];
     __device__ __forceinline__ void load(const T *p) {
         if constexpr (BYTES == 32) {
-            asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "l"(p));
+            asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+            asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "l"(p + V / 2));
         } else if constexpr (BYTES == 16) {
             asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
         } else if constexpr (BYTES == 8) {
@@ -645,7 +647,7 @@ unsigned resident(long n, int threads, int all) {
 // Whether single elements would keep all threads busy more than once or twice.
 bool many(int T, int hidden) { return static_cast<long>(T) * hidden > 2L * device_sm_count() * SM_T; }
 
-// Whether rows of `item`-byte elements can be taken `v` elements at a time.
+// Whether rows of `item`-byte elements can be taken `v` elements at a time, in accesses of at most 16 bytes.
 bool whole(const void *p, size_t ld, size_t item, int v) {
     return !p || ((reinterpret_cast<uintptr_t>(p) | ld * item) & (item * v < 16 ? item * v - 1 : 15)) == 0;
 }
