@@ -464,9 +464,14 @@ __global__ void __launch_bounds__(P_THREADS, 1) i8_pair_kernel(const __grid_cons
     const uint32_t tbase = s_tmem;
     const int ntiles = s_tiles;
     // A cluster that splits k has one tile; should groups that overlap make more of them than the host counted, all its
-    // warps meet before the next one, whose copies need the ring.
+    // warps meet before the next one, whose copies need the ring.  A warp that gives up at tile t leaves its loop by way of
+    // give_up(): it meets the others as often as they will (the tiles are the same for the whole cluster), so that nobody waits
+    // for it at a barrier without a bound; their own waits for what it no longer does run out.
     auto next_tile = [&](int t) {
         if (SPLIT && t != first) cluster_sync_all();
+    };
+    auto give_up = [&](int t) {
+        for (t += stride; SPLIT && t < ntiles; t += stride) next_tile(t);
     };
 
     if (warp == W_PROD) {
@@ -478,7 +483,10 @@ __global__ void __launch_bounds__(P_THREADS, 1) i8_pair_kernel(const __grid_cons
             const int n32 = (x.nr + 31) / 32;                        // N / 32; this CTA's share is 16 * n32 rows
             const int row_lo = x.n0 + rank * 16 * n32;
             for (int kb = kb0; kb < kb0 + KT; ++kb) {
-                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[s]), phase, abort, p.err))) goto prod_done;
+                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[s]), phase, abort, p.err))) {
+                    give_up(t);
+                    goto prod_done;
+                }
                 const uint32_t fb = map_rank(smem_u32(&full[s]), leader);
                 if (elect_one()) {
                     remote_expect_tx(fb, A_BYTES + n32 * 16 * KB);
@@ -510,11 +518,17 @@ __global__ void __launch_bounds__(P_THREADS, 1) i8_pair_kernel(const __grid_cons
             const Tile x = tile_at<P_NT>(t, list, p, W);
             const int n32 = (x.nr + 31) / 32, acc = tl & 1;
             const uint32_t idesc = idesc_i8(256) | (static_cast<uint32_t>(4 * n32) << 17);
-            if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&dempty[acc]), ((tl >> 1) & 1) ^ 1, abort, p.err))) goto mma_done;
+            if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&dempty[acc]), ((tl >> 1) & 1) ^ 1, abort, p.err))) {
+                give_up(t);
+                goto mma_done;
+            }
             tc_fence_after();
             const uint32_t dt = tbase + acc * P_NT;
             for (int kb = 0; kb < KT; ++kb) {
-                if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&full[s]), phase, abort, p.err))) goto mma_done;
+                if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&full[s]), phase, abort, p.err))) {
+                    give_up(t);
+                    goto mma_done;
+                }
                 tc_fence_after();
                 const int steps = min(4, (p.k - (kb0 + kb) * KB + 31) / 32);
                 if (elect_one()) {
@@ -562,7 +576,10 @@ __global__ void __launch_bounds__(P_THREADS, 1) i8_pair_kernel(const __grid_cons
             const int acc = tl & 1, row0 = x.m * 256 + rank * 128;
             const int r = row0 + 32 * q + lane, runs = (x.nr + 31) / 32;
             const float rw = p.wscale && r < p.n ? __ldg(p.wscale + static_cast<size_t>(x.e) * p.wscale_stride + r) : 1.f;
-            if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&dfull[acc]), (tl >> 1) & 1, abort, p.err))) break;
+            if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&dfull[acc]), (tl >> 1) & 1, abort, p.err))) {
+                give_up(t);
+                break;
+            }
             tc_fence_after();
             const uint32_t dt = tbase + acc * P_NT + (static_cast<uint32_t>(32 * q) << 16);
             const int own = runs > part ? (runs - part + C - 1) / C : 0;  // this CTA's runs
@@ -574,7 +591,10 @@ __global__ void __launch_bounds__(P_THREADS, 1) i8_pair_kernel(const __grid_cons
                     if (lane < C && lane != part) remote_arrive(map_rank(smem_u32(pready), 2 * lane + rank));
                     __syncwarp();
                 }
-                if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(pready), tl & 1, abort, p.err))) break;
+                if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(pready), tl & 1, abort, p.err))) {
+                    give_up(t);
+                    break;
+                }
                 for (int g = half; g < runs; g += 2) {
                     const int to = g % C;
                     if (to == part) continue;
@@ -587,7 +607,10 @@ __global__ void __launch_bounds__(P_THREADS, 1) i8_pair_kernel(const __grid_cons
                         asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];"
                                      ::"r"(dst + ((i ^ (lane & 7)) << 4)), "r"(v[4 * i]), "r"(v[4 * i + 1]), "r"(v[4 * i + 2]), "r"(v[4 * i + 3]), "r"(bar) : "memory");
                 }
-                if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(pfull), tl & 1, abort, p.err))) break;
+                if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(pfull), tl & 1, abort, p.err))) {
+                    give_up(t);
+                    break;
+                }
             }
             for (int i = half; i < own; i += 2) {
                 const int g = 32 * (part + i * C);
