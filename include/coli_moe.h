@@ -432,7 +432,7 @@ coli_status coli_moe_combine_grad(int act, const void *y, int rows, size_t ldy, 
  * A row that holds a NaN or an infinity gets the scale NaN and codes 0.
  *   swiglu = 0: row i is x + i * ldx (act: coli_act), k values.
  *   swiglu = 1: row i holds k gate and then k up values; what is quantised is gate / (1 + exp(-gate)) * up in float32
- *               (a few units of its last place; a gate of -infinity gives NaN).
+ *               (within 2^-20 of the real value for every finite gate; a gate of -infinity gives NaN).
  * Row i goes to the rows place[i * copies + c], c < copies, of the result (device int32; a place of -1 is left out, another
  * one outside [0, rows) too and sets COLI_DEVERR_GROUPING in the error word of `ws`; the places differ), as
  * coli_moe_sort_rows gives them with copies = top_k.  place NULL: row i to row i, copies == 1, rows == src_rows.

@@ -329,6 +329,38 @@ def test_quantize_swiglu_extremes():
         assert np.isnan(scale[1]) and not codes[1, :8].any() and np.array_equal(codes[0, :8], want)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("k", [48, 70, 1040, 2400, 13000])
+def test_quantize_swiglu_far_gates(k, dtype):
+    """Gates where 1 + exp(-gate) leaves float32 or the range of its fast quotients while SiLU(gate) * up does not: rows of such gates
+    alone, whose products set the scale, and among others."""
+    rng = np.random.default_rng(k)
+    rows = []
+    for lo in (-79.0, -80.0, -86.5, -87.0, -87.5, -88.0, -88.5, -89.0, -95.0, -104.0, -120.0, -150.0, -172.0, -177.0, -181.0, -300.0, -3e38):
+        gate = lo + (rng.random(k) * 1.5 - 1.0 if lo > -1e3 else np.zeros(k))
+        for size in (1e30, 3e38):
+            rows.append(np.concatenate([gate, size * (0.05 + 0.95 * rng.random(k)) * rng.choice([-1, 1], k)]))
+    for size in (1.0, 1e30):
+        gate, up = rng.standard_normal(k) * 3, rng.standard_normal(k) * 3
+        gate[::7], up[::7] = -80 - 15 * rng.random(len(gate[::7])), size * rng.random(len(up[::7])) * 1e6
+        rows.append(np.concatenate([gate, up]))
+    x = torch.from_numpy(np.stack(rows)).to(DT[dtype])
+    check_swiglu(x.cuda(), k)
+    if k < 3000:                                      # and where rows are many
+        check_swiglu(x.repeat(40, 1).cuda(), k)
+    # at -87.5 and -88.5 by itself, as the largest of the row
+    y = torch.zeros(2, 2 * k)
+    y[:, :k] = -1.0
+    y[0, 5], y[0, k + 5] = -87.5, 1e30
+    y[1, 5], y[1, k + 5] = -88.5, 1e30
+    y = y.to(DT[dtype])
+    codes, scale, err = run_quantize(y.cuda(), k=k, swiglu=1)
+    g, u = y[:, 5].double().numpy(), y[:, k + 5].double().numpy()
+    m = np.abs(g / (1 + np.exp(-g)) * u)
+    assert err == 0 and (codes[:, 5] == -127).all() and (np.abs(scale - m / 127) <= 2.0 ** -19 * m / 127).all()
+
+
 # ------------------------------------------------------------------ product
 
 
