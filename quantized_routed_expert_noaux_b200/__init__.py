@@ -588,11 +588,26 @@ def coli_moe_i8_product(a: I8Rows, w: I8Mats, k, offsets, out_type, out, ldo, ws
         raise ColiError("coli_moe_i8_product", status)
 
 
+_int8 = _float32 = None  # torch's types, once a tensor has come
+
+
+def _fits(codes, dim: int, scale) -> bool:
+    """Codes of the type and number of dimensions that the 8-bit kernels take, and scales of theirs: refusing this here costs a
+    few comparisons, where the kernel would read a short or narrow array behind its end."""
+    global _int8, _float32
+    if _int8 is None:
+        import torch
+        _int8, _float32 = torch.int8, torch.float32
+    return codes.dim() == dim and codes.dtype is _int8 and (scale is None or scale.dtype is _float32)
+
+
 def i8_rows_for(codes, scale=None) -> I8Rows:
-    """I8Rows over device tensors: codes [rows, >= k] int8, the values of a row side by side, scale [rows] contiguous."""
-    at = codes.get_device()
-    r, ld = codes.shape[0], codes.stride(0)
-    if codes.dim() != 2 or codes.stride(1) != 1 or not (scale is None or scale.is_contiguous()):
+    """I8Rows over device tensors: codes [rows, >= k] int8, the values of a row side by side, scale [rows] float32, contiguous."""
+    if not _fits(codes, 2, scale):
+        raise ColiError("i8_rows_for", 2 if codes.dim() != 2 else 1)
+    at, r = codes.get_device(), codes.shape[0]
+    ld, unit = codes.stride()
+    if unit != 1 or not (scale is None or (scale.shape == (r,) and scale.is_contiguous())):
         raise ColiError("i8_rows_for", 2)
     if at < 0 or not (scale is None or scale.get_device() == at):
         raise ColiError("i8_rows_for", 1)
@@ -602,12 +617,14 @@ def i8_rows_for(codes, scale=None) -> I8Rows:
 
 
 def i8_mats_for(codes, scale=None) -> I8Mats:
-    """I8Mats over device tensors: codes [count, n, >= k] int8, the values of a row side by side, scale [count, n] with a
+    """I8Mats over device tensors: codes [count, n, >= k] int8, the values of a row side by side, scale [count, n] float32 with a
     matrix's scales side by side."""
+    if not _fits(codes, 3, scale):
+        raise ColiError("i8_mats_for", 2 if codes.dim() != 3 else 1)
     at = codes.get_device()
     count, n, _ = codes.shape
     c = codes.stride()
-    if c[2] != 1 or not (scale is None or scale.stride(1) == 1):
+    if c[2] != 1 or not (scale is None or (scale.shape == (count, n) and scale.stride(1) == 1)):
         raise ColiError("i8_mats_for", 2)
     if at < 0 or not (scale is None or scale.get_device() == at):
         raise ColiError("i8_mats_for", 1)

@@ -122,6 +122,26 @@ def test_helpers_refuse_tensors_that_do_not_fit():
     refused(1, q.i8_mats_for, i8(2, 8, 64), torch.zeros(2, 8))
 
 
+def test_helpers_refuse_other_types_and_shapes():
+    """Codes that are not int8, scales that are not float32 or not one to a row: the kernels would read others as these, and
+    short ones behind their end."""
+    i8, f32 = (lambda *s: torch.zeros(*s, dtype=torch.int8)), torch.zeros
+    for t in (torch.uint8, torch.int16, torch.float32, torch.bool, torch.float8_e4m3fn):
+        refused(1, q.i8_rows_for, torch.zeros(4, 64).to(t), f32(4))
+        refused(1, q.i8_mats_for, torch.zeros(2, 8, 64).to(t), f32(2, 8))
+    for t in (torch.bfloat16, torch.float64, torch.int32):
+        refused(1, q.i8_rows_for, i8(4, 64), f32(4).to(t))
+        refused(1, q.i8_mats_for, i8(2, 8, 64), f32(2, 8).to(t))
+    for s in ((3,), (5,), (1,), (0,), (4, 1), (1, 4), ()):
+        refused(2, q.i8_rows_for, i8(4, 64), f32(s))
+    for s in ((1, 8), (2, 1), (2, 7), (2, 9), (3, 8), (16,), (8,), (2, 8, 1), ()):
+        refused(2, q.i8_mats_for, i8(2, 8, 64), f32(s))
+    for s in ((64,), (1, 4, 64), ()):
+        refused(2, q.i8_rows_for, i8(s))
+    for s in ((8, 64), (64,), (1, 2, 8, 64)):
+        refused(2, q.i8_mats_for, i8(s))
+
+
 # ------------------------------------------------------------------ quantisation
 
 
