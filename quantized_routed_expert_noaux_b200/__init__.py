@@ -453,6 +453,18 @@ def coli_moe_fp4_pack_record(cfg: MoEConfig, act, wg, wu, wd, record, ws, stream
     _check("coli_moe_fp4_pack_record", lib.coli_moe_fp4_pack_record(C.byref(cfg), act, wg, wu, wd, record, ws, st))
 
 
+_int8 = _float32 = None  # torch's types, once a tensor has come
+
+
+def _types() -> None:
+    global _int8, _float32
+    import torch
+    _int8, _float32 = torch.int8, torch.float32
+
+
+# The helpers refuse arrays that the kernels would read behind their end, or as what they are not: a few comparisons.  Block scales: at least
+# 8 bytes of a row per 128 of its codes (MX; NV has twice as many).
+
 def fp4_rows_for(codes, scales, row_scale=None) -> FP4Rows:
     """FP4Rows over device tensors: codes [rows, k/2] uint8, scales [rows, pitch] uint8, row_scale [rows],
     all of them contiguous (the kernels take no strides for them)."""
@@ -462,9 +474,16 @@ def fp4_rows_for(codes, scales, row_scale=None) -> FP4Rows:
     else:
         row, dense = row_scale.data_ptr(), codes.is_contiguous() and scales.is_contiguous() and row_scale.is_contiguous()
         together = at == scales.get_device() == row_scale.get_device()
-    if not dense or not together or at < 0:
-        raise ColiError("fp4_rows_for", 1 if dense else 2)
-    a = FP4Rows(codes.data_ptr(), scales.data_ptr(), row, codes.shape[0])
+    if _float32 is None:
+        _types()
+    if codes.dim() != 2:
+        raise ColiError("fp4_rows_for", 2)
+    rows, half = codes.shape
+    if not dense or (row is not None and row_scale.shape != (rows,)) or scales.numel() < rows * 8 * ((half + 127) // 128):
+        raise ColiError("fp4_rows_for", 2)
+    if not together or at < 0 or not codes.element_size() == scales.element_size() == 1 or (row is not None and row_scale.dtype is not _float32):
+        raise ColiError("fp4_rows_for", 1)
+    a = FP4Rows(codes.data_ptr(), scales.data_ptr(), row, rows)
     a.device = at
     return a
 
@@ -473,6 +492,8 @@ def fp4_mats_for(codes, scales, row_scale=None) -> FP4Mats:
     """FP4Mats over device tensors: codes [count, n, k/2] uint8, scales [count, bytes] uint8 in tiles,
     row_scale [count, n].  Each matrix of a tensor is contiguous; the matrices may lie further apart."""
     at = codes.get_device()
+    if codes.dim() != 3 or (row_scale is not None and row_scale.dim() != 2):
+        raise ColiError("fp4_mats_for", 2)
     count, n, half = codes.shape
     c, s = codes.stride(), scales.stride()
     if row_scale is None:
@@ -482,7 +503,12 @@ def fp4_mats_for(codes, scales, row_scale=None) -> FP4Mats:
     if not (c[2] == 1 and c[1] == half and len(s) == 2 and s[1] == 1 and r[1] == 1):  # (dimensions of one element may have any stride)
         if not all(t is None or t.is_contiguous() or t[0].is_contiguous() for t in (codes, scales, row_scale)):
             raise ColiError("fp4_mats_for", 2)
-    if not together or at < 0:
+    if _float32 is None:
+        _types()
+    if ((row is not None and row_scale.shape != (count, n)) or scales.shape[0] != count or
+            scales.numel() < count * ((n + 127) // 128) * 1024 * ((half + 127) // 128)):
+        raise ColiError("fp4_mats_for", 2)
+    if not together or at < 0 or not codes.element_size() == scales.element_size() == 1 or (row is not None and row_scale.dtype is not _float32):
         raise ColiError("fp4_mats_for", 1)
     w = FP4Mats(codes.data_ptr(), scales.data_ptr(), row, count, n, c[0], s[0], r[0])
     w.device = at
@@ -588,16 +614,10 @@ def coli_moe_i8_product(a: I8Rows, w: I8Mats, k, offsets, out_type, out, ldo, ws
         raise ColiError("coli_moe_i8_product", status)
 
 
-_int8 = _float32 = None  # torch's types, once a tensor has come
-
-
 def _fits(codes, dim: int, scale) -> bool:
-    """Codes of the type and number of dimensions that the 8-bit kernels take, and scales of theirs: refusing this here costs a
-    few comparisons, where the kernel would read a short or narrow array behind its end."""
-    global _int8, _float32
+    """Codes of the type and number of dimensions that the 8-bit kernels take, and scales of theirs."""
     if _int8 is None:
-        import torch
-        _int8, _float32 = torch.int8, torch.float32
+        _types()
     return codes.dim() == dim and codes.dtype is _int8 and (scale is None or scale.dtype is _float32)
 
 

@@ -57,6 +57,41 @@ def test_helpers_refuse_tensors_that_are_not_dense():
     refused(1, q.fp4_mats_for, *mats)
 
 
+def test_helpers_refuse_scales_that_are_too_few():
+    """One row scale to a row, and block scales for all of them: the kernels would read behind the end of fewer."""
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
+    codes, scales, row = u8(4, 160), u8(4, 32), torch.zeros(4)             # k = 320: two runs of 256
+    for s in ((3,), (5,), (1,), (4, 1), (0,), ()):
+        refused(2, q.fp4_rows_for, codes, scales, torch.zeros(s))
+    refused(2, q.fp4_rows_for, u8(1, 4, 160), scales, row)
+    refused(2, q.fp4_mats_for, codes, u8(1, 128 * 32), row[None])
+    for s in ((3, 16), (4, 8), (63,), (0,)):
+        refused(2, q.fp4_rows_for, codes, u8(s), row)
+    mats = u8(3, 8, 160), u8(3, 128 * 32), torch.zeros(3, 8)
+    for s in ((1, 8), (3, 7), (2, 8), (3, 9), (4, 8), (3, 8, 1), (24,), ()):
+        refused(2, q.fp4_mats_for, *mats[:2], torch.zeros(s))
+    for s in ((1, 128 * 32), (2, 128 * 32), (3, 128 * 15), (3, 16)):
+        refused(2, q.fp4_mats_for, mats[0], u8(s), mats[2])
+
+
+@pytest.mark.gpu
+def test_helpers_refuse_other_types():
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8, device="cuda")  # noqa: E731
+    row, rows = torch.zeros(4, device="cuda"), torch.zeros(3, 8, device="cuda")
+    for t in (torch.int16, torch.float32):
+        refused(1, q.fp4_rows_for, u8(4, 64).to(t), u8(4, 16), row)
+        refused(1, q.fp4_rows_for, u8(4, 64), u8(4, 16).to(t), row)
+        refused(1, q.fp4_mats_for, u8(3, 8, 64).to(t), u8(3, 2048), rows)
+        refused(1, q.fp4_mats_for, u8(3, 8, 64), u8(3, 2048).to(t), rows)
+    for t in (torch.bfloat16, torch.float64, torch.int32):
+        refused(1, q.fp4_rows_for, u8(4, 64), u8(4, 16), row.to(t))
+        refused(1, q.fp4_mats_for, u8(3, 8, 64), u8(3, 2048), rows.to(t))
+    # what they take: no row scales, block scales in a flat array, other types of one byte
+    for a in (q.fp4_rows_for(u8(4, 64), u8(64)), q.fp4_rows_for(u8(4, 64).view(torch.int8), u8(4, 16).view(torch.float8_e4m3fn), row)):
+        assert a.rows == 4 and a.device == 0
+    assert q.fp4_mats_for(u8(3, 8, 64), u8(3, 2048)).count == 3
+
+
 @pytest.mark.gpu
 def test_helpers_take_matrices_further_apart():
     """The matrices of a stack may lie apart: records that hold their codes, scales and row scales one after another."""

@@ -142,6 +142,19 @@ def test_helpers_refuse_other_types_and_shapes():
         refused(2, q.i8_mats_for, i8(s))
 
 
+@pytest.mark.gpu
+def test_helpers_refuse_other_types_on_the_gpu():
+    """The same of types where tensors are on the GPU (a host tensor is refused with the same status)."""
+    i8, f32 = (lambda *s: torch.zeros(*s, dtype=torch.int8, device="cuda")), (lambda *s: torch.zeros(*s, device="cuda"))
+    for t in (torch.uint8, torch.int16, torch.float32, torch.bool, torch.float8_e4m3fn):
+        refused(1, q.i8_rows_for, f32(4, 64).to(t), f32(4))
+        refused(1, q.i8_mats_for, f32(2, 8, 64).to(t), f32(2, 8))
+    for t in (torch.bfloat16, torch.float64, torch.int32):
+        refused(1, q.i8_rows_for, i8(4, 64), f32(4).to(t))
+        refused(1, q.i8_mats_for, i8(2, 8, 64), f32(2, 8).to(t))
+    assert q.i8_rows_for(i8(4, 64), f32(4)).rows == 4 and q.i8_mats_for(i8(2, 8, 64), f32(2, 16)[:, :8]).scale_stride == 16
+
+
 # ------------------------------------------------------------------ quantisation
 
 
