@@ -437,7 +437,8 @@ coli_status coli_moe_combine_grad(int act, const void *y, int rows, size_t ldy, 
  * one outside [0, rows) too and sets COLI_DEVERR_GROUPING in the error word of `ws`; the places differ), as
  * coli_moe_sort_rows gives them with copies = top_k.  place NULL: row i to row i, copies == 1, rows == src_rows.
  * Rows of the result that nothing names are left as they are.  codes overlap nothing, 16-byte aligned, ldc bytes from row to row, a
- * multiple of 16; bytes from k to the next multiple of 16 become 0.  src_rows = 0 is a no-op.  One kernel. */
+ * multiple of 16; bytes from k to the next multiple of 16 become 0.  COLI_ERR_UNSUPPORTED where rows, src_rows or src_rows *
+ * copies is above 2^30, or k above 131071.  src_rows = 0 is a no-op.  One kernel. */
 coli_status coli_moe_i8_quantize(int act, int swiglu, const void *x, int src_rows, size_t ldx, int k,
                                  const int32_t *place, int copies, int rows, int8_t *codes, size_t ldc,
                                  float *scale, void *ws, void *stream);
@@ -445,16 +446,16 @@ coli_status coli_moe_i8_quantize(int act, int swiglu, const void *x, int src_row
 typedef struct {
     const int8_t *codes;   /* [rows], ld bytes apart, 16-byte aligned */
     const float *scale;    /* [rows], or NULL: 1 */
-    int rows;
-    size_t ld;             /* bytes; a multiple of 16 */
+    int rows;              /* <= 2^30 */
+    size_t ld;             /* bytes; a multiple of 16, < 2^30 */
 } coli_i8_rows;
 
 typedef struct {
     const int8_t *codes;   /* `count` matrices of n rows, ld bytes apart, 16-byte aligned */
     const float *scale;    /* `count` arrays [n], or NULL: 1 */
     int count, n;          /* count <= 1024 */
-    size_t ld;             /* bytes; a multiple of 16 */
-    size_t codes_stride;   /* bytes between matrices; a multiple of 16 */
+    size_t ld;             /* bytes; a multiple of 16, < 2^30; n * ld < 2^40 */
+    size_t codes_stride;   /* bytes between matrices; a multiple of 16, < 2^40 */
     size_t scale_stride;   /* elements */
 } coli_i8_mats;
 
@@ -462,8 +463,10 @@ typedef struct {
  * group; offsets, groups, rows outside every group, bad offsets, out_type, out and ldo as in coli_moe_fp4_product.
  * Sums are exact (32-bit integers; any codes, -128 too), rounded to float32 and multiplied with the product of the two
  * scales, itself rounded to float32; any finite scales will do, their product may leave float32's range where the
- * result does not.  The same call gives the same bits.  rows = 0 is a no-op.  One kernel; allocates nothing;
- * may be captured. */
+ * result does not.  The same call gives the same bits.  COLI_ERR_UNSUPPORTED for k above 131071, rows, counts and strides beyond
+ * the bounds above (codes_stride and scale_stride are not looked at where count == 1), and, as tiles are counted in 32 bits, where
+ * (rows / 16 + 1) * ceil(n / 128) * (count + 1) does not fit.  rows = 0 is a no-op.  One kernel; allocates nothing; may be
+ * captured. */
 coli_status coli_moe_i8_product(const coli_i8_rows *a, const coli_i8_mats *w, int k,
                                 const int32_t *offsets, int out_type, void *out, size_t ldo, void *ws,
                                 void *stream);

@@ -95,6 +95,36 @@ def test_refusals():
     product(7, W=64)
 
 
+def test_documented_bounds_are_refused():
+    """Each bound that the header gives, one beyond it; all of them end before a launch."""
+    big = 1 << 30
+
+    def quant(**kw):
+        a = dict(act=0, swiglu=0, x=256, src_rows=4, ldx=64, k=48, place=256, copies=2, rows=8, codes=256, ldc=48, scale=256, ws=256)
+        refused(4, q.coli_moe_i8_quantize, *{**a, **kw}.values(), stream=0)
+    quant(rows=big + 1)
+    quant(src_rows=big + 1, copies=1)
+    quant(src_rows=big + 1, copies=1, rows=big + 1, place=None)
+    quant(src_rows=big // 2 + 1)
+    quant(src_rows=1, copies=big + 1)
+    quant(k=131072, ldx=131072, ldc=131072)
+
+    def product(k=64, ldo=8, offsets=256, **kw):
+        a = dict(acodes=256, ascale=256, rows=4, ald=64, wcodes=256, wscale=256, count=2, n=8, wld=64, codes_stride=512, scale_stride=8)
+        v = list({**a, **kw}.values())
+        refused(4, q.coli_moe_i8_product, q.I8Rows(*v[:4]), q.I8Mats(*v[4:]), k, offsets, 0, 256, ldo, 256, stream=0)
+    product(k=131072, ald=131072, wld=131072, codes_stride=1 << 21)
+    product(rows=big + 1)
+    product(ald=big)
+    product(wld=big, codes_stride=1 << 34)
+    product(codes_stride=1 << 40)
+    product(n=1 << 20, wld=1 << 20, codes_stride=(1 << 40) - 16, ldo=1 << 20, scale_stride=1 << 20)   # n * ld = 2^40
+    product(n=1 << 20, wld=1 << 20, count=1, offsets=None, ldo=1 << 20)
+    product(count=1025)
+    # (rows / 16 + 1) * ceil(n / 128) * (count + 1) = 2^31: 2^20 * 2^10 * 2
+    product(rows=((1 << 20) - 1) * 16, n=1 << 17, count=1, offsets=None, ldo=1 << 17)
+
+
 @pytest.mark.parametrize("explicit", [False, True])
 def test_any_tensor_off_the_gpu_is_refused(explicit):
     if torch.cuda.is_available():
