@@ -215,6 +215,14 @@ def _pointers(fn: str, stream, *tensors):
     return *map(_p, tensors), st
 
 
+def _product_pointers(fn: str, stream, a, w, *tensors):
+    """_pointers for a product, whose operands are structures that may know their device: theirs and the tensors' is one."""
+    devices = {getattr(m, "device", None) for m in (a, w)} - {None}
+    devices |= {t.get_device() for t in tensors if t is not None and t.__class__ is not int}
+    st = _stream_at(fn, stream, min(devices), len(devices) == 1) if devices else _stream(stream)
+    return *map(_p, tensors), st
+
+
 def _check(fn: str, status: int) -> None:
     if status != 0:
         raise ColiError(fn, status)
@@ -438,10 +446,7 @@ def coli_moe_fp4_product(fmt, a: FP4Rows, w: FP4Mats, k, offsets, out_type, out,
               else _stream_at("coli_moe_fp4_product", stream, at, together))
         status = _c_fp4_product(fmt, a, w, k, None if offsets is None else offsets.data_ptr(), out_type, out.data_ptr(), ldo, ws.data_ptr(), st)
     except AttributeError:
-        operands = {getattr(m, "device", None) for m in (a, w)} - {None}
-        if len(operands) > 1:
-            raise ColiError("coli_moe_fp4_product", 1) from None
-        offsets, out, ws, st = _pointers("coli_moe_fp4_product", stream, offsets, out, ws)
+        offsets, out, ws, st = _product_pointers("coli_moe_fp4_product", stream, a, w, offsets, out, ws)
         status = _c_fp4_product(fmt, a, w, k, offsets, out_type, out, ldo, ws, st)
     if status:
         raise ColiError("coli_moe_fp4_product", status)
@@ -604,11 +609,7 @@ def coli_moe_i8_product(a: I8Rows, w: I8Mats, k, offsets, out_type, out, ldo, ws
         st = _quick("coli_moe_i8_product", stream, at, together)
         status = _c_i8_product(a, w, k, None if offsets is None else offsets.data_ptr(), out_type, out.data_ptr(), ldo, ws.data_ptr(), st)
     except AttributeError:
-        operands = {getattr(m, "device", None) for m in (a, w)} - {None}
-        operands |= {t.get_device() for t in (out, ws, offsets) if hasattr(t, "get_device")}
-        if len(operands) > 1:
-            raise ColiError("coli_moe_i8_product", 1) from None
-        offsets, out, ws, st = _pointers("coli_moe_i8_product", stream, offsets, out, ws)
+        offsets, out, ws, st = _product_pointers("coli_moe_i8_product", stream, a, w, offsets, out, ws)
         status = _c_i8_product(a, w, k, offsets, out_type, out, ldo, ws, st)
     if status:
         raise ColiError("coli_moe_i8_product", status)

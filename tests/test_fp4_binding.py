@@ -114,3 +114,25 @@ def test_operands_of_another_device_are_refused():
     a, w = q.FP4Rows(256, 256, 256, 1), q.FP4Mats(256, 256, 256, 1, 8, 0, 0, 0)
     a.device, w.device = 0, 1
     refused(1, q.coli_moe_fp4_product, 0, a, w, 32, None, 0, 256, 8, 256, stream=0)
+
+
+def test_operands_of_another_device_beside_raw_pointers_are_refused(monkeypatch):
+    """Result, workspace and offsets as integers, or the result alone as a tensor: the operands' device has to be the current one
+    (0 here) all the same.  k = 0 ends the calls that get past the binding, before a launch."""
+    monkeypatch.setattr(q, "_torch_device", lambda: 0)
+    monkeypatch.setattr(q, "_torch_stream", lambda at: 0)
+
+    class Out:                                                  # a tensor on device 1
+        def get_device(self):
+            return 1
+
+        def data_ptr(self):
+            return 256
+    ops = [(q.coli_moe_fp4_product, (0,), q.FP4Rows(256, 256, 256, 1), q.FP4Mats(256, 256, 256, 1, 8, 0, 0, 0)),
+           (q.coli_moe_i8_product, (), q.I8Rows(256, 256, 1, 64), q.I8Mats(256, 256, 1, 8, 64, 512, 8))]
+    for fn, fmt, a, w in ops:
+        for stream in (None, 0):
+            for devices, out, status in (((None, None), 256, 2), ((0, 0), 256, 2), ((0, None), 256, 2), ((1, 1), 256, 1), ((None, 1), 256, 1),
+                                         ((1, None), 256, 1), ((0, 1), 256, 1), ((0, 0), Out(), 1), ((1, 1), Out(), 1), ((None, 0), Out(), 1)):
+                a.device, w.device = devices
+                refused(status, fn, *fmt, a, w, 0, None, 0, out, 8, 256, stream=stream)
