@@ -4,7 +4,7 @@
 // scale = m / 127, m = the row's largest |x| (at least 127 * 2^-126); code = the whole number nearest to x / (m / 127) of
 // the real numbers, ties to even.  With v within 2^-22 of 127 / m, the real quotient lies between x v (1 - 2^-21)
 // and x v (1 + 2^-21), and so does its nearest whole number between theirs (an FMA that adds 1.5 * 2^23 rounds each
-// once, to a whole number).  Where those two differ, once in 10^5 elements, the quotient is next to a half i + 1/2, and
+// once, to a whole number).  Where those two differ, once in 10^5 float32 elements, the quotient is next to a half i + 1/2, and
 // 127 |x| is compared with (i + 1/2) m: with p = fl((i + 1/2) m) and e = (i + 1/2) m - p (an FMA gives it exactly), 127 |x| - p is
 // a float32 too, since the two are within 2^-13 of each other and 127 |x| has 31 bits; it is compared with e.  (Both
 // sides over 128, and times 2^64 where m is below 1, so that nothing overflows or underflows.)
@@ -320,9 +320,14 @@ __global__ void __launch_bounds__(WARP ? 32 * WARP_ROWS : MOST_T, WARP ? 6 : 2) 
 }
 
 // Many rows: a CTA takes them one after another out of a ring in shared memory that bulk copies fill, so that what is on its way
-// does not depend on registers.  Rows are whole 16-byte pieces that start at multiples of 16 bytes.  8192 rows of 6144
-// bf16 30 us (HBM would take 23; 37 by i8_quantize_kernel), 16,384 SwiGLU rows of 2048 36 us (26), 4096 of them 12.3 us:
-// instructions, issued in half of the cycles with the warps that 80 registers leave room for.
+// does not depend on registers.  Rows are whole 16-byte pieces that start at multiples of 16 bytes.  With i8_quantize_kernel's time
+// behind the stroke: 1024 / 4096 / 8192 rows of 6144 bf16 values 6.1 / 13.8 / 28 us against 5.0 / 13.5 / 32 (HBM would take 23 for 8192); 1024 /
+// 4096 / 16,384 SwiGLU rows of 2048 5.3 / 10.9 / 36 against 5.2 / 10.2 / 40 (26); 1024 / 8192 float32 rows of 2304 4.3 / 16.1 against 3.4 /
+// 15.3, of 6144 8192 44 against 38.  So it is ahead from about 64 MB of bf16 rows on, behind below that by up to 1 us, and behind for
+// float32.  Instructions bound it, issued in half of the cycles with the warps that 80 registers leave room for.
+// (Ties take the exact comparison.  bf16 has few values: x = m / 2 is one, 63.5, and a maximum of 127 / 32 makes hundreds; of normal values 20
+// elements in a row of 6144 need it, in 44% of the warps: 8192 such rows 48 us.  The times above are of rows with a few louder channels: 1
+// element, 2%.)
 constexpr int RING_ROWS = 1024, MOST_SLOTS = 8;
 template <typename In, bool GLU> constexpr int RING_HOLD = sizeof(In) == 2 && !GLU ? 4 : 2;
 constexpr size_t RING_SMEM = 208 * 1024;  // of all CTAs of an SM

@@ -375,8 +375,8 @@ __global__ void __launch_bounds__(SMALL_T) sort_copy_kernel(const SortArgs a, in
 
 // The same by bulk copies through shared memory, a warp per CTA: pieces of rows come into a ring of BULK_SLOTS, lane k sends
 // one on to the place of its token's slot k.  For long rows, where what is written is no more than BULK_ALL: 2048 tokens, 8 slots
-// each, 2048 / 6144 / 8192 bf16 columns 17.7 / 40.5 / 53 us against 19.4 / 44 / 58 by sort_copy_kernel, 1024 columns the same;
-// 16,384 tokens of 4096 234 against 219.
+// each, 2048 / 6144 / 8192 bf16 columns 17.7 / 40.5 / 53 us against 19.4 / 44 / 58 by sort_copy_kernel, 1024 columns the same; 8192 columns with
+// 287 / 325 MiB written 61 / 70 against 64 / 72, 4096 tokens of 6144 (384 MiB) 85 against 83, 16,384 tokens of 4096 (1 GiB) 236 against 220.
 constexpr int BULK_SLOTS = 4, BULK_PIECE = 16384, BULK_MIN = 4096;
 constexpr long BULK_ALL = 288L << 20;
 
@@ -644,7 +644,10 @@ unsigned resident(long n, int threads, int all) {
     return static_cast<unsigned>(n < most ? n : most);
 }
 
-// Whether single elements would keep all threads busy more than once or twice.
+// Whether single elements would keep all threads busy more than twice (149 rows of 2047 elements are many).  Eight elements to a thread
+// against one, bf16 rows of 2047 elements, 8 to a token: 32 / 100 / 144 / 200 / 400 tokens combined in 3.2 / 3.2 / 3.4 / 3.8 / 5.4 us against 2.3 /
+// 3.5 / 4.7 / 5.9 / 9.4, their gradient 4.9 / 4.9 / 4.9 / 6.2 / 9.4 against 6.1 / 6.2 / 6.3 / 9.7 / 13.2; rows of 33 elements, 148 / 9600 tokens, 3.0 /
+// 10.5 against 2.2 / 8.0 and 3.7 / 16.1 against 2.6 / 14.1.
 bool many(int T, int hidden) { return static_cast<long>(T) * hidden > 2L * device_sm_count() * SM_T; }
 
 // Whether rows of `item`-byte elements can be taken `v` elements at a time, in accesses of at most 16 bytes.
